@@ -466,6 +466,133 @@ int moe_chain_forward(const moe_layer_desc* layers, int32_t L, float eps,
                       void* workspace_dev, size_t workspace_bytes,
                       hipStream_t stream);
 
+/* ------------------------------------- rows in expert order, and back
+ * For expert products of the caller's own (other activations, adapters,
+ * training): the token rows themselves in expert order, the way back with the
+ * routing weights, and the gradients of both.  Rows are row-major [.][d] of one
+ * element type (MOE_TYPE_*), any d >= 1 up to 2^20; k <= 1024, E <= 1024,
+ * T * k <= 2^30 (MOE_ERR_UNSUPPORTED beyond).  Sums in fp32, in rank order,
+ * each output rounded once to the element type; no atomics on outputs, so
+ * results are reproducible bit for bit.  Outputs must not overlap inputs. */
+enum {
+  MOE_TYPE_F32 = 0,
+  MOE_TYPE_BF16 = 1,
+  MOE_TYPE_F16 = 2
+};
+
+/* Sort: the pairs i = t*k + r stably by expert, as moe_bucket_tokens, and the
+ * rows: x_sorted_dev [T*k][d], row p = x[pair_ids[p] / k] for p < offsets[E].
+ * offsets_dev [E+1], pair_ids_dev [T*k]; row_of_dev [T*k]: the row of each
+ * pair, -1 where topk_idx is outside [0, E) (padding, dropped pairs).  Rows of
+ * x_sorted and entries of pair_ids from offsets[E] on keep what they held.
+ * The workspace (moe_sort_workspace_bytes, 0 for invalid sizes) needs no fill. */
+size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t E);
+int moe_sort_tokens(const void* x_dev, int32_t type, int32_t T, int32_t d,
+                    const int32_t* topk_idx_dev, int32_t k, int32_t E,
+                    void* x_sorted_dev, int32_t* offsets_dev,
+                    int32_t* pair_ids_dev, int32_t* row_of_dev,
+                    void* workspace_dev, size_t workspace_bytes,
+                    hipStream_t stream);
+/* Its gradient: dx[t] = sum_{r<k} dx_sorted[row_of[t,r]] over the pairs that
+ * have a row (a token without any gets zeros). */
+int moe_sort_tokens_backward(const void* dx_sorted_dev, int32_t type,
+                             int32_t T, int32_t k, int32_t d,
+                             const int32_t* row_of_dev, void* dx_dev,
+                             hipStream_t stream);
+/* Back: y[t] = sum_{r<k} w[t,r] rows[row_of[t,r]] + s_t shared[t], in that
+ * order; a pair without a row adds nothing, whatever its weight.  shared_dev
+ * [T][d] and shared_gate_dev [T] may both be NULL. */
+int moe_unsort_combine(const void* rows_dev, int32_t type, int32_t T,
+                       int32_t k, int32_t d, const int32_t* row_of_dev,
+                       const float* topk_w_dev, const void* shared_dev,
+                       const float* shared_gate_dev, void* y_dev,
+                       hipStream_t stream);
+/* Its gradients from dy_dev [T][d]: drows[row_of[t,r]] = w[t,r] dy[t] (rows no
+ * pair has keep what they held), dtopk_w[t,r] = <dy[t], rows[row_of[t,r]]> (0
+ * without a row), dshared[t] = s_t dy[t], dshared_gate[t] = <dy[t], shared[t]>;
+ * the last two are NULL exactly when shared_dev is. */
+int moe_unsort_combine_backward(const void* dy_dev, const void* rows_dev,
+                                int32_t type, int32_t T, int32_t k, int32_t d,
+                                const int32_t* row_of_dev,
+                                const float* topk_w_dev, const void* shared_dev,
+                                const float* shared_gate_dev, void* drows_dev,
+                                float* dtopk_w_dev, void* dshared_dev,
+                                float* dshared_gate_dev, hipStream_t stream);
+
+/* --------------------------------------------------- 4-bit products
+ * y = W x for 4-bit affine group-quantised matrices outside the SwiGLU block
+ * (dense projections of the resident core, single matrices of the experts):
+ * W[o][j] = scale q + bias per group of 32, 64 or 128 inputs.  A packed matrix
+ * is its codes [n_in/32][n_out][16 B] followed by its (scale, bias) fp16 pairs
+ * [n_in/group][n_out], the layout of one matrix of an expert blob.  n_in a
+ * multiple of group, up to 65536; n_out 1 to 2^24; packed matrices 4-byte and
+ * x 16-byte aligned.  x bf16, y fp32: every product exact, sums in fp32 in a
+ * fixed order that depends on the sizes alone.  A row of x that is not finite
+ * gives a row of y that is not. */
+typedef struct moe_linear_shape {
+  int32_t n_in, n_out;
+  int32_t group;
+} moe_linear_shape;
+
+size_t moe_linear_bytes(const moe_linear_shape* sh);   /* 0 if sh is invalid */
+/* Host: codes [n_out][n_in] (0..15, else MOE_ERR_INVALID_ARG), scales and
+ * biases [n_out][n_in/group] fp16 bit patterns; packed: moe_linear_bytes. */
+int moe_pack_linear_int4(const moe_linear_shape* sh, const uint8_t* codes,
+                         const uint16_t* scales, const uint16_t* biases,
+                         void* packed);
+int moe_unpack_linear_int4(const moe_linear_shape* sh, const void* packed,
+                           uint8_t* codes, uint16_t* scales, uint16_t* biases);
+/* y_dev [T][n_out] = x_dev [T][n_in] W^T. */
+int moe_linear_int4(const moe_linear_shape* sh, const void* packed_dev,
+                    const uint16_t* x_dev, int32_t T, float* y_dev,
+                    hipStream_t stream);
+/* One matrix per expert, applied to rows in expert order (moe_sort_tokens):
+ * y_sorted[p] = W_e x_sorted[p] for offsets[e] <= p < offsets[e+1].  Expert e's
+ * matrix is at packed_dev + slot * stride_bytes (a multiple of 4), slot =
+ * slot_table[e], or e without a table (then n_slots >= E).  N: rows of
+ * x_sorted and y_sorted; rows of y_sorted from offsets[E] on keep what they
+ * held.  An expert with rows whose slot is outside [0, n_slots) gives zeros
+ * and sets bit 0 of error_dev (NULL: not reported). */
+int moe_expert_linear_int4(const moe_linear_shape* sh, const void* packed_dev,
+                           size_t stride_bytes, int32_t n_slots,
+                           const int32_t* slot_table_dev, int32_t E,
+                           const uint16_t* x_sorted_dev, int32_t N,
+                           const int32_t* offsets_dev, float* y_sorted_dev,
+                           int32_t* error_dev, hipStream_t stream);
+/* The same with a matrix (0 gate, 1 up, 2 down) of the blobs in a pool, through
+ * its slot table and error word; 4-bit pools (others MOE_ERR_UNSUPPORTED). */
+int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
+                         const uint16_t* x_sorted_dev, int32_t N,
+                         const int32_t* offsets_dev, float* y_sorted_dev,
+                         hipStream_t stream);
+
+/* ------------------------------------------------- gradient of the router
+ * From the gradients of moe_router_topk's weights (dtopk_w_dev [T][k]) and
+ * shared gate (dshared_gate_dev [T], or NULL: none): with g[t,r] = w (dw -
+ * sum_j w_j dw_j) and g_s = s (1 - s) ds,
+ *   dx[t] = sum_r g[t,r] W[idx[t,r]] + g_s W[E]              fp32 [T][d]
+ *   dW[e] = sum over pairs of e of g x[t], dW[E] = sum_t g_s x[t]   [E+1][d]
+ *   dbias[e] = sum over pairs of e of g                             [E]
+ * all written whole; each output may be NULL (not all three).  topk_idx,
+ * topk_w and shared_gate as moe_router_topk gave them (a pair whose index is
+ * outside [0, E) has no logit); offsets_dev and pair_ids_dev of
+ * moe_bucket_tokens or moe_sort_tokens on the same topk_idx, needed for dW
+ * and dbias.  Sizes as moe_router_topk.  The workspace needs no fill. */
+size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t E,
+                                           int32_t k);
+int moe_router_topk_backward(const uint16_t* x_dev, int32_t T, int32_t d,
+                             const float* w_router_dev, int32_t E, int32_t k,
+                             const int32_t* topk_idx_dev,
+                             const float* topk_w_dev,
+                             const float* shared_gate_dev,
+                             const float* dtopk_w_dev,
+                             const float* dshared_gate_dev,
+                             const int32_t* offsets_dev,
+                             const int32_t* pair_ids_dev, float* dx_dev,
+                             float* dw_router_dev, float* dlogit_bias_dev,
+                             void* workspace_dev, size_t workspace_bytes,
+                             hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,8 +25,9 @@ Modules:
   layer   — router, expert FFN, whole layer
   bucket  — token -> expert bucketing (counting sort)
   lfu     — LFU + recency slot-pool simulation
+  rows    — rows in expert order and back, router gradient, single 4-bit matrices
 
 Parity status of every function is pinned by ``tests/test_oracle_pins.py``;
 none is "parity unpinned".
 """
-from . import quant, layer, bucket, lfu  # noqa: F401
+from . import quant, layer, bucket, lfu, rows  # noqa: F401

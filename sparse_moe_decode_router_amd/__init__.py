@@ -29,6 +29,10 @@ MOE_ERR_POOL_TOO_SMALL = -4
 MOE_ERR_HIP = -5
 MOE_ERR_OUT_OF_MEMORY = -6
 
+MOE_TYPE_F32 = 0
+MOE_TYPE_BF16 = 1
+MOE_TYPE_F16 = 2
+
 MOE_PATH_AUTO = 0
 MOE_PATH_DECODE = 1
 MOE_PATH_BATCHED = 2
@@ -54,6 +58,10 @@ _lib = C.CDLL(LIB_PATH)
 
 class moe_ffn_shape(C.Structure):
     _fields_ = [("d", C.c_int32), ("I", C.c_int32), ("group", C.c_int32), ("bits", C.c_int32)]
+
+
+class moe_linear_shape(C.Structure):
+    _fields_ = [("n_in", C.c_int32), ("n_out", C.c_int32), ("group", C.c_int32)]
 
 
 class moe_pool_stats(C.Structure):
@@ -126,6 +134,20 @@ _SIGS = {
     "moe_probe_mfma_f16_flops": (C.c_double, [_I, _I]),
     "moe_chain_workspace_bytes": (_S, [_P, _I, _I, _I]),
     "moe_chain_forward": (C.c_int, [_P, _I, C.c_float, _P, _I, _P, _P, _P, _P, _I, _P, _S, _P]),
+    "moe_sort_workspace_bytes": (_S, [_I, _I, _I]),
+    "moe_sort_tokens": (C.c_int, [_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _S, _P]),
+    "moe_sort_tokens_backward": (C.c_int, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_unsort_combine": (C.c_int, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "moe_unsort_combine_backward": (C.c_int, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_linear_bytes": (_S, [_P]),
+    "moe_pack_linear_int4": (C.c_int, [_P, _P, _P, _P, _P]),
+    "moe_unpack_linear_int4": (C.c_int, [_P, _P, _P, _P, _P]),
+    "moe_linear_int4": (C.c_int, [_P, _P, _P, _I, _P, _P]),
+    "moe_expert_linear_int4": (C.c_int, [_P, _P, _S, _I, _P, _I, _P, _I, _P, _P, _P, _P]),
+    "moe_pool_linear_int4": (C.c_int, [_P, _I, _P, _I, _P, _P, _P]),
+    "moe_router_backward_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "moe_router_topk_backward": (C.c_int, [_P, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S,
+                                           _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -644,6 +666,290 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
                                 _ptr(ti), path, _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "moe_chain_forward")
     return (x_out, tx, tu, ti) if trace else x_out
+
+
+# ------------------------------------------- rows in expert order, and back
+# These entry points check their tensors (ValueError), run on the tensors'
+# device whatever the current one, and allocate what they return on the
+# stream that they launch on.
+_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
+
+
+class _on:
+    """The device of tensor x and the stream (its current one if None) as current; enters as the stream's handle."""
+
+    def __init__(self, x, stream):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError("device tensors wanted")
+        self.device, self.stream, self.back = x.get_device(), stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device.index != self.device:
+                raise ValueError("the stream is of another device than the tensors")
+            self.back = torch.cuda.stream(self.stream)
+            self.back.__enter__()
+            return self.stream.cuda_stream
+        if torch.cuda.current_device() != self.device:
+            self.back = torch.cuda.device(self.device)
+            self.back.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *e):
+        if self.back is not None:
+            self.back.__exit__(*e)
+
+
+def _need(t, name, dtype, shape, device):
+    """t.data_ptr() of a contiguous device tensor of that type and shape (None passes as None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda:{device} wanted, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
+    return t.data_ptr()
+
+
+def _row_type(x, name, dims=2):
+    if x.dim() != dims or x.dtype not in _TYPES:
+        raise ValueError(f"{name}: a {dims}-d tensor of float32, bfloat16 or float16 wanted, got {x.dtype} "
+                         f"{tuple(x.shape)}")
+    return _TYPES[x.dtype]
+
+
+def _given(t, name):
+    if t is None:
+        raise ValueError(f"{name} is wanted")
+    return t
+
+
+def _scratch(workspace, nbytes, device):
+    """A workspace that needs no fill: the caller's (uint8) or a new one."""
+    if workspace is None:
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=f"cuda:{device}")
+    if workspace.get_device() != device or not workspace.is_contiguous() or workspace.dtype is not torch.uint8:
+        raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{device} wanted")
+    return workspace
+
+
+def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
+    return int(_lib.moe_sort_workspace_bytes(T, k, E))
+
+
+def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
+    """Token rows x [T, d] (float32, bfloat16 or float16) in expert order.
+    Returns (x_sorted [T*k, d], offsets int32 [E+1], pair_ids int32 [T*k],
+    row_of int32 [T, k]); rows of x_sorted and entries of pair_ids from
+    offsets[E] on keep what they held (out: that tuple, to write into)."""
+    ty = _row_type(x, "x")
+    T, d = x.shape
+    k = _given(topk_idx, "topk_idx").shape[-1]
+    n = T * k
+    with _on(x, stream) as s:
+        dev = x.get_device()
+        if out is None:
+            out = (torch.empty((n, d), dtype=x.dtype, device=x.device),
+                   torch.empty((E + 1,), dtype=torch.int32, device=x.device),
+                   torch.empty((n,), dtype=torch.int32, device=x.device),
+                   torch.empty((T, k), dtype=torch.int32, device=x.device))
+        rows, offsets, pairs, row_of = out
+        if workspace is None:
+            workspace = _scratch(None, moe_sort_workspace_bytes(T, k, E), dev)
+        else:
+            _scratch(workspace, 0, dev)
+        _check(_lib.moe_sort_tokens(
+            _need(x, "x", x.dtype, (T, d), dev), ty, T, d, _need(topk_idx, "topk_idx", torch.int32, (T, k), dev), k, E,
+            _need(rows, "x_sorted", x.dtype, (n, d), dev), _need(offsets, "offsets", torch.int32, (E + 1,), dev),
+            _need(pairs, "pair_ids", torch.int32, (n,), dev), _need(row_of, "row_of", torch.int32, (T, k), dev),
+            workspace.data_ptr(), workspace.numel(), s), "moe_sort_tokens")
+    return rows, offsets, pairs, row_of
+
+
+def moe_sort_tokens_backward(dx_sorted, row_of, out=None, stream=None):
+    """Gradient of moe_sort_tokens with respect to x: dx [T, d] from dx_sorted [T*k, d]."""
+    ty = _row_type(dx_sorted, "dx_sorted")
+    T, k = _given(row_of, "row_of").shape
+    d = dx_sorted.shape[1]
+    with _on(dx_sorted, stream) as s:
+        dev = dx_sorted.get_device()
+        dx = torch.empty((T, d), dtype=dx_sorted.dtype, device=dx_sorted.device) if out is None else out
+        _check(_lib.moe_sort_tokens_backward(
+            _need(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * k, d), dev), ty, T, k, d,
+            _need(row_of, "row_of", torch.int32, (T, k), dev), _need(dx, "out", dx_sorted.dtype, (T, d), dev), s),
+            "moe_sort_tokens_backward")
+    return dx
+
+
+def moe_unsort_combine(rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
+    """y [T, d] = sum over a token's pairs of topk_w * rows[row_of], plus
+    shared_gate * shared_out; rows [T*k, d], y and shared_out [T, d] of one type."""
+    ty = _row_type(rows, "rows")
+    T, k = _given(row_of, "row_of").shape
+    d, t = rows.shape[1], rows.dtype
+    with _on(rows, stream) as s:
+        dev = rows.get_device()
+        y = torch.empty((T, d), dtype=t, device=rows.device) if out is None else out
+        _check(_lib.moe_unsort_combine(
+            _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d, _need(row_of, "row_of", torch.int32, (T, k), dev),
+            _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
+            _need(shared_out, "shared_out", t, (T, d), dev),
+            _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(y, "out", t, (T, d), dev), s),
+            "moe_unsort_combine")
+    return y
+
+
+def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
+    """Gradients of moe_unsort_combine from dy [T, d]: (drows [T*k, d], dtopk_w
+    fp32 [T, k], dshared_out [T, d], dshared_gate fp32 [T]), the last two None
+    without shared rows; rows of drows that no pair has keep what they held."""
+    ty = _row_type(rows, "rows")
+    T, k = _given(row_of, "row_of").shape
+    d, t = rows.shape[1], rows.dtype
+    with _on(rows, stream) as s:
+        dev = rows.get_device()
+        if out is None:
+            has = shared_out is not None
+            out = (torch.empty((T * k, d), dtype=t, device=rows.device),
+                   torch.empty((T, k), dtype=torch.float32, device=rows.device),
+                   torch.empty((T, d), dtype=t, device=rows.device) if has else None,
+                   torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
+        drows, dw, dsh, dsg = out
+        _check(_lib.moe_unsort_combine_backward(
+            _need(_given(dy, "dy"), "dy", t, (T, d), dev), _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d,
+            _need(row_of, "row_of", torch.int32, (T, k), dev),
+            _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
+            _need(shared_out, "shared_out", t, (T, d), dev),
+            _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(drows, "drows", t, (T * k, d), dev),
+            _need(dw, "dtopk_w", torch.float32, (T, k), dev), _need(dsh, "dshared_out", t, (T, d), dev),
+            _need(dsg, "dshared_gate", torch.float32, (T,), dev), s), "moe_unsort_combine_backward")
+    return drows, dw, dsh, dsg
+
+
+# ----------------------------------------------------------- 4-bit products
+def moe_linear_bytes(n_in: int, n_out: int, group: int = 64) -> int:
+    return int(_lib.moe_linear_bytes(C.byref(moe_linear_shape(n_in, n_out, group))))
+
+
+def moe_pack_linear_int4(codes, scales, biases) -> np.ndarray:
+    """Packed uint8 bytes of a 4-bit matrix: codes [n_out][n_in] (0..15), scales
+    and biases fp16 [n_out][n_in / group]; the group is n_in / scales.shape[1]."""
+    c = np.ascontiguousarray(codes, dtype=np.uint8)
+    s = np.ascontiguousarray(np.asarray(scales, np.float16)).view(np.uint16)
+    b = np.ascontiguousarray(np.asarray(biases, np.float16)).view(np.uint16)
+    if c.ndim != 2 or s.ndim != 2 or s.shape != b.shape or s.shape[0] != c.shape[0] or s.shape[1] < 1 \
+            or c.shape[1] % s.shape[1]:
+        raise ValueError(f"codes {c.shape}, scales {s.shape} and biases {b.shape} do not belong together")
+    sh = moe_linear_shape(c.shape[1], c.shape[0], c.shape[1] // s.shape[1])
+    out = np.empty(int(_lib.moe_linear_bytes(C.byref(sh))), dtype=np.uint8)
+    _check(_lib.moe_pack_linear_int4(C.byref(sh), c.ctypes.data, s.ctypes.data, b.ctypes.data, out.ctypes.data),
+           "moe_pack_linear_int4")
+    return out
+
+
+def moe_unpack_linear_int4(packed: np.ndarray, n_in: int, n_out: int, group: int = 64):
+    """(codes, scales, biases) of moe_pack_linear_int4."""
+    sh = moe_linear_shape(n_in, n_out, group)
+    p = np.ascontiguousarray(packed, dtype=np.uint8)
+    if p.size != int(_lib.moe_linear_bytes(C.byref(sh))) or p.size == 0:
+        raise ValueError(f"{p.size} bytes are no packed {n_out} x {n_in} matrix with groups of {group}")
+    codes = np.empty((n_out, n_in), np.uint8)
+    s, b = np.empty((n_out, n_in // group), np.float16), np.empty((n_out, n_in // group), np.float16)
+    _check(_lib.moe_unpack_linear_int4(C.byref(sh), p.ctypes.data, codes.ctypes.data, s.ctypes.data, b.ctypes.data),
+           "moe_unpack_linear_int4")
+    return codes, s, b
+
+
+def moe_linear_int4(packed, x, n_out: int, group: int = 64, out=None, stream=None):
+    """y fp32 [T, n_out] = x W^T; x bf16 [T, n_in], packed uint8 [moe_linear_bytes]."""
+    T, n_in = x.shape
+    sh = moe_linear_shape(n_in, n_out, group)
+    with _on(x, stream) as s:
+        dev = x.get_device()
+        y = torch.empty((T, n_out), dtype=torch.float32, device=x.device) if out is None else out
+        _check(_lib.moe_linear_int4(
+            C.byref(sh), _need(packed, "packed", torch.uint8, (int(_lib.moe_linear_bytes(C.byref(sh))),), dev),
+            _need(x, "x", torch.bfloat16, (T, n_in), dev), T, _need(y, "out", torch.float32, (T, n_out), dev), s),
+            "moe_linear_int4")
+    return y
+
+
+def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, group: int = 64, error=None, out=None,
+                           stream=None):
+    """y_sorted fp32 [N, n_out]: each row of x_sorted bf16 [N, n_in] (in expert
+    order, offsets int32 [E+1]) times its expert's matrix.  packed uint8
+    [n_slots, bytes] (rows may be apart: a view into larger blobs), slot_table
+    int32 [E] or None (expert e in slot e); error: int32 [1] or None.  Rows
+    from offsets[E] on keep what they held."""
+    N, n_in = x_sorted.shape
+    sh = moe_linear_shape(n_in, n_out, group)
+    if packed.dim() != 2 or packed.dtype is not torch.uint8 or packed.stride(1) != 1 \
+            or packed.shape[1] < int(_lib.moe_linear_bytes(C.byref(sh))):
+        raise ValueError(f"packed: a uint8 tensor [n_slots, {moe_linear_bytes(n_in, n_out, group)}] wanted, got "
+                         f"{packed.dtype} {tuple(packed.shape)}")
+    with _on(x_sorted, stream) as s:
+        dev = x_sorted.get_device()
+        if packed.get_device() != dev:
+            raise ValueError(f"packed: a tensor on cuda:{dev} wanted")
+        E = offsets.shape[0] - 1
+        y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
+        _check(_lib.moe_expert_linear_int4(
+            C.byref(sh), packed.data_ptr(), packed.stride(0), packed.shape[0],
+            _need(slot_table, "slot_table", torch.int32, (E,), dev), E,
+            _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
+            _need(offsets, "offsets", torch.int32, (E + 1,), dev), _need(y, "out", torch.float32, (N, n_out), dev),
+            _need(error, "error", torch.int32, (1,), dev), s), "moe_expert_linear_int4")
+    return y
+
+
+def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, stream=None):
+    """moe_expert_linear_int4 with the "gate", "up" or "down" matrices of a 4-bit pool's experts."""
+    if matrix not in _MATS:
+        raise ValueError(f"matrix must be one of {_MATS}")
+    n_in, n_out = (pool.I, pool.d) if matrix == "down" else (pool.d, pool.I)
+    N = x_sorted.shape[0]
+    with _on(x_sorted, stream) as s:
+        dev = x_sorted.get_device()
+        y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
+        _check(_lib.moe_pool_linear_int4(
+            pool.handle, _MATS.index(matrix), _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
+            _need(_given(offsets, "offsets"), "offsets", torch.int32, (pool.E + 1,), dev),
+            _need(y, "out", torch.float32, (N, n_out), dev), s), "moe_pool_linear_int4")
+    return y
+
+
+# ------------------------------------------------------ gradient of the router
+def moe_router_backward_workspace_bytes(T: int, d: int, E: int, k: int) -> int:
+    return int(_lib.moe_router_backward_workspace_bytes(T, d, E, k))
+
+
+def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids,
+                             workspace=None, out=None, stream=None):
+    """Gradients of moe_router_topk's weights and shared gate: (dx fp32 [T, d],
+    dw_router fp32 [E+1, d], dlogit_bias fp32 [E]).  offsets and pair_ids from
+    moe_bucket_tokens or moe_sort_tokens on topk_idx; dshared_gate None: no
+    gradient.  out: that triple to write into, None for each not wanted."""
+    T, d = x.shape
+    E, k = w_router.shape[0] - 1, topk_idx.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    with _on(x, stream) as s:
+        dev = x.get_device()
+        if out is None:
+            out = (torch.empty((T, d), dtype=f32, device=x.device), torch.empty((E + 1, d), dtype=f32, device=x.device),
+                   torch.empty((E,), dtype=f32, device=x.device))
+        dx, dwr, db = out
+        if workspace is None:
+            workspace = _scratch(None, moe_router_backward_workspace_bytes(T, d, E, k), dev)
+        else:
+            _scratch(workspace, 0, dev)
+        _check(_lib.moe_router_topk_backward(
+            _need(x, "x", torch.bfloat16, (T, d), dev), T, d, _need(w_router, "w_router", f32, (E + 1, d), dev), E, k,
+            _need(topk_idx, "topk_idx", i32, (T, k), dev), _need(topk_w, "topk_w", f32, (T, k), dev),
+            _need(shared_gate, "shared_gate", f32, (T,), dev), _need(dtopk_w, "dtopk_w", f32, (T, k), dev),
+            _need(dshared_gate, "dshared_gate", f32, (T,), dev), _need(offsets, "offsets", i32, (E + 1,), dev),
+            _need(pair_ids, "pair_ids", i32, (T * k,), dev), _need(dx, "dx", f32, (T, d), dev),
+            _need(dwr, "dw_router", f32, (E + 1, d), dev), _need(db, "dlogit_bias", f32, (E,), dev),
+            workspace.data_ptr(), workspace.numel(), s), "moe_router_topk_backward")
+    return dx, dwr, db
 
 
 # --------------------------------------------------------- measurement probes

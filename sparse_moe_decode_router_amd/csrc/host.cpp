@@ -397,6 +397,11 @@ bool pool_view(const moe_pool* p, PoolView* v) {
   v->E = p->E;
   return true;
 }
+bool pool_shape(const moe_pool* p, moe_ffn_shape* sh) {
+  if (!p) return false;
+  *sh = p->sh;
+  return true;
+}
 }  // namespace moe
 
 extern "C" int moe_pool_create(int32_t E, int32_t n_slots, const moe_ffn_shape* sh, moe_pool** out) {

@@ -63,6 +63,7 @@ struct PoolView {
   int32_t E;
 };
 bool pool_view(const moe_pool* p, PoolView* v);
+bool pool_shape(const moe_pool* p, moe_ffn_shape* sh);
 
 // ------------------------------------------------------------ workspace
 // Carves a caller workspace into 256-byte aligned pieces.

@@ -1,0 +1,332 @@
+// Token rows in expert order and back, with the gradients of both.
+//
+//   sort      X[row(i)] = x[t], i = t*k + r, row(i) = the pair's place in the
+//             stable counting sort by expert (bucket.hip), -1 without one
+//     grad    dx[t] = sum_r dX[row(t,r)]
+//   unsort    y[t] = sum_r w[t,r] Y[row(t,r)] + s_t o[t]
+//     grad    dY[row(t,r)] = w[t,r] dy[t],  dw[t,r] = <dy[t], Y[row(t,r)]>,
+//             do[t] = s_t dy[t],  ds_t = <dy[t], o[t]>
+//
+// The batched and prefill passes of the Swiftlet layer ("How it works": k of E
+// experts a token) group tokens by expert inside the library; these entry
+// points give the rows themselves, for expert products of the caller's own.
+// All sums run in fp32 in rank order (or a fixed tree over the columns), with
+// no atomics, so results are bit-reproducible; each output is rounded once.
+#include "internal.h"
+#include "device.h"
+#include "elem.h"
+
+namespace moe {
+namespace {
+
+// Rows are cut into pieces of VN elements, one lane each.  The last piece of
+// a row that VN does not divide starts VN before the row's end and repeats
+// the elements it shares with the one before it (same values, same place).
+template <int VN> __device__ __forceinline__ int piece_start(int c, int d) {
+  const int e = c * VN;
+  return e + VN <= d ? e : d - VN;
+}
+
+constexpr int kWaves = 4;                       // waves a block
+constexpr unsigned kMaxBlocks = 1u << 22;       // blocks go round past this
+
+inline unsigned wave_grid(long waves) {
+  const long b = (waves + kWaves - 1) / kWaves;
+  return (unsigned)(b < (long)kMaxBlocks ? b : (long)kMaxBlocks);
+}
+
+__device__ __forceinline__ long wave_id() {
+  return (long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+__device__ __forceinline__ long wave_count() { return (long)gridDim.x * kWaves; }
+
+// One wave per sorted row p: copy the token's row there and note the row at
+// its pair; the wave also marks pair p if that pair has no expert.
+template <int TYPE, int VN>
+__global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
+    const typename El<TYPE>::raw* __restrict__ x, const int32_t* __restrict__ idx, long n, int k, int d, int E,
+    const int32_t* __restrict__ offsets, const int32_t* __restrict__ pair_ids, int32_t* __restrict__ row_of,
+    typename El<TYPE>::raw* __restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int pieces = (d + VN - 1) / VN;
+  const int live = offsets[E];
+  for (long p = wave_id(); p < n; p += wave_count()) {
+    const int key = idx[p];
+    if ((key < 0 || key >= E) && lane == 0) row_of[p] = -1;
+    if (p >= live) continue;
+    const int i = pair_ids[p];
+    if (lane == 0) row_of[i] = (int32_t)p;
+    const typename El<TYPE>::raw* src = x + (size_t)(i / k) * d;
+    typename El<TYPE>::raw* dst = out + (size_t)p * d;
+    for (int c = lane; c < pieces; c += 64) {
+      const int e = piece_start<VN>(c, d);
+      vec_store<TYPE, VN>(dst + e, vec_load<TYPE, VN>(src + e));
+    }
+  }
+}
+
+// One wave per (token, 64 pieces of its row): kB ranks' rows in flight, summed
+// in rank order.  WEIGHTED = false: the gradient of the sort (w = 1, no shared
+// rows).
+template <int TYPE, int VN, bool WEIGHTED>
+__global__ __launch_bounds__(64 * kWaves) void unsort_kernel(
+    const typename El<TYPE>::raw* __restrict__ rows, const int32_t* __restrict__ row_of, const float* __restrict__ w,
+    const typename El<TYPE>::raw* __restrict__ shared, const float* __restrict__ sgate, long T, int k, int d,
+    typename El<TYPE>::raw* __restrict__ y) {
+  constexpr int kB = 8;
+  const int lane = threadIdx.x & 63;
+  const int pieces = (d + VN - 1) / VN;
+  const int slabs = (pieces + 63) / 64;
+  const long n = T * k;
+  for (long item = wave_id(); item < T * slabs; item += wave_count()) {
+    const long t = item / slabs;
+    const int c = (int)(item - t * slabs) * 64 + lane;
+    if (c >= pieces) continue;
+    const int e = piece_start<VN>(c, d);
+    float acc[VN];
+#pragma unroll
+    for (int j = 0; j < VN; ++j) acc[j] = 0.f;
+    for (int r0 = 0; r0 < k; r0 += kB) {
+      Vec<TYPE, VN> v[kB];
+      float wv[kB];
+      bool has[kB];
+#pragma unroll
+      for (int u = 0; u < kB; ++u) {
+        const long i = t * k + (r0 + u < k ? r0 + u : k - 1);
+        const int row = row_of[i];
+        has[u] = r0 + u < k && row >= 0 && row < n;
+        wv[u] = WEIGHTED ? w[i] : 1.f;
+        v[u] = vec_load<TYPE, VN>(rows + (size_t)(has[u] ? row : 0) * d + e);
+      }
+#pragma unroll
+      for (int u = 0; u < kB; ++u) {
+        if (has[u]) {
+#pragma unroll
+          for (int j = 0; j < VN; ++j)
+            acc[j] = WEIGHTED ? fmaf(wv[u], El<TYPE>::up(v[u].e[j]), acc[j]) : acc[j] + El<TYPE>::up(v[u].e[j]);
+        }
+      }
+    }
+    if (WEIGHTED && shared) {
+      const float s = sgate[t];
+      const Vec<TYPE, VN> v = vec_load<TYPE, VN>(shared + (size_t)t * d + e);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) acc[j] = fmaf(s, El<TYPE>::up(v.e[j]), acc[j]);
+    }
+    Vec<TYPE, VN> o;
+#pragma unroll
+    for (int j = 0; j < VN; ++j) o.e[j] = El<TYPE>::down(acc[j]);
+    vec_store<TYPE, VN>(y + (size_t)t * d + e, o);
+  }
+}
+
+// One wave per (token, rank), and one more a token for the shared rows: reads
+// dy[t] and its row once, writes the row's gradient and their dot product.
+template <int TYPE, int VN>
+__global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(
+    const typename El<TYPE>::raw* __restrict__ dy, const typename El<TYPE>::raw* __restrict__ rows,
+    const int32_t* __restrict__ row_of, const float* __restrict__ w, const typename El<TYPE>::raw* __restrict__ shared,
+    const float* __restrict__ sgate, long T, int k, int d, typename El<TYPE>::raw* __restrict__ drows,
+    float* __restrict__ dw, typename El<TYPE>::raw* __restrict__ dshared, float* __restrict__ dsgate) {
+  constexpr int kB = 4;
+  const int lane = threadIdx.x & 63;
+  const int pieces = (d + VN - 1) / VN;
+  const int per = k + (shared ? 1 : 0);
+  const long n = T * k;
+  for (long item = wave_id(); item < T * per; item += wave_count()) {
+    const long t = item / per;
+    const int r = (int)(item - t * per);
+    const long i = t * k + r;
+    const typename El<TYPE>::raw* src;
+    typename El<TYPE>::raw* dst;
+    float f;
+    if (r < k) {
+      const int row = row_of[i];
+      if (row < 0 || row >= n) {
+        if (lane == 0) dw[i] = 0.f;
+        continue;
+      }
+      src = rows + (size_t)row * d;
+      dst = drows + (size_t)row * d;
+      f = w[i];
+    } else {
+      src = shared + (size_t)t * d;
+      dst = dshared + (size_t)t * d;
+      f = sgate[t];
+    }
+    const typename El<TYPE>::raw* g = dy + (size_t)t * d;
+    float dot = 0.f;
+    for (int c0 = lane; c0 < pieces; c0 += 64 * kB) {
+      Vec<TYPE, VN> a[kB], b[kB];
+#pragma unroll
+      for (int u = 0; u < kB; ++u) {
+        const int e = piece_start<VN>(c0 + 64 * u < pieces ? c0 + 64 * u : pieces - 1, d);
+        a[u] = vec_load<TYPE, VN>(g + e);
+        b[u] = vec_load<TYPE, VN>(src + e);
+      }
+#pragma unroll
+      for (int u = 0; u < kB; ++u) {
+        const int c = c0 + 64 * u;
+        if (c < pieces) {
+          const int e = piece_start<VN>(c, d);
+          const int again = c * VN - e;               // elements counted by the piece before
+          Vec<TYPE, VN> o;
+#pragma unroll
+          for (int j = 0; j < VN; ++j) {
+            const float gv = El<TYPE>::up(a[u].e[j]);
+            o.e[j] = El<TYPE>::down(f * gv);
+            dot = j >= again ? fmaf(gv, El<TYPE>::up(b[u].e[j]), dot) : dot;
+          }
+          vec_store<TYPE, VN>(dst + e, o);
+        }
+      }
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) {
+      if (r < k)
+        dw[i] = dot;
+      else
+        dsgate[t] = dot;
+    }
+  }
+}
+
+// body(type tag, piece size tag) for a run-time element type and row length.
+template <int V> struct Int { static constexpr int v = V; };
+template <class F> int by_type(int type, int d, F&& body) {
+  switch (type) {
+    case MOE_TYPE_F32: return d >= 4 ? body(Int<MOE_TYPE_F32>{}, Int<4>{}) : body(Int<MOE_TYPE_F32>{}, Int<1>{});
+    case MOE_TYPE_BF16: return d >= 8 ? body(Int<MOE_TYPE_BF16>{}, Int<8>{}) : body(Int<MOE_TYPE_BF16>{}, Int<1>{});
+    case MOE_TYPE_F16: return d >= 8 ? body(Int<MOE_TYPE_F16>{}, Int<8>{}) : body(Int<MOE_TYPE_F16>{}, Int<1>{});
+  }
+  return MOE_ERR_INVALID_ARG;
+}
+
+struct SortWs {
+  int32_t* counts;
+  void* bucket;
+  size_t bucket_bytes;
+};
+bool carve_sort(Carver& c, int T, int k, int E, SortWs* w) {
+  w->counts = c.take<int32_t>(E);
+  w->bucket_bytes = bucket_ws_bytes(T, k, E);
+  w->bucket = c.take<uint8_t>(w->bucket_bytes);
+  return c.ok();
+}
+
+__global__ void zero_i32_kernel(int32_t* p, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0;
+}
+
+// Sizes every entry point of this file takes.
+int check_rows(int type, int T, int k, int d) {
+  MOE_CHECK(type_size(type) != 0 && T >= 0 && k >= 1 && d >= 1);
+  if (k > 1024 || d > (1 << 20) || (long)T * k > (1L << 30)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || k > 1024 || E < 1 || E > 1024 || (long)T * k > (1L << 30)) return 0;
+  Carver c(nullptr, (size_t)-1);
+  SortWs w;
+  carve_sort(c, T, k, E, &w);
+  return c.off + 256;
+}
+
+extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d, const int32_t* idx, int32_t k,
+                               int32_t E, void* x_sorted, int32_t* offsets, int32_t* pair_ids, int32_t* row_of,
+                               void* ws, size_t ws_bytes, hipStream_t s) {
+  MOE_TRY(check_rows(type, T, k, d));
+  MOE_CHECK(E >= 1 && E <= 1024 && offsets);
+  if (T == 0) {
+    zero_i32_kernel<<<1, 256, 0, s>>>(offsets, E + 1);
+    MOE_HIP(hipGetLastError());
+    return MOE_OK;
+  }
+  const int es = type_size(type);
+  MOE_CHECK(x && idx && x_sorted && pair_ids && row_of && ws);
+  MOE_CHECK(aligned(x, es) && aligned(x_sorted, es) && aligned(ws, 256));
+  MOE_CHECK(aligned(idx, 4) && aligned(offsets, 4) && aligned(pair_ids, 4) && aligned(row_of, 4));
+  Carver c(ws, ws_bytes);
+  SortWs w;
+  if (!carve_sort(c, T, k, E, &w)) return MOE_ERR_INVALID_ARG;
+  MOE_TRY(bucket_launch(idx, T, k, E, w.counts, offsets, pair_ids, w.bucket, w.bucket_bytes, s, nullptr));
+  const long n = (long)T * k;
+  return by_type(type, d, [&](auto ty, auto vn) -> int {
+    typedef typename El<decltype(ty)::v>::raw raw;
+    gather_rows_kernel<decltype(ty)::v, decltype(vn)::v><<<wave_grid(n), 64 * kWaves, 0, s>>>(
+        static_cast<const raw*>(x), idx, n, k, d, E, offsets, pair_ids, row_of, static_cast<raw*>(x_sorted));
+    MOE_HIP(hipGetLastError());
+    return MOE_OK;
+  });
+}
+
+namespace moe {
+namespace {
+template <bool WEIGHTED>
+int unsort_launch(const void* rows, int type, int T, int k, int d, const int32_t* row_of, const float* w,
+                  const void* shared, const float* sgate, void* y, hipStream_t s) {
+  return by_type(type, d, [&](auto ty, auto vn) -> int {
+    constexpr int VN = decltype(vn)::v;
+    typedef typename El<decltype(ty)::v>::raw raw;
+    const long slabs = ((d + VN - 1) / VN + 63) / 64;
+    unsort_kernel<decltype(ty)::v, VN, WEIGHTED><<<wave_grid(T * slabs), 64 * kWaves, 0, s>>>(
+        static_cast<const raw*>(rows), row_of, w, static_cast<const raw*>(shared), sgate, T, k, d,
+        static_cast<raw*>(y));
+    MOE_HIP(hipGetLastError());
+    return MOE_OK;
+  });
+}
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_sort_tokens_backward(const void* dx_sorted, int32_t type, int32_t T, int32_t k, int32_t d,
+                                        const int32_t* row_of, void* dx, hipStream_t s) {
+  MOE_TRY(check_rows(type, T, k, d));
+  if (T == 0) return MOE_OK;
+  const int es = type_size(type);
+  MOE_CHECK(dx_sorted && row_of && dx);
+  MOE_CHECK(aligned(dx_sorted, es) && aligned(dx, es) && aligned(row_of, 4));
+  return unsort_launch<false>(dx_sorted, type, T, k, d, row_of, nullptr, nullptr, nullptr, dx, s);
+}
+
+extern "C" int moe_unsort_combine(const void* rows, int32_t type, int32_t T, int32_t k, int32_t d,
+                                  const int32_t* row_of, const float* w, const void* shared, const float* sgate,
+                                  void* y, hipStream_t s) {
+  MOE_TRY(check_rows(type, T, k, d));
+  if (T == 0) return MOE_OK;
+  const int es = type_size(type);
+  MOE_CHECK(rows && row_of && w && y);
+  MOE_CHECK((shared == nullptr) == (sgate == nullptr));
+  MOE_CHECK(aligned(rows, es) && aligned(y, es) && aligned(shared, es) && aligned(row_of, 4) && aligned(w, 4) &&
+            aligned(sgate, 4));
+  return unsort_launch<true>(rows, type, T, k, d, row_of, w, shared, sgate, y, s);
+}
+
+extern "C" int moe_unsort_combine_backward(const void* dy, const void* rows, int32_t type, int32_t T, int32_t k,
+                                           int32_t d, const int32_t* row_of, const float* w, const void* shared,
+                                           const float* sgate, void* drows, float* dw, void* dshared, float* dsgate,
+                                           hipStream_t s) {
+  MOE_TRY(check_rows(type, T, k, d));
+  if (T == 0) return MOE_OK;
+  const int es = type_size(type);
+  MOE_CHECK(dy && rows && row_of && w && drows && dw);
+  const bool has = shared != nullptr;
+  MOE_CHECK((sgate != nullptr) == has && (dshared != nullptr) == has && (dsgate != nullptr) == has);
+  MOE_CHECK(aligned(dy, es) && aligned(rows, es) && aligned(shared, es) && aligned(drows, es) && aligned(dshared, es));
+  MOE_CHECK(aligned(row_of, 4) && aligned(w, 4) && aligned(sgate, 4) && aligned(dw, 4) && aligned(dsgate, 4));
+  return by_type(type, d, [&](auto ty, auto vn) -> int {
+    typedef typename El<decltype(ty)::v>::raw raw;
+    const long waves = (long)T * (k + (has ? 1 : 0));
+    unsort_grad_kernel<decltype(ty)::v, decltype(vn)::v><<<wave_grid(waves), 64 * kWaves, 0, s>>>(
+        static_cast<const raw*>(dy), static_cast<const raw*>(rows), row_of, w, static_cast<const raw*>(shared), sgate,
+        T, k, d, static_cast<raw*>(drows), dw, static_cast<raw*>(dshared), dsgate);
+    MOE_HIP(hipGetLastError());
+    return MOE_OK;
+  });
+}

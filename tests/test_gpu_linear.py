@@ -1,0 +1,208 @@
+"""4-bit products on the GPU against fp64.
+
+Tolerance, derived: the products q x and x are exact (4 + 8 significant bits),
+their sums over a group of at most 128 inputs are taken in fp32 with each
+addition off by at most 2^-23 of the partial sum (half of that for an adder
+that rounds to nearest), the two sums are scaled and added (three roundings)
+and the groups are added one after the other and across at most 16 partial
+sums.  With c = 16 + q <= 31 the error of y[o] is at most
+    (128 + 3 + G + 16) 2^-23 sum_g (|s| sum c |x| + |b - 16 s| sum |x|)."""
+import numpy as np
+import pytest
+
+import moe_synth as ms
+from gpu_support import DeviceLayer
+from oracle import layer as olayer
+from oracle import rows as orows
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+moe = pytest.importorskip("sparse_moe_decode_router_amd")
+
+
+def _matrix(rng, out, n_in, group):
+    codes = rng.integers(0, 16, (out, n_in), dtype=np.uint8)
+    s = rng.uniform(0.002, 0.02, (out, n_in // group)).astype(np.float16)
+    return codes, s, (-8 * s.astype(np.float32) * rng.uniform(0.9, 1.1, s.shape)).astype(np.float16)
+
+
+def _x(rng, T, n_in):
+    bits = ms.f32_to_bf16_bits(rng.standard_normal((T, n_in), dtype=np.float32))
+    return olayer.bf16_to_f64(bits), torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def _check(y, x, m, what=""):
+    codes, s, b = m
+    G = s.shape[1]
+    group = codes.shape[1] // G
+    up = lambda a: np.repeat(np.asarray(a, np.float64), group, axis=1)
+    mag = np.abs(x) @ (np.abs(up(s)) * (16.0 + codes) + np.abs(up(b.astype(np.float64) - 16.0 * s.astype(np.float64)))).T
+    err = np.abs(y.cpu().double().numpy() - x @ orows.linear_weights(*m).T)
+    tol = (128 + 3 + G + 16) * 2.0 ** -23 * mag
+    bad = np.argwhere(~(err <= tol))
+    assert bad.size == 0, (what, bad[:4].tolist(), float(np.nanmax(err / np.maximum(tol, 1e-300))))
+
+
+@pytest.mark.parametrize("T,n_in,n_out,group", [
+    (1, 64, 1, 64), (1, 32, 3, 32), (1, 128, 17, 128), (1, 2048, 512, 64), (2, 320, 100, 64), (7, 96, 33, 32),
+    (8, 2048, 130, 64), (15, 192, 16, 64), (16, 1024, 47, 128), (17, 256, 65, 64), (31, 512, 40, 32),
+    (33, 4096, 72, 128), (48, 640, 129, 64), (64, 64, 64, 64), (65, 1088, 31, 64), (130, 32, 20, 32),
+    (200, 448, 50, 64), (3, 8192, 24, 64), (1, 65536, 5, 64), (300, 128, 1, 128), (5, 1920, 1000, 128)])
+def test_linear(T, n_in, n_out, group):
+    rng = np.random.default_rng([T, n_in, n_out, group])
+    m = _matrix(rng, n_out, n_in, group)
+    w = torch.from_numpy(moe.moe_pack_linear_int4(*m)).cuda()
+    x, xd = _x(rng, T, n_in)
+    y = moe.moe_linear_int4(w, xd, n_out, group)
+    _check(y, x, m)
+    # the same row of x gives the same bits wherever it sits among rows of the same number
+    assert torch.equal(moe.moe_linear_int4(w, xd.flip(0).contiguous(), n_out, group), y.flip(0))
+
+
+def test_linear_no_rows_and_non_finite_rows():
+    rng = np.random.default_rng(3)
+    m = _matrix(rng, 40, 256, 64)
+    w = torch.from_numpy(moe.moe_pack_linear_int4(*m)).cuda()
+    assert moe.moe_linear_int4(w, torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), 40).shape == (0, 40)
+    x, xd = _x(rng, 5, 256)
+    y = moe.moe_linear_int4(w, xd, 40)
+    xd[2, 7], xd[4, 255] = float("nan"), float("inf")
+    z = moe.moe_linear_int4(w, xd, 40)
+    assert torch.equal(z[[0, 1, 3]], y[[0, 1, 3]]) and not torch.isfinite(z[[2, 4]]).any()
+
+
+def test_linear_unaligned_weights_and_streams():
+    """Packed matrices need 4-byte alignment only; another stream, and a graph."""
+    rng = np.random.default_rng(4)
+    m = _matrix(rng, 77, 192, 64)
+    p = torch.from_numpy(moe.moe_pack_linear_int4(*m)).cuda()
+    buf = torch.zeros(p.numel() + 4, dtype=torch.uint8, device="cuda")
+    buf[4:] = p
+    x, xd = _x(rng, 6, 192)
+    y = moe.moe_linear_int4(p, xd, 77)
+    assert torch.equal(moe.moe_linear_int4(buf[4:], xd, 77), y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    z = moe.moe_linear_int4(p, xd, 77, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(z, y)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        z = moe.moe_linear_int4(p, xd, 77)
+    for _ in range(3):
+        xd.copy_(_x(rng, 6, 192)[1])
+        graph.replay()
+        got = z.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, moe.moe_linear_int4(p, xd, 77))
+
+
+@pytest.mark.parametrize("T,k,E,n_in,n_out,group", [
+    (1, 1, 1, 64, 16, 64), (1, 10, 512, 256, 32, 64), (3, 2, 16, 96, 33, 32), (64, 8, 64, 128, 48, 128),
+    (40, 6, 20, 320, 65, 64), (200, 3, 4, 64, 20, 64), (900, 2, 5, 64, 17, 32), (9, 4, 1024, 64, 40, 64)])
+def test_experts(T, k, E, n_in, n_out, group):
+    rng = np.random.default_rng([T, k, E, n_in])
+    mats = [_matrix(rng, n_out, n_in, group) for _ in range(E)]
+    slots = rng.permutation(E + 3)[:E].astype(np.int32)
+    nb = moe.moe_linear_bytes(n_in, n_out, group)
+    slab = np.zeros((E + 3, nb + 12), np.uint8)
+    for e in range(E):
+        slab[slots[e], :nb] = moe.moe_pack_linear_int4(*mats[e])
+    slab = torch.from_numpy(slab).cuda()
+    idx = np.minimum(rng.geometric(0.2, (T, k)) - 1, E).astype(np.int32)      # skewed; some pairs without an expert
+    idx[0, 0] = E - 1
+    x, xd = _x(rng, T, n_in)
+    X, off, pairs, row = moe.moe_sort_tokens(xd, torch.from_numpy(idx).cuda(), E)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((T * k, n_out), float("nan"), device="cuda")
+    y = moe.moe_expert_linear_int4(slab[:, :nb], torch.from_numpy(slots).cuda(), X, off, n_out, group, error=err,
+                                   out=out)
+    rX, roff, rpairs, _ = orows.sort_rows(x, idx, E)
+    for e in range(E):
+        if roff[e + 1] > roff[e]:
+            _check(y[roff[e]:roff[e + 1]], rX[roff[e]:roff[e + 1]], mats[e], e)
+    assert torch.isnan(y[roff[-1]:]).all() and int(err) == 0
+    # without a table: expert e in slot e
+    order = torch.from_numpy(np.argsort(slots)).cuda()
+    direct = torch.empty(E, nb, dtype=torch.uint8, device="cuda")
+    direct[:] = slab[torch.from_numpy(slots).cuda().long(), :nb]
+    z = moe.moe_expert_linear_int4(direct, None, X, off, n_out, group)
+    assert torch.equal(z[:roff[-1]], y[:roff[-1]])
+
+
+def test_missing_expert_gives_zeros_and_the_error_bit():
+    rng = np.random.default_rng(8)
+    E, n_in, n_out = 6, 64, 24
+    mats = [_matrix(rng, n_out, n_in, 64) for _ in range(E)]
+    slab = torch.from_numpy(np.stack([moe.moe_pack_linear_int4(*m) for m in mats])).cuda()
+    idx = torch.tensor([[0, 2], [2, 4], [5, 1]], dtype=torch.int32, device="cuda")
+    X, off, _, _ = moe.moe_sort_tokens(_x(rng, 3, n_in)[1], idx, E)
+    full = moe.moe_expert_linear_int4(slab, None, X, off, n_out)
+    for bad in (-1, 6, 1 << 30):
+        table = torch.arange(E, dtype=torch.int32, device="cuda")
+        table[2] = bad
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = moe.moe_expert_linear_int4(slab, table, X, off, n_out, error=err)
+        want = full.clone()
+        want[int(off[2]):int(off[3])] = 0
+        assert torch.equal(y, want) and int(err) == 1
+        assert torch.equal(moe.moe_expert_linear_int4(slab, table, X, off, n_out), want)
+    table[2], table[3] = 2, -1                        # an absent expert that no row asks for
+    err.zero_()
+    assert torch.equal(moe.moe_expert_linear_int4(slab, table, X, off, n_out, error=err), full) and int(err) == 0
+
+
+def test_offsets_of_other_rows_stay_in_bounds():
+    """Offsets that reach past N: the rows there are not touched."""
+    rng = np.random.default_rng(9)
+    slab = torch.from_numpy(np.stack([moe.moe_pack_linear_int4(*_matrix(rng, 16, 64, 64)) for _ in range(4)])).cuda()
+    X = _x(rng, 40, 64)[1]
+    buf = torch.full((64, 16), 3.0, device="cuda")
+    off = torch.tensor([0, 10, 30, 50, 60], dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 10, 30, 40, 40], dtype=torch.int32, device="cuda")
+    y = moe.moe_expert_linear_int4(slab, None, X, off, 16, out=buf[:40])
+    assert torch.equal(y[:40], moe.moe_expert_linear_int4(slab, None, X, good, 16)) and (buf[40:] == 3).all()
+
+
+def test_pool_matrices():
+    L = DeviceLayer(ms.CONFIGS["tiny"])
+    cfg = L.cfg
+    rng = np.random.default_rng(10)
+    idx = torch.from_numpy(rng.integers(0, cfg.E, (9, 2)).astype(np.int32)).cuda()
+    for mat, n_in in (("gate", cfg.d), ("up", cfg.d), ("down", cfg.I)):
+        x, xd = _x(rng, 9, n_in)
+        X, off, _, _ = moe.moe_sort_tokens(xd, idx, cfg.E)
+        y = moe.moe_pool_linear_int4(L.pool, mat, X, off)
+        rX, roff, _, _ = orows.sort_rows(x, idx.cpu().numpy(), cfg.E)
+        for e in range(cfg.E):
+            m = L.raw(e)[mat]
+            _check(y[roff[e]:roff[e + 1]], rX[roff[e]:roff[e + 1]], (m["codes"], m["scales"], m["biases"]), (mat, e))
+    assert L.pool.check_error() == moe.MOE_OK
+    table, _ = L.pool.read_state()
+    table[int(idx[0, 0])] = -1
+    L.pool.set_slot_table(table)
+    moe.moe_pool_linear_int4(L.pool, "down", X, off)
+    assert L.pool.check_error() == moe.MOE_ERR_NOT_RESIDENT
+
+
+def test_refusals_on_the_device():
+    L8 = DeviceLayer(ms.CONFIGS["tiny_int8"])
+    X = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(17, dtype=torch.int32, device="cuda")
+    with pytest.raises(moe.MoeError) as ei:
+        moe.moe_pool_linear_int4(L8.pool, "gate", X, off)
+    assert ei.value.status == moe.MOE_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        moe.moe_pool_linear_int4(L8.pool, "sideways", X, off)
+    w = torch.zeros(moe.moe_linear_bytes(256, 8), dtype=torch.uint8, device="cuda")
+    for call in [lambda: moe.moe_linear_int4(w, X.float(), 8), lambda: moe.moe_linear_int4(w[:-4], X, 8),
+                 lambda: moe.moe_linear_int4(w, X.t().contiguous().t(), 8), lambda: moe.moe_linear_int4(w.cpu(), X, 8),
+                 lambda: moe.moe_linear_int4(w, X, 8, out=torch.zeros(4, 9, device="cuda")),
+                 lambda: moe.moe_expert_linear_int4(w, None, X, off, 8),
+                 lambda: moe.moe_expert_linear_int4(w.view(1, -1)[:, ::2], None, X, off, 8)]:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(moe.MoeError):                 # one slot for 16 experts without a table
+        moe.moe_expert_linear_int4(w.view(1, -1), None, X, off, 8)
