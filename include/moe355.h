@@ -525,8 +525,8 @@ int moe_unsort_combine_backward(const void* dy_dev, const void* rows_dev,
  * W[o][j] = scale q + bias per group of 32, 64 or 128 inputs.  A packed matrix
  * is its codes [n_in/32][n_out][16 B] followed by its (scale, bias) fp16 pairs
  * [n_in/group][n_out], the layout of one matrix of an expert blob.  n_in a
- * multiple of group, up to 65536; n_out 1 to 2^24; packed matrices 4-byte and
- * x 16-byte aligned.  x bf16, y fp32: every product exact, sums in fp32 in a
+ * multiple of group, up to 65536; n_out 1 to 2^24; a matrix below 4 GiB; packed
+ * matrices 4-byte and x 16-byte aligned.  x bf16, y fp32: every product exact, sums in fp32 in a
  * fixed order that depends on the sizes alone.  A row of x that is not finite
  * gives a row of y that is not. */
 typedef struct moe_linear_shape {

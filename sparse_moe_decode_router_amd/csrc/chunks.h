@@ -31,8 +31,11 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
   int off[17];
 #pragma unroll
   for (int u = 0; u <= 16; ++u) {
-    const int e = lane * per + (u < per ? u : per);
-    off[u] = offsets[e < E ? e : E];
+    off[u] = 0;
+    if (u <= per) {
+      const int e = lane * per + u;
+      off[u] = offsets[e < E ? e : E];
+    }
   }
   auto chunks_of = [&](int u) {
     const int rows = off[u + 1] - off[u];

@@ -21,6 +21,7 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 struct LinArgs {
   const uint8_t* w;             // codes, then (scale, bias); expert slots w_stride apart
@@ -34,6 +35,10 @@ struct LinArgs {
   int32_t n_in, n_out;
   long N;                       // rows of x
   long chunks;                  // upper bound of row chunks
+  long chunk0;                  // this launch's first one
+  // a block: wr row groups of 16 RT weight rows times wk shares of the inputs,
+  // one wave each, over `turns` tiles of 16 RT wr rows (1 where wk > 1)
+  int32_t wr, wk, turns;
 };
 
 // Eight codes of a word as bf16 16 + q, pairs (q[u], q[u+4]), u = 0..3.
@@ -55,124 +60,159 @@ __device__ __forceinline__ bf16x8_t pair_x(u32x4_t v) {
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
-// A block: 16 RT weight rows times 16 NT rows of x, the inputs dealt to its
-// waves in steps of 64 (32 with groups of 32) and joined through LDS in wave
-// order.  Lane (m = lane & 15, kb = lane >> 4) holds weight row m and token m
-// of each tile; in a step of 64 its codes are words 2 (kb >> 1) + {0, 1} of the
-// 16-byte piece kb & 1, its activations the 16 inputs those words cover.
-template <int GROUP, int NT, int RT, bool EXP>
+// A wave: 16 RT weight rows times 16 NT rows of x over the steps kq, kq + wk,
+// ... of 64 inputs (32 with groups of 32), U steps of loads in flight.  Lane
+// (m = lane & 15, kb = lane >> 4) holds weight row m and token m of each tile;
+// in a step of 64 it loads words 2 (kb >> 1) + {0, 1} of the 16-byte piece kb & 1
+// and swaps rows of lanes so that it holds word kb of both, whose inputs are the
+// 16 bytes kb of either half of a 128-byte line of x.  The wk waves that
+// share rows are joined through LDS in order.
+template <int GROUP, int NT, int RT, int U, bool EXP>
 __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   constexpr int kStep = GROUP == 32 ? 32 : 64;
   constexpr int kM = kStep / 32;                // matrix instructions a step
-  constexpr int kU = NT == 1 ? 4 : 2;           // steps in flight a wave
-  extern __shared__ float red[];                // [waves][RT][NT][4][64]
+  extern __shared__ float red[];                // [waves][RT][NT][4][64], wk > 1
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int waves = blockDim.x >> 6;
+  const int wr = wave / a.wk, kq = wave - wr * a.wk;
   const int m = lane & 15, kb = lane >> 4;
-  const int tiles = (a.n_out + 16 * RT - 1) / (16 * RT);
+  const int rows = 16 * RT * a.wr;              // of a tile
+  const int tiles = (a.n_out + rows - 1) / rows;
+  const int tile_blocks = (tiles + a.turns - 1) / a.turns;
   const int steps = a.n_in / kStep;
   uint32_t mask = 0x00780078u, base = 0x41804180u;
   asm("" : "+s"(mask));
   asm("" : "+v"(base));
   const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, (u32x4_t){0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-  for (long item = blockIdx.x; item < a.chunks * tiles; item += gridDim.x) {
-    const long chunk = item / tiles;
-    const int tile = (int)(item - chunk * tiles);
-    long start;
-    int n;
-    const uint8_t* w = a.w;
-    bool missing = false;
-    if (EXP) {
-      const RowChunk rc = find_chunk<false>(a.offsets, a.E, a.N, chunk, 16 * NT, nullptr);
-      if (rc.e < 0) return;                     // chunks only grow with the item
-      start = rc.start;
-      n = rc.n;
-      const int slot = a.slot_table ? a.slot_table[rc.e] : rc.e;
-      missing = slot < 0 || slot >= a.n_slots;
-      if (missing) {
-        if (threadIdx.x == 0 && a.err && n > 0) atomicOr(a.err, 1);
-      } else {
-        w += (uint64_t)slot * a.w_stride;
-      }
+  const long chunk = a.chunk0 + blockIdx.x / tile_blocks;
+  const int tile0 = (int)(blockIdx.x % tile_blocks) * a.turns;
+  long start;
+  int n;
+  const uint8_t* w = a.w;
+  bool missing = false;
+  if (EXP) {
+    const RowChunk rc = find_chunk<false>(a.offsets, a.E, a.N, chunk, 16 * NT, nullptr);
+    if (rc.e < 0) return;                       // past the last chunk
+    start = rc.start;
+    n = rc.n;
+    const int slot = __builtin_amdgcn_readfirstlane(a.slot_table ? a.slot_table[rc.e] : rc.e);
+    missing = slot < 0 || slot >= a.n_slots;
+    if (missing) {
+      if (threadIdx.x == 0 && a.err && n > 0) atomicOr(a.err, 1);
     } else {
-      start = chunk * 16 * NT;
-      n = a.N - start < 16 * NT ? (int)(a.N - start) : 16 * NT;
+      w += (uint64_t)slot * a.w_stride;
     }
-    const uint32_t* sb = reinterpret_cast<const uint32_t*>(w + (uint64_t)(a.n_in / 32) * a.n_out * 16);
-    int row[RT];
+  } else {
+    start = chunk * 16 * NT;
+    n = a.N - start < 16 * NT ? (int)(a.N - start) : 16 * NT;
+  }
+  const uint32_t sb0 = (uint32_t)(a.n_in / 32) * (uint32_t)a.n_out * 16u;
+  const rsrc_t mr = make_rsrc(w, sb0 + (uint32_t)(a.n_in / GROUP) * (uint32_t)a.n_out * 4u);
+  const int end = missing ? 0 : steps;
+  // rows of x past the chunk read zeros from past the end of the buffer
+  const rsrc_t xr = make_rsrc(a.x + (size_t)start * a.n_in, (uint32_t)(n * a.n_in) * 2u);
+  const int x_lane = (m * a.n_in + 8 * kb) * 2;
+  for (int turn = 0; turn < a.turns && tile0 + turn < tiles; ++turn) {
+    const int row0 = ((tile0 + turn) * a.wr + wr) * 16 * RT;
+    uint32_t q_lane[RT], sb_lane[RT];         // byte offsets within a step's codes, a group's scales
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      row[r] = (tile * RT + r) * 16 + m;
-      if (row[r] >= a.n_out) row[r] = a.n_out - 1;
+      const int row = row0 + 16 * r + m < a.n_out ? row0 + 16 * r + m : a.n_out - 1;
+      q_lane[r] = kM == 2 ? (uint32_t)((kb & 1) * a.n_out + row) * 16u + (kb >> 1) * 8 : (uint32_t)row * 16u + kb * 4;
+      sb_lane[r] = (uint32_t)row * 4u;
     }
     f32x4_t acc[RT][NT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[r][t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    const int end = missing ? 0 : steps;
-    for (int s0 = wave; s0 < end; s0 += waves * kU) {
-      uint32_t q[kU][RT][kM], sc[kU][RT];
-      u32x4_t xv[kU][NT][kM];
+    uint32_t q[U][RT][kM], sc[U][RT];
+    u32x4_t xv[U][NT][kM];
+    auto load = [&](int u, int s) {
+      const int qs = (int)((uint32_t)s * (uint32_t)(kStep / 2) * (uint32_t)a.n_out);
+      const int ss = (int)(sb0 + (uint32_t)(s * kStep / GROUP) * (uint32_t)a.n_out * 4u);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int s = s0 + u * waves < end ? s0 + u * waves : s0;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          if (kM == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(
-                w + ((uint64_t)(2 * s + (kb & 1)) * a.n_out + row[r]) * 16 + (kb >> 1) * 8);
-            q[u][r][0] = v.x;
-            q[u][r][kM - 1] = v.y;
-          } else {
-            q[u][r][0] = *reinterpret_cast<const uint32_t*>(w + ((uint64_t)s * a.n_out + row[r]) * 16 + kb * 4);
-          }
-          sc[u][r] = sb[(uint64_t)(s * kStep / GROUP) * a.n_out + row[r]];
+      for (int r = 0; r < RT; ++r) {
+        if constexpr (kM == 2) {
+          const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(mr, q_lane[r], qs, 0);
+          q[u][r][0] = v[0];
+          q[u][r][kM - 1] = v[1];
+        } else {
+          q[u][r][0] = __builtin_amdgcn_raw_buffer_load_b32(mr, q_lane[r], qs, 0);
         }
-        const int at = kM == 2 ? s * 64 + 32 * (kb & 1) + 16 * (kb >> 1) : s * 32 + 8 * kb;
+        sc[u][r] = __builtin_amdgcn_raw_buffer_load_b32(mr, sb_lane[r], ss, 0);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < kM; ++j)
+          xv[u][t][j] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_lane + 16 * t * a.n_in * 2, s * kStep * 2 + 64 * j, 0);
+    };
+    auto compute = [&](int u) {
+      bf16x8_t xa[NT][kM];
+      f32x4_t xs[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        xs[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kM; ++j) {
+          xa[t][j] = pair_x(xv[u][t][j]);
+          xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[t][j], ones, xs[t], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float sv = f16_to_f32(sc[u][r]), bv = fmaf(-16.f, sv, f16_to_f32(sc[u][r] >> 16));
+        if constexpr (kM == 2) {                // word kb of piece 0, of piece 1
+          const auto v = __builtin_amdgcn_permlane16_swap(q[u][r][0], q[u][r][1], false, false);
+          q[u][r][0] = v[0];
+          q[u][r][1] = v[1];
+        }
+        bf16x8_t wb[kM];
+#pragma unroll
+        for (int j = 0; j < kM; ++j) wb[j] = codes_bf16(q[u][r][j], mask, base);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const bool live = 16 * t + m < n;
+          f32x4_t p = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < kM; ++j)
-            xv[u][t][j] = live ? *reinterpret_cast<const u32x4_t*>(a.x + (size_t)(start + 16 * t + m) * a.n_in + at + 8 * j)
-                               : (u32x4_t){0u, 0u, 0u, 0u};
+          for (int j = 0; j < kM; ++j) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[t][j], wb[j], p, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(sv, p[i], fmaf(bv, xs[t][i], acc[r][t][i]));
         }
       }
+    };
+    const int count = kq < end ? (end - kq + a.wk - 1) / a.wk : 0;
+    auto step = [&](int i) { return kq + i * a.wk; };
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (s0 + u * waves < end) {
-          bf16x8_t xa[NT][kM];
-          f32x4_t xs[NT];
+    for (int u = 0; u < U; ++u)
+      if (u < count) load(u, step(u));
+    int i = 0;
+    for (; i + U <= count; i += U) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            xs[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < kM; ++j) {
-              xa[t][j] = pair_x(xv[u][t][j]);
-              xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[t][j], ones, xs[t], 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const float sv = f16_to_f32(sc[u][r]), bv = fmaf(-16.f, sv, f16_to_f32(sc[u][r] >> 16));
-            bf16x8_t wb[kM];
-#pragma unroll
-            for (int j = 0; j < kM; ++j) wb[j] = codes_bf16(q[u][r][j], mask, base);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              f32x4_t p = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int j = 0; j < kM; ++j) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[t][j], wb[j], p, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[r][t][i] += fmaf(sv, p[i], bv * xs[t][i]);
-            }
-          }
-        }
+      for (int u = 0; u < U; ++u) {
+        // the compiler would otherwise gather the loads behind all the sums
+        __builtin_amdgcn_sched_barrier(0);
+        compute(u);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + U + u < count) load(u, step(i + U + u));
       }
     }
-    __syncthreads();                            // the item before has been read
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (i + u < count) compute(u);
+    if (a.wk == 1) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int o = row0 + 16 * r + m, tok = 16 * t + 4 * kb + i;
+            if (o < a.n_out && tok < n) a.y[(size_t)(start + tok) * a.n_out + o] = acc[r][t][i];
+          }
+      continue;
+    }
+    __syncthreads();                          // the item before has been read
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -180,50 +220,82 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[((wave * RT + r) * NT + t) * 256 + i * 64 + lane] = acc[r][t][i];
     __syncthreads();
-    for (int v = threadIdx.x; v < RT * NT * 256; v += blockDim.x) {
-      float sum = red[v];
-      for (int q = 1; q < waves; ++q) sum += red[q * RT * NT * 256 + v];
-      const int l = v & 63, i = (v >> 6) & 3, t = (v >> 8) % NT, r = (v >> 8) / NT;
-      const int o = (tile * RT + r) * 16 + (l & 15), tok = 16 * t + 4 * (l >> 4) + i;
+    for (int v = threadIdx.x; v < a.wr * RT * NT * 256; v += blockDim.x) {
+      const int g = v / (RT * NT * 256), z = v - g * (RT * NT * 256);
+      const float* p = red + (size_t)g * a.wk * (RT * NT * 256) + z;
+      float sum = p[0];
+      for (int j = 1; j < a.wk; ++j) sum += p[j * (RT * NT * 256)];
+      const int l = z & 63, i = (z >> 6) & 3, t = (z >> 8) % NT, r = (z >> 8) / NT;
+      const int o = ((tile0 + turn) * a.wr + g) * 16 * RT + 16 * r + (l & 15), tok = 16 * t + 4 * (l >> 4) + i;
       if (o < a.n_out && tok < n) a.y[(size_t)(start + tok) * a.n_out + o] = sum;
     }
   }
 }
 
-constexpr unsigned kMaxBlocks = 1u << 20;
+constexpr long kMaxBlocks = 1l << 21;           // of a launch (its threads are counted in 32 bits)
 
-template <int GROUP, int NT, int RT, bool EXP>
-int launch(const LinArgs& a, hipStream_t s) {
+template <int GROUP, int NT, int RT, int U, bool EXP>
+int launch(LinArgs a, int wk, long likely, hipStream_t s) {
   const int steps = a.n_in / (GROUP == 32 ? 32 : 64);
-  const int waves = steps >= 16 ? 8 : steps >= 4 ? 4 : 1;
-  const long tiles = (a.n_out + 16 * RT - 1) / (16 * RT);
-  const long items = a.chunks * tiles;
-  const unsigned grid = (unsigned)(items < (long)kMaxBlocks ? items : (long)kMaxBlocks);
-  const size_t lds = (size_t)waves * RT * NT * 256 * sizeof(float);
-  linear_int4_kernel<GROUP, NT, RT, EXP><<<grid, 64 * waves, lds, s>>>(a);
-  MOE_HIP(hipGetLastError());
+  a.wk = wk;
+  while (a.wk > 1 && 4 * a.wk > steps) a.wk /= 2;       // a share of four steps at least
+  a.wr = a.wk >= 4 ? 1 : 4 / a.wk;
+  const long tiles = (a.n_out + 16 * RT * a.wr - 1) / (16 * RT * a.wr);
+  a.turns = EXP && a.wk == 1 && tiles * likely >= 2048 ? 2 : 1;
+  const long tile_blocks = (tiles + a.turns - 1) / a.turns;
+  const size_t lds = a.wk > 1 ? (size_t)a.wr * a.wk * RT * NT * 256 * sizeof(float) : 0;
+  const long per = kMaxBlocks / tile_blocks > 0 ? kMaxBlocks / tile_blocks : 1;        // chunks a launch
+  for (a.chunk0 = 0; a.chunk0 < a.chunks; a.chunk0 += per) {
+    const long c = a.chunks - a.chunk0 < per ? a.chunks - a.chunk0 : per;
+    linear_int4_kernel<GROUP, NT, RT, U, EXP><<<(unsigned)(c * tile_blocks), 64 * a.wr * a.wk, lds, s>>>(a);
+    MOE_HIP(hipGetLastError());
+  }
   return MOE_OK;
 }
 
+// Tile shapes by the number of 16 x 16 output tiles, about a block for each of
+// the 256 CUs first.  A block reads its rows of x and of W once, so beyond that
+// wider tiles save reads: x is re-read for every row tile (from L2, which is
+// what bounds more than a few rows of x), W for every 16 rows.  Measured, us:
+//   4096 x 4096   T = 1: RT 1 5.6, RT 2 6.8    T = 32: RT 1 13, RT 2 8.6, RT 4 11.2
+//                 T = 64: RT 2 13.2, RT 4 11.5   T = 1024: RT 4 94, NT 4 RT 4 76
+//   2048 x 8192   T = 1: RT 2 5.1, RT 1 5.3      T = 64: RT 4 11.5
+//   4096 x 16384  T = 8: RT 2 10.6, RT 4 11.4    T = 16: RT 2 13.2, RT 4 11.9
+// Inputs are split over the waves of a block (8 shares where blocks are few, 4
+// or none where they are many), which keeps more loads in flight per CU than
+// more steps per wave: 2048 x 2048, T = 1: 4.3 with four shares, 5.1 with two.
 template <int GROUP, bool EXP>
 int by_rows(LinArgs a, hipStream_t s) {
-  // rows a chunk: all of them for one matrix, the expected rows of a bucket for experts
-  const long rows = EXP ? (a.N + a.E - 1) / a.E : a.N;
-  const int nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  a.chunks = EXP ? max_chunks(a.N, a.E, 16 * nt, false) : (a.N + 16 * nt - 1) / (16 * nt);
-  return nt == 1 ? launch<GROUP, 1, 1, EXP>(a, s) : nt == 2 ? launch<GROUP, 2, 1, EXP>(a, s)
-                                                            : launch<GROUP, 4, 1, EXP>(a, s);
+  const long rows = EXP ? (a.N + a.E - 1) / a.E : a.N;          // expected of a bucket, for experts
+  const long t16 = (a.n_out + 15) / 16;
+  const auto chunks = [&](int size, bool most) -> long {
+    if (!EXP) return (a.N + size - 1) / size;
+    return most ? max_chunks(a.N, a.E, size, false) : (a.N < a.E ? a.N : (rows + size - 1) / size * a.E);
+  };
+  const long wide = chunks(64, false);
+  if (rows > 32 && t16 / 4 * wide >= 256) {
+    a.chunks = chunks(64, true);
+    return launch<GROUP, 4, 4, 1, EXP>(a, t16 / 4 * wide >= 1024 ? 1 : 4, wide, s);
+  }
+  a.chunks = chunks(16, true);
+  const long likely = chunks(16, false), units = t16 * likely;
+  if (units > 512 && rows > 8) return launch<GROUP, 1, 4, 2, EXP>(a, units > 8192 ? 1 : units > 1024 ? 4 : 8, likely, s);
+  if (units > 256) return launch<GROUP, 1, 2, 2, EXP>(a, units > 16384 ? 1 : units > 1024 ? 4 : 8, likely, s);
+  if (a.n_in >= 4096) return launch<GROUP, 1, 1, 4, EXP>(a, 8, likely, s);
+  return launch<GROUP, 1, 1, 2, EXP>(a, 4, likely, s);
 }
 
 template <bool EXP> int linear_launch(const LinArgs& a, int group, hipStream_t s) {
   return group == 32 ? by_rows<32, EXP>(a, s) : group == 64 ? by_rows<64, EXP>(a, s) : by_rows<128, EXP>(a, s);
 }
 
+size_t codes_bytes(const moe_linear_shape* sh) { return (size_t)sh->n_in / 2 * sh->n_out; }
+// A matrix is read through 32-bit buffer offsets: below 4 GiB.
 bool linear_ok(const moe_linear_shape* sh) {
   return sh && (sh->group == 32 || sh->group == 64 || sh->group == 128) && sh->n_in >= sh->group &&
-         sh->n_in % sh->group == 0 && sh->n_in <= 65536 && sh->n_out >= 1 && sh->n_out <= (1 << 24);
+         sh->n_in % sh->group == 0 && sh->n_in <= 65536 && sh->n_out >= 1 && sh->n_out <= (1 << 24) &&
+         codes_bytes(sh) + (size_t)(sh->n_in / sh->group) * sh->n_out * 4 < (1ull << 32);
 }
-size_t codes_bytes(const moe_linear_shape* sh) { return (size_t)sh->n_in / 2 * sh->n_out; }
 
 }  // namespace
 }  // namespace moe
