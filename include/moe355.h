@@ -577,7 +577,8 @@ int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
  * topk_w and shared_gate as moe_router_topk gave them (a pair whose index is
  * outside [0, E) has no logit); offsets_dev and pair_ids_dev of
  * moe_bucket_tokens or moe_sort_tokens on the same topk_idx, needed for dW
- * and dbias.  Sizes as moe_router_topk.  The workspace needs no fill. */
+ * and dbias.  Sizes as moe_router_topk
+ * with T * k <= 2^28 and T * d <= 2^33.  The workspace needs no fill. */
 size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t E,
                                            int32_t k);
 int moe_router_topk_backward(const uint16_t* x_dev, int32_t T, int32_t d,

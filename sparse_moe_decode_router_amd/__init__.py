@@ -675,36 +675,28 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 _TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
 
 
-class _on:
-    """The device of tensor x and the stream (its current one if None) as current; enters as the stream's handle."""
+# the current stream's handle without a stream object: 0.1 against 1.1 us of a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, x, stream):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            raise ValueError("device tensors wanted")
-        self.device, self.stream, self.back = x.get_device(), stream, None
 
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device.index != self.device:
-                raise ValueError("the stream is of another device than the tensors")
-            self.back = torch.cuda.stream(self.stream)
-            self.back.__enter__()
-            return self.stream.cuda_stream
-        if torch.cuda.current_device() != self.device:
-            self.back = torch.cuda.device(self.device)
-            self.back.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *e):
-        if self.back is not None:
-            self.back.__exit__(*e)
+def _elsewhere(x, stream):
+    """None where tensor x is on the current device and no stream is named; else a context that makes its device
+    and the stream current."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("device tensors wanted")
+    dev = x.get_device()
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream is of another device than the tensors")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
 
 
 def _need(t, name, dtype, shape, device):
     """t.data_ptr() of a contiguous device tensor of that type and shape (None passes as None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda:{device} wanted, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
     return t.data_ptr()
@@ -745,23 +737,26 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
     T, d = x.shape
     k = _given(topk_idx, "topk_idx").shape[-1]
     n = T * k
-    with _on(x, stream) as s:
-        dev = x.get_device()
-        if out is None:
-            out = (torch.empty((n, d), dtype=x.dtype, device=x.device),
-                   torch.empty((E + 1,), dtype=torch.int32, device=x.device),
-                   torch.empty((n,), dtype=torch.int32, device=x.device),
-                   torch.empty((T, k), dtype=torch.int32, device=x.device))
-        rows, offsets, pairs, row_of = out
-        if workspace is None:
-            workspace = _scratch(None, moe_sort_workspace_bytes(T, k, E), dev)
-        else:
-            _scratch(workspace, 0, dev)
-        _check(_lib.moe_sort_tokens(
-            _need(x, "x", x.dtype, (T, d), dev), ty, T, d, _need(topk_idx, "topk_idx", torch.int32, (T, k), dev), k, E,
-            _need(rows, "x_sorted", x.dtype, (n, d), dev), _need(offsets, "offsets", torch.int32, (E + 1,), dev),
-            _need(pairs, "pair_ids", torch.int32, (n,), dev), _need(row_of, "row_of", torch.int32, (T, k), dev),
-            workspace.data_ptr(), workspace.numel(), s), "moe_sort_tokens")
+    away = _elsewhere(x, stream)
+    if away is not None:
+        with away:
+            return moe_sort_tokens(x, topk_idx, E, workspace, out)
+    dev = x.get_device()
+    if out is None:
+        out = (torch.empty((n, d), dtype=x.dtype, device=x.device),
+               torch.empty((E + 1,), dtype=torch.int32, device=x.device),
+               torch.empty((n,), dtype=torch.int32, device=x.device),
+               torch.empty((T, k), dtype=torch.int32, device=x.device))
+    rows, offsets, pairs, row_of = out
+    if workspace is None:
+        workspace = _scratch(None, moe_sort_workspace_bytes(T, k, E), dev)
+    else:
+        _scratch(workspace, 0, dev)
+    _check(_lib.moe_sort_tokens(
+        _need(x, "x", x.dtype, (T, d), dev), ty, T, d, _need(topk_idx, "topk_idx", torch.int32, (T, k), dev), k, E,
+        _need(rows, "x_sorted", x.dtype, (n, d), dev), _need(offsets, "offsets", torch.int32, (E + 1,), dev),
+        _need(pairs, "pair_ids", torch.int32, (n,), dev), _need(row_of, "row_of", torch.int32, (T, k), dev),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)), "moe_sort_tokens")
     return rows, offsets, pairs, row_of
 
 
@@ -770,13 +765,16 @@ def moe_sort_tokens_backward(dx_sorted, row_of, out=None, stream=None):
     ty = _row_type(dx_sorted, "dx_sorted")
     T, k = _given(row_of, "row_of").shape
     d = dx_sorted.shape[1]
-    with _on(dx_sorted, stream) as s:
-        dev = dx_sorted.get_device()
-        dx = torch.empty((T, d), dtype=dx_sorted.dtype, device=dx_sorted.device) if out is None else out
-        _check(_lib.moe_sort_tokens_backward(
-            _need(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * k, d), dev), ty, T, k, d,
-            _need(row_of, "row_of", torch.int32, (T, k), dev), _need(dx, "out", dx_sorted.dtype, (T, d), dev), s),
-            "moe_sort_tokens_backward")
+    away = _elsewhere(dx_sorted, stream)
+    if away is not None:
+        with away:
+            return moe_sort_tokens_backward(dx_sorted, row_of, out)
+    dev = dx_sorted.get_device()
+    dx = torch.empty((T, d), dtype=dx_sorted.dtype, device=dx_sorted.device) if out is None else out
+    _check(_lib.moe_sort_tokens_backward(
+        _need(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * k, d), dev), ty, T, k, d,
+        _need(row_of, "row_of", torch.int32, (T, k), dev), _need(dx, "out", dx_sorted.dtype, (T, d), dev), _raw_stream(dev)),
+        "moe_sort_tokens_backward")
     return dx
 
 
@@ -786,15 +784,18 @@ def moe_unsort_combine(rows, row_of, topk_w, shared_out=None, shared_gate=None, 
     ty = _row_type(rows, "rows")
     T, k = _given(row_of, "row_of").shape
     d, t = rows.shape[1], rows.dtype
-    with _on(rows, stream) as s:
-        dev = rows.get_device()
-        y = torch.empty((T, d), dtype=t, device=rows.device) if out is None else out
-        _check(_lib.moe_unsort_combine(
-            _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d, _need(row_of, "row_of", torch.int32, (T, k), dev),
-            _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
-            _need(shared_out, "shared_out", t, (T, d), dev),
-            _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(y, "out", t, (T, d), dev), s),
-            "moe_unsort_combine")
+    away = _elsewhere(rows, stream)
+    if away is not None:
+        with away:
+            return moe_unsort_combine(rows, row_of, topk_w, shared_out, shared_gate, out)
+    dev = rows.get_device()
+    y = torch.empty((T, d), dtype=t, device=rows.device) if out is None else out
+    _check(_lib.moe_unsort_combine(
+        _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d, _need(row_of, "row_of", torch.int32, (T, k), dev),
+        _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
+        _need(shared_out, "shared_out", t, (T, d), dev),
+        _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(y, "out", t, (T, d), dev), _raw_stream(dev)),
+        "moe_unsort_combine")
     return y
 
 
@@ -805,23 +806,26 @@ def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, share
     ty = _row_type(rows, "rows")
     T, k = _given(row_of, "row_of").shape
     d, t = rows.shape[1], rows.dtype
-    with _on(rows, stream) as s:
-        dev = rows.get_device()
-        if out is None:
-            has = shared_out is not None
-            out = (torch.empty((T * k, d), dtype=t, device=rows.device),
-                   torch.empty((T, k), dtype=torch.float32, device=rows.device),
-                   torch.empty((T, d), dtype=t, device=rows.device) if has else None,
-                   torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
-        drows, dw, dsh, dsg = out
-        _check(_lib.moe_unsort_combine_backward(
-            _need(_given(dy, "dy"), "dy", t, (T, d), dev), _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d,
-            _need(row_of, "row_of", torch.int32, (T, k), dev),
-            _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
-            _need(shared_out, "shared_out", t, (T, d), dev),
-            _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(drows, "drows", t, (T * k, d), dev),
-            _need(dw, "dtopk_w", torch.float32, (T, k), dev), _need(dsh, "dshared_out", t, (T, d), dev),
-            _need(dsg, "dshared_gate", torch.float32, (T,), dev), s), "moe_unsort_combine_backward")
+    away = _elsewhere(rows, stream)
+    if away is not None:
+        with away:
+            return moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out, shared_gate, out)
+    dev = rows.get_device()
+    if out is None:
+        has = shared_out is not None
+        out = (torch.empty((T * k, d), dtype=t, device=rows.device),
+               torch.empty((T, k), dtype=torch.float32, device=rows.device),
+               torch.empty((T, d), dtype=t, device=rows.device) if has else None,
+               torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
+    drows, dw, dsh, dsg = out
+    _check(_lib.moe_unsort_combine_backward(
+        _need(_given(dy, "dy"), "dy", t, (T, d), dev), _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d,
+        _need(row_of, "row_of", torch.int32, (T, k), dev),
+        _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
+        _need(shared_out, "shared_out", t, (T, d), dev),
+        _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(drows, "drows", t, (T * k, d), dev),
+        _need(dw, "dtopk_w", torch.float32, (T, k), dev), _need(dsh, "dshared_out", t, (T, d), dev),
+        _need(dsg, "dshared_gate", torch.float32, (T,), dev), _raw_stream(dev)), "moe_unsort_combine_backward")
     return drows, dw, dsh, dsg
 
 
@@ -863,13 +867,16 @@ def moe_linear_int4(packed, x, n_out: int, group: int = 64, out=None, stream=Non
     """y fp32 [T, n_out] = x W^T; x bf16 [T, n_in], packed uint8 [moe_linear_bytes]."""
     T, n_in = x.shape
     sh = moe_linear_shape(n_in, n_out, group)
-    with _on(x, stream) as s:
-        dev = x.get_device()
-        y = torch.empty((T, n_out), dtype=torch.float32, device=x.device) if out is None else out
-        _check(_lib.moe_linear_int4(
-            C.byref(sh), _need(packed, "packed", torch.uint8, (int(_lib.moe_linear_bytes(C.byref(sh))),), dev),
-            _need(x, "x", torch.bfloat16, (T, n_in), dev), T, _need(y, "out", torch.float32, (T, n_out), dev), s),
-            "moe_linear_int4")
+    away = _elsewhere(x, stream)
+    if away is not None:
+        with away:
+            return moe_linear_int4(packed, x, n_out, group, out)
+    dev = x.get_device()
+    y = torch.empty((T, n_out), dtype=torch.float32, device=x.device) if out is None else out
+    _check(_lib.moe_linear_int4(
+        C.byref(sh), _need(packed, "packed", torch.uint8, (int(_lib.moe_linear_bytes(C.byref(sh))),), dev),
+        _need(x, "x", torch.bfloat16, (T, n_in), dev), T, _need(y, "out", torch.float32, (T, n_out), dev), _raw_stream(dev)),
+        "moe_linear_int4")
     return y
 
 
@@ -886,18 +893,21 @@ def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, gr
             or packed.shape[1] < int(_lib.moe_linear_bytes(C.byref(sh))):
         raise ValueError(f"packed: a uint8 tensor [n_slots, {moe_linear_bytes(n_in, n_out, group)}] wanted, got "
                          f"{packed.dtype} {tuple(packed.shape)}")
-    with _on(x_sorted, stream) as s:
-        dev = x_sorted.get_device()
-        if packed.get_device() != dev:
-            raise ValueError(f"packed: a tensor on cuda:{dev} wanted")
-        E = offsets.shape[0] - 1
-        y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
-        _check(_lib.moe_expert_linear_int4(
-            C.byref(sh), packed.data_ptr(), packed.stride(0), packed.shape[0],
-            _need(slot_table, "slot_table", torch.int32, (E,), dev), E,
-            _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
-            _need(offsets, "offsets", torch.int32, (E + 1,), dev), _need(y, "out", torch.float32, (N, n_out), dev),
-            _need(error, "error", torch.int32, (1,), dev), s), "moe_expert_linear_int4")
+    away = _elsewhere(x_sorted, stream)
+    if away is not None:
+        with away:
+            return moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out, group, error, out)
+    dev = x_sorted.get_device()
+    if packed.get_device() != dev:
+        raise ValueError(f"packed: a tensor on cuda:{dev} wanted")
+    E = offsets.shape[0] - 1
+    y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
+    _check(_lib.moe_expert_linear_int4(
+        C.byref(sh), packed.data_ptr(), packed.stride(0), packed.shape[0],
+        _need(slot_table, "slot_table", torch.int32, (E,), dev), E,
+        _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
+        _need(offsets, "offsets", torch.int32, (E + 1,), dev), _need(y, "out", torch.float32, (N, n_out), dev),
+        _need(error, "error", torch.int32, (1,), dev), _raw_stream(dev)), "moe_expert_linear_int4")
     return y
 
 
@@ -907,13 +917,16 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
         raise ValueError(f"matrix must be one of {_MATS}")
     n_in, n_out = (pool.I, pool.d) if matrix == "down" else (pool.d, pool.I)
     N = x_sorted.shape[0]
-    with _on(x_sorted, stream) as s:
-        dev = x_sorted.get_device()
-        y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
-        _check(_lib.moe_pool_linear_int4(
-            pool.handle, _MATS.index(matrix), _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
-            _need(_given(offsets, "offsets"), "offsets", torch.int32, (pool.E + 1,), dev),
-            _need(y, "out", torch.float32, (N, n_out), dev), s), "moe_pool_linear_int4")
+    away = _elsewhere(x_sorted, stream)
+    if away is not None:
+        with away:
+            return moe_pool_linear_int4(pool, matrix, x_sorted, offsets, out)
+    dev = x_sorted.get_device()
+    y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
+    _check(_lib.moe_pool_linear_int4(
+        pool.handle, _MATS.index(matrix), _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
+        _need(_given(offsets, "offsets"), "offsets", torch.int32, (pool.E + 1,), dev),
+        _need(y, "out", torch.float32, (N, n_out), dev), _raw_stream(dev)), "moe_pool_linear_int4")
     return y
 
 
@@ -931,24 +944,27 @@ def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w
     T, d = x.shape
     E, k = w_router.shape[0] - 1, topk_idx.shape[1]
     f32, i32 = torch.float32, torch.int32
-    with _on(x, stream) as s:
-        dev = x.get_device()
-        if out is None:
-            out = (torch.empty((T, d), dtype=f32, device=x.device), torch.empty((E + 1, d), dtype=f32, device=x.device),
-                   torch.empty((E,), dtype=f32, device=x.device))
-        dx, dwr, db = out
-        if workspace is None:
-            workspace = _scratch(None, moe_router_backward_workspace_bytes(T, d, E, k), dev)
-        else:
-            _scratch(workspace, 0, dev)
-        _check(_lib.moe_router_topk_backward(
-            _need(x, "x", torch.bfloat16, (T, d), dev), T, d, _need(w_router, "w_router", f32, (E + 1, d), dev), E, k,
-            _need(topk_idx, "topk_idx", i32, (T, k), dev), _need(topk_w, "topk_w", f32, (T, k), dev),
-            _need(shared_gate, "shared_gate", f32, (T,), dev), _need(dtopk_w, "dtopk_w", f32, (T, k), dev),
-            _need(dshared_gate, "dshared_gate", f32, (T,), dev), _need(offsets, "offsets", i32, (E + 1,), dev),
-            _need(pair_ids, "pair_ids", i32, (T * k,), dev), _need(dx, "dx", f32, (T, d), dev),
-            _need(dwr, "dw_router", f32, (E + 1, d), dev), _need(db, "dlogit_bias", f32, (E,), dev),
-            workspace.data_ptr(), workspace.numel(), s), "moe_router_topk_backward")
+    away = _elsewhere(x, stream)
+    if away is not None:
+        with away:
+            return moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids, workspace, out)
+    dev = x.get_device()
+    if out is None:
+        out = (torch.empty((T, d), dtype=f32, device=x.device), torch.empty((E + 1, d), dtype=f32, device=x.device),
+               torch.empty((E,), dtype=f32, device=x.device))
+    dx, dwr, db = out
+    if workspace is None:
+        workspace = _scratch(None, moe_router_backward_workspace_bytes(T, d, E, k), dev)
+    else:
+        _scratch(workspace, 0, dev)
+    _check(_lib.moe_router_topk_backward(
+        _need(x, "x", torch.bfloat16, (T, d), dev), T, d, _need(w_router, "w_router", f32, (E + 1, d), dev), E, k,
+        _need(topk_idx, "topk_idx", i32, (T, k), dev), _need(topk_w, "topk_w", f32, (T, k), dev),
+        _need(shared_gate, "shared_gate", f32, (T,), dev), _need(dtopk_w, "dtopk_w", f32, (T, k), dev),
+        _need(dshared_gate, "dshared_gate", f32, (T,), dev), _need(offsets, "offsets", i32, (E + 1,), dev),
+        _need(pair_ids, "pair_ids", i32, (T * k,), dev), _need(dx, "dx", f32, (T, d), dev),
+        _need(dwr, "dw_router", f32, (E + 1, d), dev), _need(db, "dlogit_bias", f32, (E,), dev),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)), "moe_router_topk_backward")
     return dx, dwr, db
 
 

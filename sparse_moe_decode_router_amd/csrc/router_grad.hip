@@ -6,74 +6,208 @@
 //     db[e]  = sum over the pairs of bucket e of g
 // Only k + 1 of E + 1 logits of a token have a gradient, so both products are
 // weighted sums of rows: dx gathers router rows per token, dW gathers token
-// rows per bucket (the stable lists of moe_bucket_tokens), in chunks of kCP
-// rows whose partial sums are joined in chunk order.  fp32 throughout, fixed
-// order, no atomics.
+// rows per bucket (the stable lists of moe_bucket_tokens).  One launch, its
+// blocks in three roles; fp32 throughout, fixed order, no atomics.
 #include "internal.h"
-#include "chunks.h"
 #include "device.h"
 
 namespace moe {
 namespace {
 
-constexpr int kCols = 512;      // columns a block
-constexpr int kCP = 64;         // rows a chunk
-constexpr unsigned kMaxBlocks = 1u << 20;
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kXCols = 256;     // columns a wave of the dx role
+constexpr int kWCols = 512;     // columns a block of the expert rows
+constexpr int kECols = 64;      // columns a block of row E
+constexpr int kTile = 512;      // pairs of a bucket at a time
+// Up to this many pairs each role forms their g itself; more take a launch of
+// their own first, which saves every column slab the k products of each pair.
+constexpr long kPairsMax = 4096;
 
-inline unsigned capped(long n) { return (unsigned)(n < (long)kMaxBlocks ? n : (long)kMaxBlocks); }
+struct GradArgs {
+  const uint16_t* x;
+  const float* W;
+  const int32_t* idx;
+  const float* w;
+  const float* sgate;
+  const float* dw;
+  const float* dsgate;          // or null
+  const int32_t* offsets;
+  const int32_t* pair_ids;
+  const float* g;               // [T][k+1], or null: formed where it is used
+  float* dx;
+  float* dW;
+  float* dbias;
+  int T, d, E, k;
+  unsigned blocks_e, blocks_w;  // blocks of row E, of the expert rows; the rest: dx
+};
 
-// g [T][k+1] and dx; block = (token, kCols columns).
-__global__ __launch_bounds__(128) void router_grad_x_kernel(
-    const float* __restrict__ W, const int32_t* __restrict__ idx, const float* __restrict__ w,
-    const float* __restrict__ sgate, const float* __restrict__ dw, const float* __restrict__ dsgate, int T, int d,
-    int E, int k, float* __restrict__ g, float* __restrict__ dx) {
-  extern __shared__ float lg[];                 // [k+1] g | [k+1] router row
-  int* le = reinterpret_cast<int*>(lg + k + 1);
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int slabs = dx ? (d + kCols - 1) / kCols : 1;
-  for (long item = blockIdx.x; item < (long)T * slabs; item += gridDim.x) {
-    const int t = (int)(item / slabs), slab = (int)(item % slabs);
-    float z = 0.f;
-    for (int r = lane; r < k; r += 64) z = fmaf(w[(size_t)t * k + r], dw[(size_t)t * k + r], z);
-    z = wave_sum(z);
-    __syncthreads();
-    for (int r = tid; r <= k; r += 128) {
-      float v = 0.f;
-      int e = E;
-      if (r < k) {
-        const size_t i = (size_t)t * k + r;
-        v = w[i] * (dw[i] - z);
-        e = idx[i];
-        if (e < 0 || e >= E) {                  // a pair without an expert
-          v = 0.f;
-          e = -1;
-        }
-      } else if (dsgate) {
-        const float s = sgate[t];
-        v = dsgate[t] * (s * (1.f - s));
-      }
-      lg[r] = v;
-      le[r] = e;
-      if (slab == 0) g[(size_t)t * (k + 1) + r] = v;
+__device__ __forceinline__ float gate_grad(const GradArgs& a, int t) {
+  if (!a.dsgate) return 0.f;
+  const float s = a.sgate[t];
+  return a.dsgate[t] * (s * (1.f - s));
+}
+
+// g of pair i of token t (one thread).
+__device__ __forceinline__ float pair_grad(const GradArgs& a, long i, int t) {
+  const float* w = a.w + (size_t)t * a.k;
+  const float* dw = a.dw + (size_t)t * a.k;
+  float z = 0.f;
+  for (int r = 0; r < a.k; ++r) z = fmaf(w[r], dw[r], z);
+  return a.w[i] * (a.dw[i] - z);
+}
+
+__global__ __launch_bounds__(256) void router_grad_pairs_kernel(GradArgs a, float* __restrict__ g) {
+  const long n = (long)a.T * (a.k + 1);
+  for (long j = (long)blockIdx.x * 256 + threadIdx.x; j < n; j += (long)gridDim.x * 256) {
+    const int t = (int)(j / (a.k + 1)), r = (int)(j - (long)t * (a.k + 1));
+    g[j] = r < a.k ? pair_grad(a, (long)t * a.k + r, t) : gate_grad(a, t);
+  }
+}
+
+// acc[8] += gv * 8 bf16 of v
+__device__ __forceinline__ void fma8(float (&acc)[8], float gv, uint4 v) {
+  const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(gv, bf16_lo(p[i]), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(gv, bf16_hi(p[i]), acc[2 * i + 1]);
+  }
+}
+
+// dW[E], kECols columns: 64 groups of 8 lanes take the tokens in turn.
+__device__ void row_e(const GradArgs& a, int slab, float* red, float* lg) {
+  constexpr int kB = 8, kG = kThreads / 8;
+  const int tid = threadIdx.x, grp = tid >> 3;
+  const uint16_t* x = a.x + slab * kECols + (tid & 7) * 8;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int t0 = 0; t0 < a.T; t0 += kG * kB) {
+    uint4 v[kB];
+#pragma unroll
+    for (int u = 0; u < kB; ++u) {
+      const int t = t0 + u * kG + grp;
+      v[u] = *reinterpret_cast<const uint4*>(x + (size_t)(t < a.T ? t : a.T - 1) * a.d);
     }
     __syncthreads();
-    const int c = slab * kCols + tid * 4;
-    if (!dx || c >= d) continue;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kB = 8;
-    for (int r0 = 0; r0 <= k; r0 += kB) {
+    if (t0 + tid < a.T) lg[tid] = a.g ? a.g[(size_t)(t0 + tid) * (a.k + 1) + a.k] : gate_grad(a, t0 + tid);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kB; ++u)
+      if (t0 + u * kG + grp < a.T) fma8(acc, lg[u * kG + grp], v[u]);
+  }
+  static_assert(kG * kB == kThreads, "one weight a thread");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[grp * 65 + (tid & 7) * 8 + i] = acc[i];
+  __syncthreads();
+  if (tid < kECols) {
+    float v = 0.f;
+    for (int q = 0; q < kG; ++q) v += red[q * 65 + tid];
+    a.dW[(size_t)a.E * a.d + slab * kECols + tid] = v;
+  }
+}
+
+// dW[e], kWCols columns (and db[e]): the waves take the bucket's pairs in turn.
+__device__ void row_expert(const GradArgs& a, int e, int slab, float* red, float* lg, int* lt) {
+  constexpr int kB = 8;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const long n = (long)a.T * a.k;
+  long lo = a.offsets[e], hi = a.offsets[e + 1];
+  lo = lo < 0 ? 0 : lo;                         // offsets of other pairs reach no memory past these
+  hi = hi > n ? n : hi;
+  const int c = slab * kWCols + lane * 8;
+  const uint16_t* x = a.x + (c < a.d ? c : a.d - 8);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float bias = 0.f;
+  for (long p0 = lo; p0 < hi; p0 += kTile) {
+    const int m = hi - p0 < kTile ? (int)(hi - p0) : kTile;
+    __syncthreads();
+    if (tid < m) {
+      const int i = a.pair_ids[p0 + tid];
+      const bool ok = i >= 0 && i < n;
+      const int t = ok ? i / a.k : 0;
+      const float g = !ok ? 0.f : a.g ? a.g[(size_t)i + t] : pair_grad(a, i, t);
+      lt[tid] = t;
+      lg[tid] = g;
+      bias += g;
+    }
+    __syncthreads();
+    if (a.dW) {
+      for (int q0 = wave; q0 < m; q0 += kWaves * kB) {
+        uint4 v[kB];
+#pragma unroll
+        for (int u = 0; u < kB; ++u)
+          if (q0 + u * kWaves < m)
+            v[u] = *reinterpret_cast<const uint4*>(x + (size_t)__builtin_amdgcn_readfirstlane(lt[q0 + u * kWaves]) * a.d);
+#pragma unroll
+        for (int u = 0; u < kB; ++u)
+          if (q0 + u * kWaves < m) fma8(acc, lg[q0 + u * kWaves], v[u]);
+      }
+    }
+  }
+  if (a.dW) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[wave * kWCols + i * 64 + lane] = acc[i];
+    __syncthreads();
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kWaves; ++q) v += red[q * kWCols + (tid & 7) * 64 + (tid >> 3)];
+    static_assert(kWCols == kThreads, "one column a thread");
+    if (slab * kWCols + tid < a.d) a.dW[(size_t)e * a.d + slab * kWCols + tid] = v;
+  }
+  if (a.dbias && slab == 0) {
+    bias = wave_sum(bias);
+    __syncthreads();
+    if (lane == 0) lg[wave] = bias;
+    __syncthreads();
+    if (tid == 0) {
+      float v = 0.f;
+      for (int q = 0; q < kWaves; ++q) v += lg[q];
+      a.dbias[e] = v;
+    }
+  }
+}
+
+// dx of one token, kXCols columns: one wave.
+__device__ void token_x(const GradArgs& a, int t, int slab) {
+  constexpr int kB = 11;
+  const int lane = threadIdx.x & 63;
+  const int c = slab * kXCols + lane * 4;
+  const float* W = a.W + (c < a.d ? c : a.d - 4);
+  float z = 0.f;
+  if (!a.g) {
+    for (int r = lane; r < a.k; r += 64) z = fmaf(a.w[(size_t)t * a.k + r], a.dw[(size_t)t * a.k + r], z);
+    z = wave_sum(z);
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = 0; r0 <= a.k; r0 += 64) {       // 64 router rows' weights in the lanes
+    const int r = r0 + lane;
+    float gl = 0.f;
+    int el = -1;
+    if (r < a.k) {
+      const size_t i = (size_t)t * a.k + r;
+      el = a.idx[i];
+      if (el >= a.E) el = -1;
+      gl = a.g ? a.g[i + t] : a.w[i] * (a.dw[i] - z);
+    } else if (r == a.k) {
+      el = a.E;
+      gl = a.g ? a.g[(size_t)t * (a.k + 1) + a.k] : gate_grad(a, t);
+    }
+    const int m = a.k + 1 - r0 < 64 ? a.k + 1 - r0 : 64;
+    for (int q0 = 0; q0 < m; q0 += kB) {
       float4 v[kB];
       float gv[kB];
+      int e[kB];
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
-        const int r = r0 + u <= k ? r0 + u : k;
-        const int e = le[r];
-        gv[u] = lg[r];
-        v[u] = *reinterpret_cast<const float4*>(W + (size_t)(e < 0 ? 0 : e) * d + c);
+        const int q = q0 + u < m ? q0 + u : m - 1;
+        e[u] = q0 + u < m ? __builtin_amdgcn_readlane(el, q) : -1;
+        gv[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gl), q));
+        if (e[u] >= 0) v[u] = *reinterpret_cast<const float4*>(W + (size_t)e[u] * a.d);
       }
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
-        if (r0 + u <= k && le[r0 + u] >= 0) {
+        if (e[u] >= 0) {
           acc.x = fmaf(gv[u], v[u].x, acc.x);
           acc.y = fmaf(gv[u], v[u].y, acc.y);
           acc.z = fmaf(gv[u], v[u].z, acc.z);
@@ -81,167 +215,39 @@ __global__ __launch_bounds__(128) void router_grad_x_kernel(
         }
       }
     }
-    *reinterpret_cast<float4*>(dx + (size_t)t * d + c) = acc;
   }
+  if (c < a.d) *reinterpret_cast<float4*>(a.dx + (size_t)t * a.d + c) = acc;
 }
 
-// One chunk of a bucket (or of all tokens for row E), kCols columns: four
-// waves take the chunk's rows in turn, joined in wave order.
-__global__ __launch_bounds__(256) void router_grad_w_kernel(
-    const uint16_t* __restrict__ x, const float* __restrict__ g, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ pair_ids, int T, int d, int E, int k, long chunks, float* __restrict__ dW,
-    float* __restrict__ part, long part_rows) {
-  __shared__ float red[4][8][64];
-  __shared__ float lg[kCP];
-  __shared__ int lt[kCP];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int slabs = (d + kCols - 1) / kCols;
-  const long n = (long)T * k;
-  for (long item = blockIdx.x; item < chunks * slabs; item += gridDim.x) {
-    const long j = item / slabs;
-    const int slab = (int)(item - j * slabs);
-    ChunkTotals tot;
-    RowChunk rc = find_chunk<true>(offsets, E, n, j, kCP, &tot);
-    if (rc.e < 0) {                             // row E: the tokens themselves
-      const long first = (j - tot.chunks) * kCP;
-      if (first >= (T > 0 ? T : 1)) return;     // chunks only grow with the item
-      rc.e = E;
-      rc.start = (int)first;
-      rc.n = T - first < kCP ? (int)(T - first) : kCP;
-      rc.index = (int)(j - tot.chunks);
-      rc.of = (T + kCP - 1) / kCP;              // no tokens: one chunk of none
-      rc.multi = tot.multi;
-    }
-    __syncthreads();
-    if (tid < kCP) {
-      int t = 0;
-      float v = 0.f;
-      if (tid < rc.n) {
-        if (rc.e == E) {
-          t = rc.start + tid;
-          v = g[(size_t)t * (k + 1) + k];
-        } else {
-          const int i = pair_ids[rc.start + tid];
-          if (i >= 0 && i < n) {
-            t = i / k;
-            v = g[(size_t)i + t];
-          }
-        }
-      }
-      lt[tid] = t;
-      lg[tid] = v;
-    }
-    __syncthreads();
-    const int c = slab * kCols + lane * 8;
-    const int cc = c < d ? c : d - 8;           // columns past the row: a piece that is not stored
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    constexpr int kB = 8;
-    for (int q0 = wave; q0 < rc.n; q0 += 4 * kB) {
-      uint4 v[kB];
-      float gv[kB];
-#pragma unroll
-      for (int u = 0; u < kB; ++u) {
-        const int q = q0 + 4 * u < kCP ? q0 + 4 * u : kCP - 1;
-        gv[u] = q0 + 4 * u < rc.n ? lg[q] : 0.f;
-        v[u] = *reinterpret_cast<const uint4*>(x + (size_t)lt[q] * d + cc);
-      }
-#pragma unroll
-      for (int u = 0; u < kB; ++u) {
-        if (q0 + 4 * u < rc.n) {
-          const uint32_t p[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[2 * i] = fmaf(gv[u], bf16_lo(p[i]), acc[2 * i]);
-            acc[2 * i + 1] = fmaf(gv[u], bf16_hi(p[i]), acc[2 * i + 1]);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) red[wave][i][lane] = acc[i];
-    __syncthreads();
-    if (rc.of > 1 && rc.multi + rc.index >= part_rows) continue;   // offsets that are not T k rows
-    float* dst = rc.of > 1 ? part + (size_t)(rc.multi + rc.index) * d : dW + (size_t)rc.e * d;
-    for (int o = tid; o < kCols; o += 256) {
-      const int l = o >> 3, i = o & 7;
-      const float v = ((red[0][i][l] + red[1][i][l]) + red[2][i][l]) + red[3][i][l];
-      if (slab * kCols + o < d) dst[slab * kCols + o] = v;
-    }
+// Blocks of row E first (they take longest), then the expert rows, then dx.
+// Blocks go to the 8 XCDs in turn, so numbering the column slabs fastest keeps
+// one XCD's L2 on the same columns of x and W where their number divides 8.
+__global__ __launch_bounds__(kThreads) void router_grad_kernel(GradArgs a) {
+  __shared__ float red[kThreads / 8 * 65 > kWaves * kWCols ? kThreads / 8 * 65 : kWaves * kWCols];
+  __shared__ float lg[kTile];
+  __shared__ int lt[kTile];
+  unsigned b = blockIdx.x;
+  if (b < a.blocks_e) {
+    row_e(a, (int)b, red, lg);
+    return;
   }
+  b -= a.blocks_e;
+  if (b < a.blocks_w) {
+    const int slabs = a.dW ? (a.d + kWCols - 1) / kWCols : 1;
+    row_expert(a, (int)(b / slabs), (int)(b % slabs), red, lg, lt);
+    return;
+  }
+  b -= a.blocks_w;
+  const int slabs = (a.d + kXCols - 1) / kXCols;
+  const int t = (int)(b / slabs) * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (t < a.T) token_x(a, t, (int)(b % slabs));
 }
 
-// Chunk sums of the rows that have several, joined in order; db.  Block =
-// (router row, kCols columns).
-__global__ __launch_bounds__(128) void router_grad_join_kernel(
-    const float* __restrict__ g, const int32_t* __restrict__ offsets, const int32_t* __restrict__ pair_ids, int T,
-    int d, int E, int k, const float* __restrict__ part, long part_rows, float* __restrict__ dW, float* __restrict__ dbias) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int slabs = dW ? (d + kCols - 1) / kCols : 1;
-  const long n = (long)T * k;
-  for (int item = blockIdx.x; item < (E + 1) * slabs; item += gridDim.x) {
-    const int e = item / slabs, slab = item % slabs;
-    // chunks of multi-chunk experts before e, and of e itself
-    int before = 0, mine = 0;
-    for (int q = lane; q < E && q <= e; q += 64) {
-      const int rows = offsets[q + 1] - offsets[q];
-      const int c = rows > 0 ? (rows + kCP - 1) / kCP : 0;
-      if (q < e) before += c > 1 ? c : 0;
-    }
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) before += __shfl_xor(before, s, 64);
-    if (e < E) {
-      const int rows = offsets[e + 1] - offsets[e];
-      mine = rows > 0 ? (rows + kCP - 1) / kCP : 0;
-    } else {
-      mine = (T + kCP - 1) / kCP;
-    }
-    const int c = slab * kCols + tid * 4;
-    if (dW && mine > 1 && c < d && (long)before + mine <= part_rows) {
-      const float* p = part + (size_t)before * d + c;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kB = 8;
-      for (int q0 = 0; q0 < mine; q0 += kB) {
-        float4 v[kB];
-#pragma unroll
-        for (int u = 0; u < kB; ++u)
-          v[u] = *reinterpret_cast<const float4*>(p + (size_t)(q0 + u < mine ? q0 + u : mine - 1) * d);
-#pragma unroll
-        for (int u = 0; u < kB; ++u) {
-          if (q0 + u < mine) {
-            acc.x += v[u].x; acc.y += v[u].y; acc.z += v[u].z; acc.w += v[u].w;
-          }
-        }
-      }
-      *reinterpret_cast<float4*>(dW + (size_t)e * d + c) = acc;
-    }
-    if (dbias && slab == 0 && e < E && tid < 64) {
-      float v = 0.f;
-      for (long q = (long)offsets[e] + lane; q < offsets[e + 1] && q >= 0 && q < n; q += 64) {
-        const int i = pair_ids[q];
-        if (i >= 0 && i < n) v += g[(size_t)i + i / k];
-      }
-      v = wave_sum(v);
-      if (lane == 0) dbias[e] = v;
-    }
-  }
-}
-
-struct GradWs {
-  float* g;
-  float* part;
-  long part_rows;
-};
-bool carve_grad(Carver& c, int T, int d, int E, int k, GradWs* w) {
-  w->g = c.take<float>((size_t)T * (k + 1));
-  // chunks of buckets that have more than one: rows <= T k make at most 2 T k / kCP of them
-  w->part_rows = 2 * (long)T * k / kCP + (T + kCP - 1) / kCP + 1;
-  w->part = c.take<float>((size_t)w->part_rows * d);
-  return c.ok();
-}
 bool sizes_ok(int T, int d, int E, int k) {
   return T >= 0 && d >= 64 && d % 64 == 0 && d <= 8192 && E >= 1 && E <= 1024 && k >= 1 && k <= E &&
-         (long)T * k <= (1L << 30);
+         (long)T * k <= (1L << 28) && (long)T * d <= (1L << 33);
 }
+size_t pairs_bytes(int T, int k) { return (size_t)T * (k + 1) * sizeof(float); }
 
 }  // namespace
 }  // namespace moe
@@ -250,10 +256,7 @@ using namespace moe;
 
 extern "C" size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t E, int32_t k) {
   if (!sizes_ok(T, d, E, k)) return 0;
-  Carver c(nullptr, (size_t)-1);
-  GradWs w;
-  carve_grad(c, T, d, E, k, &w);
-  return c.off + 256;
+  return pairs_bytes(T, k) + 256;
 }
 
 extern "C" int moe_router_topk_backward(const uint16_t* x, int32_t T, int32_t d, const float* W, int32_t E, int32_t k,
@@ -268,27 +271,21 @@ extern "C" int moe_router_topk_backward(const uint16_t* x, int32_t T, int32_t d,
     MOE_CHECK((dW == nullptr && dbias == nullptr) || pair_ids);
   }
   MOE_CHECK(aligned(x, 16) && aligned(W, 16) && aligned(dx, 16) && aligned(dW, 16) && aligned(ws, 256));
-  GradWs b{};
-  if (T > 0) {
-    Carver c(ws, ws_bytes);
-    if (!carve_grad(c, T, d, E, k, &b)) return MOE_ERR_INVALID_ARG;
-    const long slabs = dx ? (d + kCols - 1) / kCols : 1;
-    router_grad_x_kernel<<<capped(T * slabs), 128, (size_t)(k + 1) * 8, s>>>(W, idx, w, sgate, dw, dsgate, T, d, E, k,
-                                                                            b.g, dx);
+  MOE_CHECK(T == 0 || ws_bytes >= pairs_bytes(T, k));
+  GradArgs a{x, W, idx, w, sgate, dw, dsgate, offsets, pair_ids, nullptr, dx, dW, dbias, T, d, E, k, 0, 0};
+  if ((long)T * k > kPairsMax) {
+    float* g = static_cast<float*>(ws);
+    const long blocks = ((long)T * (k + 1) + 255) / 256;
+    router_grad_pairs_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(a, g);
     MOE_HIP(hipGetLastError());
+    a.g = g;
   }
-  if (dW) {
-    const long slabs = (d + kCols - 1) / kCols;
-    const long chunks = max_chunks((long)T * k, E, kCP, true) + (T > 0 ? (T + kCP - 1) / kCP : 1);
-    router_grad_w_kernel<<<capped(chunks * slabs), 256, 0, s>>>(x, b.g, offsets, pair_ids, T, d, E, k, chunks, dW,
-                                                               b.part, b.part_rows);
-    MOE_HIP(hipGetLastError());
-  }
-  if (dW || dbias) {
-    const long slabs = dW ? (d + kCols - 1) / kCols : 1;
-    router_grad_join_kernel<<<capped((E + 1) * slabs), 128, 0, s>>>(b.g, offsets, pair_ids, T, d, E, k, b.part,
-                                                                    b.part_rows, dW, dbias);
-    MOE_HIP(hipGetLastError());
-  }
+  a.blocks_e = dW ? (unsigned)(d / kECols) : 0;
+  a.blocks_w = dW ? (unsigned)(E * ((d + kWCols - 1) / kWCols)) : dbias ? (unsigned)E : 0;
+  const unsigned blocks_x = dx ? (unsigned)((T + kWaves - 1) / kWaves) * (unsigned)((d + kXCols - 1) / kXCols) : 0;
+  const unsigned blocks = a.blocks_e + a.blocks_w + blocks_x;
+  if (blocks == 0) return MOE_OK;               // dx of no tokens
+  router_grad_kernel<<<blocks, kThreads, 0, s>>>(a);
+  MOE_HIP(hipGetLastError());
   return MOE_OK;
 }

@@ -65,6 +65,132 @@ __global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
   }
 }
 
+// The whole sort in one launch, up to kOneMax pairs.  Each block places P
+// consecutive pairs and copies their rows.  It counts all the keys for itself
+// (LDS histogram; the low half of a counter takes every pair, the high half
+// those before the block's own), scans the counts over the experts, ranks its
+// pairs among themselves by ballots and adds the three.  The row of a wave's
+// first pair is on its way meanwhile.
+constexpr int kOneMax = 65535;
+constexpr int kOneThreads = 1024;
+struct __attribute__((packed, aligned(4))) Key4 { int32_t v[4]; };
+
+template <int TYPE, int VN>
+__global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
+    const typename El<TYPE>::raw* __restrict__ x, const int32_t* __restrict__ idx, int n, int k, int d, int E, int P,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ pair_ids, int32_t* __restrict__ row_of,
+    typename El<TYPE>::raw* __restrict__ out) {
+  constexpr int kA = 4;                         // pieces a lane holds ahead
+  __shared__ uint32_t cnt[1024];                // counts, then the next free row of each expert
+  __shared__ uint32_t wsum[16];
+  __shared__ int place[128];                    // P <= 128
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int first = blockIdx.x * P;
+  const int mine = n - first < P ? n - first : P;
+  const int pieces = (d + VN - 1) / VN;
+  Vec<TYPE, VN> ahead[kA];
+  if (wave < mine) {
+    const typename El<TYPE>::raw* src = x + (size_t)((first + wave) / k) * d;
+#pragma unroll
+    for (int u = 0; u < kA; ++u)
+      if (64 * u < pieces) ahead[u] = vec_load<TYPE, VN>(src + piece_start<VN>(lane + 64 * u < pieces ? lane + 64 * u : pieces - 1, d));
+  }
+  if (tid < E) cnt[tid] = 0;
+  __syncthreads();
+  auto count = [&](int j, int key) {
+    if (key >= 0 && key < E) atomicAdd(&cnt[key], j < first ? 0x10001u : 1u);
+  };
+  constexpr int kQ = 4;                         // loads in flight
+  const int quads = n >> 2;
+  for (int q0 = tid; q0 < quads; q0 += kQ * kOneThreads) {
+    Key4 v[kQ];
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int q = q0 + u * kOneThreads;
+      v[u] = *reinterpret_cast<const Key4*>(idx + 4 * (q < quads ? q : q0));
+    }
+#pragma unroll
+    for (int u = 0; u < kQ; ++u) {
+      const int q = q0 + u * kOneThreads;
+      if (q < quads) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) count(4 * q + j, v[u].v[j]);
+      }
+    }
+  }
+  if (tid < (n & 3)) count(4 * quads + tid, idx[4 * quads + tid]);
+  int key = -1;
+  if (wave == 0 && lane < mine) key = idx[first + lane];
+  __syncthreads();
+  const uint32_t c = tid < E ? cnt[tid] : 0;
+  uint32_t incl = c & 0xFFFFu;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint32_t v = __shfl_up(incl, s, 64);
+    if (lane >= s) incl += v;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  uint32_t before = 0;
+  for (int q = 0; q < wave; ++q) before += wsum[q];
+  if (tid < E) {
+    const uint32_t lo = before + incl - (c & 0xFFFFu);
+    cnt[tid] = lo + (c >> 16);
+    if (blockIdx.x == 0) {
+      offsets[tid] = (int32_t)lo;
+      if (tid == E - 1) offsets[E] = (int32_t)(before + incl);
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const int nb = 32 - __clz(E > 1 ? E - 1 : 1);
+    for (int b0 = 0; b0 < mine; b0 += 64) {
+      if (b0 > 0) key = b0 + lane < mine ? idx[first + b0 + lane] : -1;
+      const bool valid = key >= 0 && key < E;
+      uint64_t peers = __ballot(valid);
+      for (int b = 0; b < nb; ++b) {
+        const uint64_t on = __ballot((key >> b) & 1);
+        peers &= ((key >> b) & 1) ? on : ~on;
+      }
+      const int rank = __popcll(peers & ((1ull << lane) - 1));
+      int row = -1;
+      if (valid) row = (int)cnt[key] + rank;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (valid && rank == 0) cnt[key] += (uint32_t)__popcll(peers);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (b0 + lane < mine) {
+        place[b0 + lane] = row;
+        row_of[first + b0 + lane] = row;
+        if (valid) pair_ids[row] = first + b0 + lane;
+      }
+    }
+  }
+  __syncthreads();
+  for (int q = wave; q < mine; q += kOneThreads / 64) {
+    const int row = __builtin_amdgcn_readfirstlane(place[q]);
+    const typename El<TYPE>::raw* src = x + (size_t)((first + q) / k) * d;
+    typename El<TYPE>::raw* dst = out + (size_t)(row < 0 ? 0 : row) * d;
+    for (int c0 = 0; c0 < pieces; c0 += 64 * kA) {
+      if (q != wave || c0 > 0) {
+#pragma unroll
+        for (int u = 0; u < kA; ++u) {
+          const int p = c0 + 64 * u + lane;
+          if (c0 + 64 * u < pieces) ahead[u] = vec_load<TYPE, VN>(src + piece_start<VN>(p < pieces ? p : pieces - 1, d));
+        }
+      }
+      if (row < 0) break;
+#pragma unroll
+      for (int u = 0; u < kA; ++u) {
+        const int p = c0 + 64 * u + lane;
+        if (p < pieces) vec_store<TYPE, VN>(dst + piece_start<VN>(p, d), ahead[u]);
+      }
+    }
+  }
+}
+
 // One wave per (token, 64 pieces of its row): kB ranks' rows in flight, summed
 // in rank order.  WEIGHTED = false: the gradient of the sort (w = 1, no shared
 // rows).
@@ -73,7 +199,7 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(
     const typename El<TYPE>::raw* __restrict__ rows, const int32_t* __restrict__ row_of, const float* __restrict__ w,
     const typename El<TYPE>::raw* __restrict__ shared, const float* __restrict__ sgate, long T, int k, int d,
     typename El<TYPE>::raw* __restrict__ y) {
-  constexpr int kB = 8;
+  constexpr int kB = 12;
   const int lane = threadIdx.x & 63;
   const int pieces = (d + VN - 1) / VN;
   const int slabs = (pieces + 63) / 64;
@@ -96,7 +222,7 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(
         const int row = row_of[i];
         has[u] = r0 + u < k && row >= 0 && row < n;
         wv[u] = WEIGHTED ? w[i] : 1.f;
-        v[u] = vec_load<TYPE, VN>(rows + (size_t)(has[u] ? row : 0) * d + e);
+        if (has[u]) v[u] = vec_load<TYPE, VN>(rows + (size_t)row * d + e);
       }
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
@@ -252,11 +378,21 @@ extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d
   MOE_CHECK(x && idx && x_sorted && pair_ids && row_of && ws);
   MOE_CHECK(aligned(x, es) && aligned(x_sorted, es) && aligned(ws, 256));
   MOE_CHECK(aligned(idx, 4) && aligned(offsets, 4) && aligned(pair_ids, 4) && aligned(row_of, 4));
+  const long n = (long)T * k;
   Carver c(ws, ws_bytes);
   SortWs w;
   if (!carve_sort(c, T, k, E, &w)) return MOE_ERR_INVALID_ARG;
+  if (n <= kOneMax) {
+    const int P = n <= 4096 ? 16 : n <= 8192 ? 32 : n <= 16384 ? 64 : 128;
+    return by_type(type, d, [&](auto ty, auto vn) -> int {
+      typedef typename El<decltype(ty)::v>::raw raw;
+      sort_one_kernel<decltype(ty)::v, decltype(vn)::v><<<(unsigned)((n + P - 1) / P), kOneThreads, 0, s>>>(
+          static_cast<const raw*>(x), idx, (int)n, k, d, E, P, offsets, pair_ids, row_of, static_cast<raw*>(x_sorted));
+      MOE_HIP(hipGetLastError());
+      return MOE_OK;
+    });
+  }
   MOE_TRY(bucket_launch(idx, T, k, E, w.counts, offsets, pair_ids, w.bucket, w.bucket_bytes, s, nullptr));
-  const long n = (long)T * k;
   return by_type(type, d, [&](auto ty, auto vn) -> int {
     typedef typename El<decltype(ty)::v>::raw raw;
     gather_rows_kernel<decltype(ty)::v, decltype(vn)::v><<<wave_grid(n), 64 * kWaves, 0, s>>>(
