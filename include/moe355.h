@@ -471,7 +471,7 @@ int moe_chain_forward(const moe_layer_desc* layers, int32_t L, float eps,
  * training): the token rows themselves in expert order, the way back with the
  * routing weights, and the gradients of both.  Rows are row-major [.][d] of one
  * element type (MOE_TYPE_*), any d >= 1 up to 2^20; k <= 1024, E <= 1024,
- * T * k <= 2^30 (MOE_ERR_UNSUPPORTED beyond).  Sums in fp32, in rank order,
+ * T * (k + 1) < 2^31 and T * k <= 2^30 (MOE_ERR_UNSUPPORTED beyond).  Sums in fp32, in rank order,
  * each output rounded once to the element type; no atomics on outputs, so
  * results are reproducible bit for bit.  Outputs must not overlap inputs. */
 enum {

@@ -13,7 +13,7 @@ namespace moe {
 
 inline int type_size(int t) { return t == MOE_TYPE_F32 ? 4 : (t == MOE_TYPE_BF16 || t == MOE_TYPE_F16) ? 2 : 0; }
 
-struct __attribute__((packed, aligned(2))) Piece16 { uint32_t v[4]; };
+typedef uint32_t Piece16 __attribute__((ext_vector_type(4), aligned(2)));
 
 // El<type>: kN elements of a 16-byte piece; rounding to nearest even, NaN kept.
 template <int TYPE> struct El;
@@ -40,14 +40,15 @@ template <> struct El<MOE_TYPE_F16> {
 template <int TYPE, int VN> struct Vec {
   typename El<TYPE>::raw e[VN];
 };
-template <int TYPE, int VN>
+// ONCE: read a single time (kept out of the way of what the caches hold).
+template <int TYPE, int VN, bool ONCE = false>
 __device__ __forceinline__ Vec<TYPE, VN> vec_load(const typename El<TYPE>::raw* p) {
   Vec<TYPE, VN> r;
   if constexpr (VN == 1) {
     r.e[0] = p[0];
   } else {
-    const Piece16 q = *reinterpret_cast<const Piece16*>(p);
-    r = __builtin_bit_cast(Vec<TYPE, VN>, q);
+    const Piece16* q = reinterpret_cast<const Piece16*>(p);
+    r = __builtin_bit_cast(Vec<TYPE, VN>, ONCE ? __builtin_nontemporal_load(q) : *q);
   }
   return r;
 }

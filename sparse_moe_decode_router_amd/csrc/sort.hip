@@ -29,6 +29,7 @@ template <int VN> __device__ __forceinline__ int piece_start(int c, int d) {
 
 constexpr int kWaves = 4;                       // waves a block
 constexpr unsigned kMaxBlocks = 1u << 22;       // blocks go round past this
+constexpr long kMaxItems = (1l << 31) - 1;      // waves' work items, counted in 32 bits
 
 inline unsigned wave_grid(long waves) {
   const long b = (waves + kWaves - 1) / kWaves;
@@ -69,8 +70,8 @@ __global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
 // consecutive pairs and copies their rows.  It counts all the keys for itself
 // (LDS histogram; the low half of a counter takes every pair, the high half
 // those before the block's own), scans the counts over the experts, ranks its
-// pairs among themselves by ballots and adds the three.  The row of a wave's
-// first pair is on its way meanwhile.
+// pairs among themselves by ballots and adds the three.  The first row of each
+// wave is on its way meanwhile.
 constexpr int kOneMax = 65535;
 constexpr int kOneThreads = 1024;
 struct __attribute__((packed, aligned(4))) Key4 { int32_t v[4]; };
@@ -83,19 +84,25 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
   constexpr int kA = 4;                         // pieces a lane holds ahead
   __shared__ uint32_t cnt[1024];                // counts, then the next free row of each expert
   __shared__ uint32_t wsum[16];
-  __shared__ int place[128];                    // P <= 128
+  __shared__ int place[256];                    // P <= 256
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int first = blockIdx.x * P;
   const int mine = n - first < P ? n - first : P;
   const int pieces = (d + VN - 1) / VN;
+  // a wave's pairs: consecutive ones, so that those of one token share a load
+  const int per = (mine + kOneThreads / 64 - 1) / (kOneThreads / 64);
+  const int q0 = wave * per, q1 = q0 + per < mine ? q0 + per : mine;
   Vec<TYPE, VN> ahead[kA];
-  if (wave < mine) {
-    const typename El<TYPE>::raw* src = x + (size_t)((first + wave) / k) * d;
+  auto load = [&](int t, int c0) {
+    const typename El<TYPE>::raw* src = x + (size_t)t * d;
 #pragma unroll
-    for (int u = 0; u < kA; ++u)
-      if (64 * u < pieces) ahead[u] = vec_load<TYPE, VN>(src + piece_start<VN>(lane + 64 * u < pieces ? lane + 64 * u : pieces - 1, d));
-  }
+    for (int u = 0; u < kA; ++u) {
+      const int p = c0 + 64 * u + lane;
+      if (c0 + 64 * u < pieces) ahead[u] = vec_load<TYPE, VN>(src + piece_start<VN>(p < pieces ? p : pieces - 1, d));
+    }
+  };
+  if (q0 < q1) load((first + q0) / k, 0);
   if (tid < E) cnt[tid] = 0;
   __syncthreads();
   auto count = [&](int j, int key) {
@@ -169,19 +176,14 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
     }
   }
   __syncthreads();
-  for (int q = wave; q < mine; q += kOneThreads / 64) {
-    const int row = __builtin_amdgcn_readfirstlane(place[q]);
-    const typename El<TYPE>::raw* src = x + (size_t)((first + q) / k) * d;
-    typename El<TYPE>::raw* dst = out + (size_t)(row < 0 ? 0 : row) * d;
-    for (int c0 = 0; c0 < pieces; c0 += 64 * kA) {
-      if (q != wave || c0 > 0) {
-#pragma unroll
-        for (int u = 0; u < kA; ++u) {
-          const int p = c0 + 64 * u + lane;
-          if (c0 + 64 * u < pieces) ahead[u] = vec_load<TYPE, VN>(src + piece_start<VN>(p < pieces ? p : pieces - 1, d));
-        }
-      }
-      if (row < 0) break;
+  for (int c0 = 0; c0 < pieces; c0 += 64 * kA) {
+    int held = c0 == 0 && q0 < q1 ? (first + q0) / k : -1;
+    for (int q = q0; q < q1; ++q) {
+      const int row = __builtin_amdgcn_readfirstlane(place[q]);
+      const int t = (first + q) / k;
+      if (row < 0) continue;
+      if (t != held) load(held = t, c0);
+      typename El<TYPE>::raw* dst = out + (size_t)row * d;
 #pragma unroll
       for (int u = 0; u < kA; ++u) {
         const int p = c0 + 64 * u + lane;
@@ -191,58 +193,77 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
   }
 }
 
-// One wave per (token, 64 pieces of its row): kB ranks' rows in flight, summed
-// in rank order.  WEIGHTED = false: the gradient of the sort (w = 1, no shared
-// rows).
-template <int TYPE, int VN, bool WEIGHTED>
+// One wave per (token, PP x 64 pieces of its row): the rows of kB ranks in
+// flight, summed in rank order.  WEIGHTED = false: the gradient of the sort
+// (w = 1, no shared rows).  HBM-bound; each row is read once, so past the
+// caches' replacement: 168 MB of rows, us: 38.2 with ordinary loads, 33.6 so,
+// 31 so with PP = 4 (5.9 TB/s of a row's 4 KB in one wave).  Fewer tokens than
+// kWideTokens take PP = 1, for more waves (64 tokens: 7.4 against 9.4).
+constexpr int kWideTokens = 1024;
+template <int TYPE, int VN, int PP, bool WEIGHTED>
 __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(
     const typename El<TYPE>::raw* __restrict__ rows, const int32_t* __restrict__ row_of, const float* __restrict__ w,
-    const typename El<TYPE>::raw* __restrict__ shared, const float* __restrict__ sgate, long T, int k, int d,
+    const typename El<TYPE>::raw* __restrict__ shared, const float* __restrict__ sgate, int T, int k, int d,
     typename El<TYPE>::raw* __restrict__ y) {
-  constexpr int kB = 12;
+  constexpr int kB = PP == 1 ? 10 : 4;
   const int lane = threadIdx.x & 63;
   const int pieces = (d + VN - 1) / VN;
-  const int slabs = (pieces + 63) / 64;
-  const long n = T * k;
-  for (long item = wave_id(); item < T * slabs; item += wave_count()) {
-    const long t = item / slabs;
-    const int c = (int)(item - t * slabs) * 64 + lane;
-    if (c >= pieces) continue;
-    const int e = piece_start<VN>(c, d);
-    float acc[VN];
+  const unsigned slabs = (unsigned)(pieces + 64 * PP - 1) / (64 * PP);
+  const long n = (long)T * k;
+  for (unsigned item = (unsigned)wave_id(); item < (unsigned)T * slabs; item += (unsigned)wave_count()) {
+    const int t = (int)(item / slabs);
+    const int c0 = (int)(item % slabs) * 64 * PP + lane;
+    int e[PP];
+    bool mine[PP];
 #pragma unroll
-    for (int j = 0; j < VN; ++j) acc[j] = 0.f;
+    for (int p = 0; p < PP; ++p) {
+      mine[p] = c0 + 64 * p < pieces;
+      e[p] = piece_start<VN>(mine[p] ? c0 + 64 * p : pieces - 1, d);
+    }
+    float acc[PP][VN];
+#pragma unroll
+    for (int p = 0; p < PP; ++p)
+#pragma unroll
+      for (int j = 0; j < VN; ++j) acc[p][j] = 0.f;
     for (int r0 = 0; r0 < k; r0 += kB) {
-      Vec<TYPE, VN> v[kB];
+      Vec<TYPE, VN> v[kB][PP];
       float wv[kB];
       bool has[kB];
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
-        const long i = t * k + (r0 + u < k ? r0 + u : k - 1);
+        const long i = (long)t * k + (r0 + u < k ? r0 + u : k - 1);
         const int row = row_of[i];
         has[u] = r0 + u < k && row >= 0 && row < n;
         wv[u] = WEIGHTED ? w[i] : 1.f;
-        if (has[u]) v[u] = vec_load<TYPE, VN>(rows + (size_t)row * d + e);
+        const typename El<TYPE>::raw* src = rows + (size_t)(has[u] ? row : 0) * d;
+#pragma unroll
+        for (int p = 0; p < PP; ++p) v[u][p] = vec_load<TYPE, VN, true>(src + e[p]);
       }
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
         if (has[u]) {
 #pragma unroll
-          for (int j = 0; j < VN; ++j)
-            acc[j] = WEIGHTED ? fmaf(wv[u], El<TYPE>::up(v[u].e[j]), acc[j]) : acc[j] + El<TYPE>::up(v[u].e[j]);
+          for (int p = 0; p < PP; ++p)
+#pragma unroll
+            for (int j = 0; j < VN; ++j)
+              acc[p][j] = WEIGHTED ? fmaf(wv[u], El<TYPE>::up(v[u][p].e[j]), acc[p][j])
+                                   : acc[p][j] + El<TYPE>::up(v[u][p].e[j]);
         }
       }
     }
-    if (WEIGHTED && shared) {
-      const float s = sgate[t];
-      const Vec<TYPE, VN> v = vec_load<TYPE, VN>(shared + (size_t)t * d + e);
 #pragma unroll
-      for (int j = 0; j < VN; ++j) acc[j] = fmaf(s, El<TYPE>::up(v.e[j]), acc[j]);
+    for (int p = 0; p < PP; ++p) {
+      if (WEIGHTED && shared) {
+        const float s = sgate[t];
+        const Vec<TYPE, VN> v = vec_load<TYPE, VN, true>(shared + (size_t)t * d + e[p]);
+#pragma unroll
+        for (int j = 0; j < VN; ++j) acc[p][j] = fmaf(s, El<TYPE>::up(v.e[j]), acc[p][j]);
+      }
+      Vec<TYPE, VN> o;
+#pragma unroll
+      for (int j = 0; j < VN; ++j) o.e[j] = El<TYPE>::down(acc[p][j]);
+      if (mine[p]) vec_store<TYPE, VN>(y + (size_t)t * d + e[p], o);
     }
-    Vec<TYPE, VN> o;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) o.e[j] = El<TYPE>::down(acc[j]);
-    vec_store<TYPE, VN>(y + (size_t)t * d + e, o);
   }
 }
 
@@ -252,17 +273,17 @@ template <int TYPE, int VN>
 __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(
     const typename El<TYPE>::raw* __restrict__ dy, const typename El<TYPE>::raw* __restrict__ rows,
     const int32_t* __restrict__ row_of, const float* __restrict__ w, const typename El<TYPE>::raw* __restrict__ shared,
-    const float* __restrict__ sgate, long T, int k, int d, typename El<TYPE>::raw* __restrict__ drows,
+    const float* __restrict__ sgate, int T, int k, int d, typename El<TYPE>::raw* __restrict__ drows,
     float* __restrict__ dw, typename El<TYPE>::raw* __restrict__ dshared, float* __restrict__ dsgate) {
   constexpr int kB = 4;
   const int lane = threadIdx.x & 63;
   const int pieces = (d + VN - 1) / VN;
   const int per = k + (shared ? 1 : 0);
-  const long n = T * k;
-  for (long item = wave_id(); item < T * per; item += wave_count()) {
-    const long t = item / per;
-    const int r = (int)(item - t * per);
-    const long i = t * k + r;
+  const long n = (long)T * k;
+  for (unsigned item = (unsigned)wave_id(); item < (unsigned)T * (unsigned)per; item += (unsigned)wave_count()) {
+    const int t = (int)(item / (unsigned)per);
+    const int r = (int)(item % (unsigned)per);
+    const long i = (long)t * k + r;
     const typename El<TYPE>::raw* src;
     typename El<TYPE>::raw* dst;
     float f;
@@ -288,7 +309,7 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(
       for (int u = 0; u < kB; ++u) {
         const int e = piece_start<VN>(c0 + 64 * u < pieces ? c0 + 64 * u : pieces - 1, d);
         a[u] = vec_load<TYPE, VN>(g + e);
-        b[u] = vec_load<TYPE, VN>(src + e);
+        b[u] = vec_load<TYPE, VN, true>(src + e);
       }
 #pragma unroll
       for (int u = 0; u < kB; ++u) {
@@ -347,7 +368,7 @@ __global__ void zero_i32_kernel(int32_t* p, int n) {
 // Sizes every entry point of this file takes.
 int check_rows(int type, int T, int k, int d) {
   MOE_CHECK(type_size(type) != 0 && T >= 0 && k >= 1 && d >= 1);
-  if (k > 1024 || d > (1 << 20) || (long)T * k > (1L << 30)) return MOE_ERR_UNSUPPORTED;
+  if (k > 1024 || d > (1 << 20) || (long)T * k > (1L << 30) || (long)T * (k + 1) > kMaxItems) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -383,7 +404,8 @@ extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d
   SortWs w;
   if (!carve_sort(c, T, k, E, &w)) return MOE_ERR_INVALID_ARG;
   if (n <= kOneMax) {
-    const int P = n <= 4096 ? 16 : n <= 8192 ? 32 : n <= 16384 ? 64 : 128;
+    // pairs a block: a block for each of the 256 CUs, 16 pairs (one a wave) at least
+    const int P = n <= 16 * 256 ? 16 : (int)((n + 255) / 256);
     return by_type(type, d, [&](auto ty, auto vn) -> int {
       typedef typename El<decltype(ty)::v>::raw raw;
       sort_one_kernel<decltype(ty)::v, decltype(vn)::v><<<(unsigned)((n + P - 1) / P), kOneThreads, 0, s>>>(
@@ -410,10 +432,15 @@ int unsort_launch(const void* rows, int type, int T, int k, int d, const int32_t
   return by_type(type, d, [&](auto ty, auto vn) -> int {
     constexpr int VN = decltype(vn)::v;
     typedef typename El<decltype(ty)::v>::raw raw;
-    const long slabs = ((d + VN - 1) / VN + 63) / 64;
-    unsort_kernel<decltype(ty)::v, VN, WEIGHTED><<<wave_grid(T * slabs), 64 * kWaves, 0, s>>>(
-        static_cast<const raw*>(rows), row_of, w, static_cast<const raw*>(shared), sgate, T, k, d,
-        static_cast<raw*>(y));
+    constexpr int PP = VN == 1 ? 1 : 4;
+    const long pieces = (d + VN - 1) / VN;
+    const bool wide = PP > 1 && T >= kWideTokens && pieces > 128;
+    const long items = T * ((pieces + (wide ? 64 * PP : 64) - 1) / (wide ? 64 * PP : 64));
+    if (items > kMaxItems) return MOE_ERR_UNSUPPORTED;
+    auto* kernel = wide ? unsort_kernel<decltype(ty)::v, VN, PP, WEIGHTED> : unsort_kernel<decltype(ty)::v, VN, 1, WEIGHTED>;
+    kernel<<<wave_grid(items), 64 * kWaves, 0, s>>>(static_cast<const raw*>(rows), row_of, w,
+                                                    static_cast<const raw*>(shared), sgate, T, k, d,
+                                                    static_cast<raw*>(y));
     MOE_HIP(hipGetLastError());
     return MOE_OK;
   });
