@@ -40,9 +40,9 @@ MOE_PATH_PREFILL = 3
 MOE_PATH_PREFILL_TILED = 4
 MOE_PATH_PREFILL_STREAM = 5
 
-if not os.path.exists(LIB_PATH):
+if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_HERE, "_rowops.so")):
     raise ImportError(
-        f"libmoe355.so not built at {LIB_PATH}; run "
+        f"libmoe355.so or _rowops.so not built at {LIB_PATH}, {_HERE}; run "
         "`python sparse_moe_decode_router_amd/build.py` (the HIP library is required; "
         "there is no CPU fallback)")
 
@@ -54,6 +54,8 @@ if not os.path.exists(LIB_PATH):
 import torch  # noqa: E402,F401
 
 _lib = C.CDLL(LIB_PATH)
+
+from . import _rowops  # noqa: E402  (built beside the library)
 
 
 class moe_ffn_shape(C.Structure):
@@ -671,57 +673,33 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 # ------------------------------------------- rows in expert order, and back
 # These entry points check their tensors (ValueError), run on the tensors'
 # device whatever the current one, and allocate what they return on the
-# stream that they launch on.
-_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
-
-
-# the current stream's handle without a stream object: 0.1 against 1.1 us of a call
+# stream that they launch on.  The checks and the call itself are in
+# csrc/binding.cpp.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_rowops.bind(*(C.cast(getattr(_lib, _n), C.c_void_p).value for _n in (
+    "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_combine",
+    "moe_unsort_combine_backward", "moe_linear_bytes", "moe_linear_int4", "moe_expert_linear_int4",
+    "moe_pool_linear_int4", "moe_router_topk_backward")))
 
 
 def _elsewhere(x, stream):
     """None where tensor x is on the current device and no stream is named; else a context that makes its device
     and the stream current."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("device tensors wanted")
+        raise ValueError("a device tensor is wanted")
     dev = x.get_device()
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError("the stream is of another device than the tensors")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+    if stream is None:
+        return None if _current_device() == dev else torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError("the stream is of another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
-def _need(t, name, dtype, shape, device):
-    """t.data_ptr() of a contiguous device tensor of that type and shape (None passes as None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda:{device} wanted, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
-    return t.data_ptr()
-
-
-def _row_type(x, name, dims=2):
-    if x.dim() != dims or x.dtype not in _TYPES:
-        raise ValueError(f"{name}: a {dims}-d tensor of float32, bfloat16 or float16 wanted, got {x.dtype} "
-                         f"{tuple(x.shape)}")
-    return _TYPES[x.dtype]
-
-
-def _given(t, name):
-    if t is None:
-        raise ValueError(f"{name} is wanted")
-    return t
-
-
-def _scratch(workspace, nbytes, device):
-    """A workspace that needs no fill: the caller's (uint8) or a new one."""
-    if workspace is None:
-        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=f"cuda:{device}")
-    if workspace.get_device() != device or not workspace.is_contiguous() or workspace.dtype is not torch.uint8:
-        raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{device} wanted")
-    return workspace
+def _matrix(x, name):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name}: a 2-d device tensor is wanted")
+    return x.shape
 
 
 def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
@@ -733,100 +711,73 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
     Returns (x_sorted [T*k, d], offsets int32 [E+1], pair_ids int32 [T*k],
     row_of int32 [T, k]); rows of x_sorted and entries of pair_ids from
     offsets[E] on keep what they held (out: that tuple, to write into)."""
-    ty = _row_type(x, "x")
-    T, d = x.shape
-    k = _given(topk_idx, "topk_idx").shape[-1]
-    n = T * k
     away = _elsewhere(x, stream)
     if away is not None:
         with away:
             return moe_sort_tokens(x, topk_idx, E, workspace, out)
-    dev = x.get_device()
-    if out is None:
-        out = (torch.empty((n, d), dtype=x.dtype, device=x.device),
-               torch.empty((E + 1,), dtype=torch.int32, device=x.device),
-               torch.empty((n,), dtype=torch.int32, device=x.device),
-               torch.empty((T, k), dtype=torch.int32, device=x.device))
+    if out is None or workspace is None:
+        (T, d), k = _matrix(x, "x"), _matrix(topk_idx, "topk_idx")[1]
+        if out is None:
+            i32 = dict(dtype=torch.int32, device=x.device)
+            out = (torch.empty((T * k, d), dtype=x.dtype, device=x.device), torch.empty((max(E, 0) + 1,), **i32),
+                   torch.empty((T * k,), **i32), torch.empty((T, k), **i32))
+        if workspace is None:
+            workspace = torch.empty(moe_sort_workspace_bytes(T, k, E), dtype=torch.uint8, device=x.device)
     rows, offsets, pairs, row_of = out
-    if workspace is None:
-        workspace = _scratch(None, moe_sort_workspace_bytes(T, k, E), dev)
-    else:
-        _scratch(workspace, 0, dev)
-    _check(_lib.moe_sort_tokens(
-        _need(x, "x", x.dtype, (T, d), dev), ty, T, d, _need(topk_idx, "topk_idx", torch.int32, (T, k), dev), k, E,
-        _need(rows, "x_sorted", x.dtype, (n, d), dev), _need(offsets, "offsets", torch.int32, (E + 1,), dev),
-        _need(pairs, "pair_ids", torch.int32, (n,), dev), _need(row_of, "row_of", torch.int32, (T, k), dev),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)), "moe_sort_tokens")
-    return rows, offsets, pairs, row_of
+    st = _rowops.sort(x, topk_idx, E, rows, offsets, pairs, row_of, workspace, _raw_stream(x.get_device()))
+    if st:
+        _check(st, "moe_sort_tokens")
+    return out
 
 
 def moe_sort_tokens_backward(dx_sorted, row_of, out=None, stream=None):
     """Gradient of moe_sort_tokens with respect to x: dx [T, d] from dx_sorted [T*k, d]."""
-    ty = _row_type(dx_sorted, "dx_sorted")
-    T, k = _given(row_of, "row_of").shape
-    d = dx_sorted.shape[1]
     away = _elsewhere(dx_sorted, stream)
     if away is not None:
         with away:
             return moe_sort_tokens_backward(dx_sorted, row_of, out)
-    dev = dx_sorted.get_device()
-    dx = torch.empty((T, d), dtype=dx_sorted.dtype, device=dx_sorted.device) if out is None else out
-    _check(_lib.moe_sort_tokens_backward(
-        _need(dx_sorted, "dx_sorted", dx_sorted.dtype, (T * k, d), dev), ty, T, k, d,
-        _need(row_of, "row_of", torch.int32, (T, k), dev), _need(dx, "out", dx_sorted.dtype, (T, d), dev), _raw_stream(dev)),
-        "moe_sort_tokens_backward")
-    return dx
+    if out is None:
+        out = torch.empty((_matrix(row_of, "row_of")[0], _matrix(dx_sorted, "dx_sorted")[1]), dtype=dx_sorted.dtype,
+                          device=dx_sorted.device)
+    st = _rowops.sort_grad(dx_sorted, row_of, out, _raw_stream(dx_sorted.get_device()))
+    if st:
+        _check(st, "moe_sort_tokens_backward")
+    return out
 
 
 def moe_unsort_combine(rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
     """y [T, d] = sum over a token's pairs of topk_w * rows[row_of], plus
     shared_gate * shared_out; rows [T*k, d], y and shared_out [T, d] of one type."""
-    ty = _row_type(rows, "rows")
-    T, k = _given(row_of, "row_of").shape
-    d, t = rows.shape[1], rows.dtype
     away = _elsewhere(rows, stream)
     if away is not None:
         with away:
             return moe_unsort_combine(rows, row_of, topk_w, shared_out, shared_gate, out)
-    dev = rows.get_device()
-    y = torch.empty((T, d), dtype=t, device=rows.device) if out is None else out
-    _check(_lib.moe_unsort_combine(
-        _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d, _need(row_of, "row_of", torch.int32, (T, k), dev),
-        _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
-        _need(shared_out, "shared_out", t, (T, d), dev),
-        _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(y, "out", t, (T, d), dev), _raw_stream(dev)),
-        "moe_unsort_combine")
-    return y
+    if out is None:
+        out = torch.empty((_matrix(row_of, "row_of")[0], _matrix(rows, "rows")[1]), dtype=rows.dtype,
+                          device=rows.device)
+    st = _rowops.unsort(rows, row_of, topk_w, shared_out, shared_gate, out, _raw_stream(rows.get_device()))
+    if st:
+        _check(st, "moe_unsort_combine")
+    return out
 
 
 def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
     """Gradients of moe_unsort_combine from dy [T, d]: (drows [T*k, d], dtopk_w
     fp32 [T, k], dshared_out [T, d], dshared_gate fp32 [T]), the last two None
     without shared rows; rows of drows that no pair has keep what they held."""
-    ty = _row_type(rows, "rows")
-    T, k = _given(row_of, "row_of").shape
-    d, t = rows.shape[1], rows.dtype
     away = _elsewhere(rows, stream)
     if away is not None:
         with away:
             return moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out, shared_gate, out)
-    dev = rows.get_device()
     if out is None:
-        has = shared_out is not None
-        out = (torch.empty((T * k, d), dtype=t, device=rows.device),
-               torch.empty((T, k), dtype=torch.float32, device=rows.device),
-               torch.empty((T, d), dtype=t, device=rows.device) if has else None,
+        (T, k), has = _matrix(row_of, "row_of"), shared_out is not None
+        out = (torch.empty_like(rows), torch.empty((T, k), dtype=torch.float32, device=rows.device),
+               torch.empty_like(shared_out) if has else None,
                torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
-    drows, dw, dsh, dsg = out
-    _check(_lib.moe_unsort_combine_backward(
-        _need(_given(dy, "dy"), "dy", t, (T, d), dev), _need(rows, "rows", t, (T * k, d), dev), ty, T, k, d,
-        _need(row_of, "row_of", torch.int32, (T, k), dev),
-        _need(_given(topk_w, "topk_w"), "topk_w", torch.float32, (T, k), dev),
-        _need(shared_out, "shared_out", t, (T, d), dev),
-        _need(shared_gate, "shared_gate", torch.float32, (T,), dev), _need(drows, "drows", t, (T * k, d), dev),
-        _need(dw, "dtopk_w", torch.float32, (T, k), dev), _need(dsh, "dshared_out", t, (T, d), dev),
-        _need(dsg, "dshared_gate", torch.float32, (T,), dev), _raw_stream(dev)), "moe_unsort_combine_backward")
-    return drows, dw, dsh, dsg
+    st = _rowops.unsort_grad(dy, rows, row_of, topk_w, shared_out, shared_gate, *out, _raw_stream(rows.get_device()))
+    if st:
+        _check(st, "moe_unsort_combine_backward")
+    return out
 
 
 # ----------------------------------------------------------- 4-bit products
@@ -865,19 +816,16 @@ def moe_unpack_linear_int4(packed: np.ndarray, n_in: int, n_out: int, group: int
 
 def moe_linear_int4(packed, x, n_out: int, group: int = 64, out=None, stream=None):
     """y fp32 [T, n_out] = x W^T; x bf16 [T, n_in], packed uint8 [moe_linear_bytes]."""
-    T, n_in = x.shape
-    sh = moe_linear_shape(n_in, n_out, group)
     away = _elsewhere(x, stream)
     if away is not None:
         with away:
             return moe_linear_int4(packed, x, n_out, group, out)
-    dev = x.get_device()
-    y = torch.empty((T, n_out), dtype=torch.float32, device=x.device) if out is None else out
-    _check(_lib.moe_linear_int4(
-        C.byref(sh), _need(packed, "packed", torch.uint8, (int(_lib.moe_linear_bytes(C.byref(sh))),), dev),
-        _need(x, "x", torch.bfloat16, (T, n_in), dev), T, _need(y, "out", torch.float32, (T, n_out), dev), _raw_stream(dev)),
-        "moe_linear_int4")
-    return y
+    if out is None:
+        out = torch.empty((_matrix(x, "x")[0], n_out), dtype=torch.float32, device=x.device)
+    st = _rowops.linear(packed, x, n_out, group, out, _raw_stream(x.get_device()))
+    if st:
+        _check(st, "moe_linear_int4")
+    return out
 
 
 def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, group: int = 64, error=None, out=None,
@@ -887,28 +835,17 @@ def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, gr
     [n_slots, bytes] (rows may be apart: a view into larger blobs), slot_table
     int32 [E] or None (expert e in slot e); error: int32 [1] or None.  Rows
     from offsets[E] on keep what they held."""
-    N, n_in = x_sorted.shape
-    sh = moe_linear_shape(n_in, n_out, group)
-    if packed.dim() != 2 or packed.dtype is not torch.uint8 or packed.stride(1) != 1 \
-            or packed.shape[1] < int(_lib.moe_linear_bytes(C.byref(sh))):
-        raise ValueError(f"packed: a uint8 tensor [n_slots, {moe_linear_bytes(n_in, n_out, group)}] wanted, got "
-                         f"{packed.dtype} {tuple(packed.shape)}")
     away = _elsewhere(x_sorted, stream)
     if away is not None:
         with away:
             return moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out, group, error, out)
-    dev = x_sorted.get_device()
-    if packed.get_device() != dev:
-        raise ValueError(f"packed: a tensor on cuda:{dev} wanted")
-    E = offsets.shape[0] - 1
-    y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
-    _check(_lib.moe_expert_linear_int4(
-        C.byref(sh), packed.data_ptr(), packed.stride(0), packed.shape[0],
-        _need(slot_table, "slot_table", torch.int32, (E,), dev), E,
-        _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
-        _need(offsets, "offsets", torch.int32, (E + 1,), dev), _need(y, "out", torch.float32, (N, n_out), dev),
-        _need(error, "error", torch.int32, (1,), dev), _raw_stream(dev)), "moe_expert_linear_int4")
-    return y
+    if out is None:
+        out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
+    st = _rowops.expert_linear(packed, slot_table, x_sorted, offsets, n_out, group, out, error,
+                               _raw_stream(x_sorted.get_device()))
+    if st:
+        _check(st, "moe_expert_linear_int4")
+    return out
 
 
 def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, stream=None):
@@ -916,18 +853,17 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
     if matrix not in _MATS:
         raise ValueError(f"matrix must be one of {_MATS}")
     n_in, n_out = (pool.I, pool.d) if matrix == "down" else (pool.d, pool.I)
-    N = x_sorted.shape[0]
     away = _elsewhere(x_sorted, stream)
     if away is not None:
         with away:
             return moe_pool_linear_int4(pool, matrix, x_sorted, offsets, out)
-    dev = x_sorted.get_device()
-    y = torch.empty((N, n_out), dtype=torch.float32, device=x_sorted.device) if out is None else out
-    _check(_lib.moe_pool_linear_int4(
-        pool.handle, _MATS.index(matrix), _need(x_sorted, "x_sorted", torch.bfloat16, (N, n_in), dev), N,
-        _need(_given(offsets, "offsets"), "offsets", torch.int32, (pool.E + 1,), dev),
-        _need(y, "out", torch.float32, (N, n_out), dev), _raw_stream(dev)), "moe_pool_linear_int4")
-    return y
+    if out is None:
+        out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
+    st = _rowops.pool_linear(pool.handle.value, _MATS.index(matrix), n_in, n_out, pool.E, x_sorted, offsets, out,
+                             _raw_stream(x_sorted.get_device()))
+    if st:
+        _check(st, "moe_pool_linear_int4")
+    return out
 
 
 # ------------------------------------------------------ gradient of the router
@@ -941,31 +877,24 @@ def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w
     dw_router fp32 [E+1, d], dlogit_bias fp32 [E]).  offsets and pair_ids from
     moe_bucket_tokens or moe_sort_tokens on topk_idx; dshared_gate None: no
     gradient.  out: that triple to write into, None for each not wanted."""
-    T, d = x.shape
-    E, k = w_router.shape[0] - 1, topk_idx.shape[1]
-    f32, i32 = torch.float32, torch.int32
     away = _elsewhere(x, stream)
     if away is not None:
         with away:
-            return moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids, workspace, out)
-    dev = x.get_device()
-    if out is None:
-        out = (torch.empty((T, d), dtype=f32, device=x.device), torch.empty((E + 1, d), dtype=f32, device=x.device),
-               torch.empty((E,), dtype=f32, device=x.device))
-    dx, dwr, db = out
-    if workspace is None:
-        workspace = _scratch(None, moe_router_backward_workspace_bytes(T, d, E, k), dev)
-    else:
-        _scratch(workspace, 0, dev)
-    _check(_lib.moe_router_topk_backward(
-        _need(x, "x", torch.bfloat16, (T, d), dev), T, d, _need(w_router, "w_router", f32, (E + 1, d), dev), E, k,
-        _need(topk_idx, "topk_idx", i32, (T, k), dev), _need(topk_w, "topk_w", f32, (T, k), dev),
-        _need(shared_gate, "shared_gate", f32, (T,), dev), _need(dtopk_w, "dtopk_w", f32, (T, k), dev),
-        _need(dshared_gate, "dshared_gate", f32, (T,), dev), _need(offsets, "offsets", i32, (E + 1,), dev),
-        _need(pair_ids, "pair_ids", i32, (T * k,), dev), _need(dx, "dx", f32, (T, d), dev),
-        _need(dwr, "dw_router", f32, (E + 1, d), dev), _need(db, "dlogit_bias", f32, (E,), dev),
-        workspace.data_ptr(), workspace.numel(), _raw_stream(dev)), "moe_router_topk_backward")
-    return dx, dwr, db
+            return moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate,
+                                            offsets, pair_ids, workspace, out)
+    if out is None or workspace is None:
+        (T, d), E, k = _matrix(x, "x"), _matrix(w_router, "w_router")[0] - 1, _matrix(topk_idx, "topk_idx")[1]
+        if out is None:
+            f32 = dict(dtype=torch.float32, device=x.device)
+            out = (torch.empty((T, d), **f32), torch.empty((E + 1, d), **f32), torch.empty((E,), **f32))
+        if workspace is None:
+            workspace = torch.empty(moe_router_backward_workspace_bytes(T, d, E, k), dtype=torch.uint8,
+                                    device=x.device)
+    st = _rowops.router_grad(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids,
+                             *out, workspace, _raw_stream(x.get_device()))
+    if st:
+        _check(st, "moe_router_topk_backward")
+    return out
 
 
 # --------------------------------------------------------- measurement probes
