@@ -12,7 +12,6 @@
 // the running fp32 sum with its own scale.  The offset 16 is the smallest that
 // bf16 allows, which keeps the cancellation between the two terms small.
 #include "internal.h"
-#include "chunks.h"
 #include "device.h"
 
 namespace moe {
@@ -40,6 +39,78 @@ struct LinArgs {
   // one wave each, over `turns` tiles of 16 RT wr rows (1 where wk > 1)
   int32_t wr, wk, turns;
 };
+
+// Inclusive sum over the lanes of a wave (row shifts, then the row totals).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// Sorted rows are cut into chunks of `size` that do not cross an expert's
+// border, numbered in expert order.
+struct RowChunk {
+  bool any;     // false past the last chunk
+  int slot;     // of its expert
+  int start;    // first row
+  int n;        // rows (0..size)
+};
+
+// Chunk j.  Every wave finds its own: borders and slots of all experts in
+// coalesced loads, all in flight at once (lane l holds experts l, l + 64, ..),
+// chunks counted by wave scans of 64 experts.  Offsets that do not describe N
+// rows give no row outside them.
+__device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offsets,
+                                               const int32_t* __restrict__ slot_table, int E, long N, long j,
+                                               int size) {
+  constexpr int kU = 16;                        // E <= 1024
+  const int lane = threadIdx.x & 63;
+  int off[kU + 1], slots[kU];
+#pragma unroll
+  for (int u = 0; u <= kU; ++u) {
+    off[u] = 0;
+    if (u < kU) slots[u] = 64 * u + lane;
+    if (64 * u <= E) {
+      const int e = 64 * u + lane;
+      off[u] = offsets[e < E ? e : E];
+      if (u < kU && slot_table) slots[u] = slot_table[e < E ? e : E - 1];
+    }
+  }
+  RowChunk r{false, 0, 0, 0};
+  int before = 0;                               // chunks of the experts of earlier u
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    if (64 * u < E && !r.any) {
+      // the next lane's border (lane 63: the first of the next 64)
+      const int next = __builtin_amdgcn_update_dpp(__builtin_amdgcn_readlane(off[u + 1], 0), off[u], 0x130, 0xF, 0xF, false);
+      const int rows = 64 * u + 63 < E || lane < E - 64 * u ? next - off[u] : 0;
+      const int c = rows > 0 ? (int)((unsigned)(rows + size - 1) / (unsigned)size) : 0;
+      const int incl = wave_scan(c) + before;
+      const uint64_t past = __ballot((long)incl > j);
+      if (past != 0) {
+        const int owner = __ffsll((unsigned long long)past) - 1;
+        const int skip = ((int)j - __builtin_amdgcn_readlane(incl - c, owner)) * size;
+        const int left = __builtin_amdgcn_readlane(rows, owner) - skip;
+        r = RowChunk{true, __builtin_amdgcn_readlane(slots[u], owner), __builtin_amdgcn_readlane(off[u], owner) + skip,
+                     left < size ? left : size};
+      }
+      before = __builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+  if (r.start < 0 || (long)r.start >= N || r.n < 0) r.start = r.n = 0;
+  if ((long)r.start + r.n > N) r.n = (int)(N - r.start);
+  return r;
+}
+
+// The most chunks that N rows in E buckets can make.
+inline long max_chunks(long N, int E, int size) {
+  const long ne = N < E ? N : E;                // each bucket with rows makes at most one short chunk
+  return ne + (N - ne) / size;
+}
 
 // Eight codes of a word as bf16 16 + q, pairs (q[u], q[u+4]), u = 0..3.
 __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t mask, uint32_t base) {
@@ -91,11 +162,11 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   const uint8_t* w = a.w;
   bool missing = false;
   if (EXP) {
-    const RowChunk rc = find_chunk<false>(a.offsets, a.E, a.N, chunk, 16 * NT, nullptr);
-    if (rc.e < 0) return;                       // past the last chunk
+    const RowChunk rc = find_chunk(a.offsets, a.slot_table, a.E, a.N, chunk, 16 * NT);
+    if (!rc.any) return;                        // past the last chunk
     start = rc.start;
     n = rc.n;
-    const int slot = __builtin_amdgcn_readfirstlane(a.slot_table ? a.slot_table[rc.e] : rc.e);
+    const int slot = rc.slot;
     missing = slot < 0 || slot >= a.n_slots;
     if (missing) {
       if (threadIdx.x == 0 && a.err && n > 0) atomicOr(a.err, 1);
@@ -261,6 +332,7 @@ int launch(LinArgs a, int wk, long likely, hipStream_t s) {
 //                 T = 64: RT 2 13.2, RT 4 11.5   T = 1024: RT 4 94, NT 4 RT 4 76
 //   2048 x 8192   T = 1: RT 2 5.1, RT 1 5.3      T = 64: RT 4 11.5
 //   4096 x 16384  T = 8: RT 2 10.6, RT 4 11.4    T = 16: RT 2 13.2, RT 4 11.9
+//   256 experts of 512 x 2048, 512 rows: RT 4 35.6, RT 2 37.2
 // Inputs are split over the waves of a block (8 shares where blocks are few, 4
 // or none where they are many), which keeps more loads in flight per CU than
 // more steps per wave: 2048 x 2048, T = 1: 4.3 with four shares, 5.1 with two.
@@ -270,7 +342,7 @@ int by_rows(LinArgs a, hipStream_t s) {
   const long t16 = (a.n_out + 15) / 16;
   const auto chunks = [&](int size, bool most) -> long {
     if (!EXP) return (a.N + size - 1) / size;
-    return most ? max_chunks(a.N, a.E, size, false) : (a.N < a.E ? a.N : (rows + size - 1) / size * a.E);
+    return most ? max_chunks(a.N, a.E, size) : (a.N < a.E ? a.N : (rows + size - 1) / size * a.E);
   };
   const long wide = chunks(64, false);
   if (rows > 32 && t16 / 4 * wide >= 256) {
@@ -279,6 +351,7 @@ int by_rows(LinArgs a, hipStream_t s) {
   }
   a.chunks = chunks(16, true);
   const long likely = chunks(16, false), units = t16 * likely;
+  if (EXP && units > 16384) return launch<GROUP, 1, 4, 2, EXP>(a, 1, likely, s);
   if (units > 512 && rows > 8) return launch<GROUP, 1, 4, 2, EXP>(a, units > 8192 ? 1 : units > 1024 ? 4 : 8, likely, s);
   if (units > 256) return launch<GROUP, 1, 2, 2, EXP>(a, units > 16384 ? 1 : units > 1024 ? 4 : 8, likely, s);
   if (a.n_in >= 4096) return launch<GROUP, 1, 1, 4, EXP>(a, 8, likely, s);
