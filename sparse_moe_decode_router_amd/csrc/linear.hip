@@ -38,6 +38,7 @@ struct LinArgs {
   // a block: wr row groups of 16 RT weight rows times wk shares of the inputs,
   // one wave each, over `turns` tiles of 16 RT wr rows (1 where wk > 1)
   int32_t wr, wk, turns;
+  int32_t size;                 // rows a chunk, at most 16 NT
 };
 
 // Inclusive sum over the lanes of a wave (row shifts, then the row totals).
@@ -138,11 +139,12 @@ __device__ __forceinline__ bf16x8_t pair_x(u32x4_t v) {
 // and swaps rows of lanes so that it holds word kb of both, whose inputs are the
 // 16 bytes kb of either half of a 128-byte line of x.  The wk waves that
 // share rows are joined through LDS in order.
-template <int GROUP, int NT, int RT, int U, bool EXP>
+template <int GROUP, int NT, int RT, int U, bool EXP, bool XL>
 __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   constexpr int kStep = GROUP == 32 ? 32 : 64;
   constexpr int kM = kStep / 32;                // matrix instructions a step
-  extern __shared__ float red[];                // [waves][RT][NT][4][64], wk > 1
+  static_assert(!XL || NT == 1, "x in LDS: one tile of tokens");
+  extern __shared__ float red[];                // [waves][RT][NT][4][64] where wk > 1 | XL: x
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wr = wave / a.wk, kq = wave - wr * a.wk;
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   const uint8_t* w = a.w;
   bool missing = false;
   if (EXP) {
-    const RowChunk rc = find_chunk(a.offsets, a.slot_table, a.E, a.N, chunk, 16 * NT);
+    const RowChunk rc = find_chunk(a.offsets, a.slot_table, a.E, a.N, chunk, a.size);
     if (!rc.any) return;                        // past the last chunk
     start = rc.start;
     n = rc.n;
@@ -174,8 +176,8 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
       w += (uint64_t)slot * a.w_stride;
     }
   } else {
-    start = chunk * 16 * NT;
-    n = a.N - start < 16 * NT ? (int)(a.N - start) : 16 * NT;
+    start = chunk * a.size;
+    n = a.N - start < a.size ? (int)(a.N - start) : a.size;
   }
   const uint32_t sb0 = (uint32_t)(a.n_in / 32) * (uint32_t)a.n_out * 16u;
   const rsrc_t mr = make_rsrc(w, sb0 + (uint32_t)(a.n_in / GROUP) * (uint32_t)a.n_out * 4u);
@@ -183,6 +185,25 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   // rows of x past the chunk read zeros from past the end of the buffer
   const rsrc_t xr = make_rsrc(a.x + (size_t)start * a.n_in, (uint32_t)(n * a.n_in) * 2u);
   const int x_lane = (m * a.n_in + 8 * kb) * 2;
+  // XL: x in LDS as operands, rows 16 bytes more than n_in apart (16 rows on 16
+  // banks of four), lanes past the chunk on its last row
+  uint8_t* xl = reinterpret_cast<uint8_t*>(red + (a.wk > 1 ? a.wr * a.wk * RT * NT * 256 : 0));
+  const uint32_t xl_lane = (uint32_t)((m < n ? m : n - 1) * (2 * a.n_in + 16) + 16 * kb);
+  constexpr int kXP = 2;                        // pieces a thread loads before the weights
+  const int x_pieces = n * (a.n_in / 8);
+  u32x4_t xp[kXP];
+  auto load_piece = [&](int p) {
+    return __builtin_amdgcn_raw_buffer_load_b128(xr, p * 16, 0, 0);
+  };
+  auto store_piece = [&](int p, u32x4_t v) {
+    const int t = p / (a.n_in / 8), c = p - t * (a.n_in / 8);
+    *reinterpret_cast<bf16x8_t*>(xl + t * (2 * a.n_in + 16) + 16 * c) = pair_x(v);
+  };
+  if (XL) {
+#pragma unroll
+    for (int u = 0; u < kXP; ++u)
+      if (threadIdx.x + u * blockDim.x < x_pieces) xp[u] = load_piece(threadIdx.x + u * blockDim.x);
+  }
   for (int turn = 0; turn < a.turns && tile0 + turn < tiles; ++turn) {
     const int row0 = ((tile0 + turn) * a.wr + wr) * 16 * RT;
     uint32_t q_lane[RT], sb_lane[RT];         // byte offsets within a step's codes, a group's scales
@@ -198,7 +219,7 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[r][t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
     uint32_t q[U][RT][kM], sc[U][RT];
-    u32x4_t xv[U][NT][kM];
+    u32x4_t xv[XL ? 1 : U][NT][kM];
     auto load = [&](int u, int s) {
       const int qs = (int)((uint32_t)s * (uint32_t)(kStep / 2) * (uint32_t)a.n_out);
       const int ss = (int)(sb0 + (uint32_t)(s * kStep / GROUP) * (uint32_t)a.n_out * 4u);
@@ -213,13 +234,15 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
         }
         sc[u][r] = __builtin_amdgcn_raw_buffer_load_b32(mr, sb_lane[r], ss, 0);
       }
+      if constexpr (!XL) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < kM; ++j)
-          xv[u][t][j] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_lane + 16 * t * a.n_in * 2, s * kStep * 2 + 64 * j, 0);
+          for (int j = 0; j < kM; ++j)
+            xv[u][t][j] = __builtin_amdgcn_raw_buffer_load_b128(xr, x_lane + 16 * t * a.n_in * 2, s * kStep * 2 + 64 * j, 0);
+      }
     };
-    auto compute = [&](int u) {
+    auto compute = [&](int u, int s) {
       bf16x8_t xa[NT][kM];
       f32x4_t xs[NT];
 #pragma unroll
@@ -227,7 +250,10 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
         xs[t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kM; ++j) {
-          xa[t][j] = pair_x(xv[u][t][j]);
+          if constexpr (XL)
+            xa[t][j] = *reinterpret_cast<const bf16x8_t*>(xl + xl_lane + s * kStep * 2 + 64 * j);
+          else
+            xa[t][j] = pair_x(xv[u][t][j]);
           xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[t][j], ones, xs[t], 0, 0, 0);
         }
       }
@@ -257,20 +283,27 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (u < count) load(u, step(u));
+    if (XL && turn == 0) {
+#pragma unroll
+      for (int u = 0; u < kXP; ++u)
+        if (threadIdx.x + u * blockDim.x < x_pieces) store_piece(threadIdx.x + u * blockDim.x, xp[u]);
+      for (int p = threadIdx.x + kXP * blockDim.x; p < x_pieces; p += blockDim.x) store_piece(p, load_piece(p));
+      __syncthreads();
+    }
     int i = 0;
     for (; i + U <= count; i += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // the compiler would otherwise gather the loads behind all the sums
         __builtin_amdgcn_sched_barrier(0);
-        compute(u);
+        compute(u, step(i + u));
         __builtin_amdgcn_sched_barrier(0);
         if (i + U + u < count) load(u, step(i + U + u));
       }
     }
 #pragma unroll
     for (int u = 0; u < U - 1; ++u)
-      if (i + u < count) compute(u);
+      if (i + u < count) compute(u, step(i + u));
     if (a.wk == 1) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
@@ -303,22 +336,25 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   }
 }
 
+inline size_t x_lds_bytes(int rows, int n_in) { return (size_t)rows * (2 * n_in + 16); }
+
 constexpr long kMaxBlocks = 1l << 21;           // of a launch (its threads are counted in 32 bits)
 
-template <int GROUP, int NT, int RT, int U, bool EXP>
+template <int GROUP, int NT, int RT, int U, bool EXP, bool XL>
 int launch(LinArgs a, int wk, long likely, hipStream_t s) {
   const int steps = a.n_in / (GROUP == 32 ? 32 : 64);
   a.wk = wk;
   while (a.wk > 1 && 4 * a.wk > steps) a.wk /= 2;       // a share of four steps at least
-  a.wr = a.wk >= 4 ? 1 : 4 / a.wk;
+  a.wr = a.wk >= 4 ? 1 : XL && !EXP ? 8 / a.wk : 4 / a.wk;
   const long tiles = (a.n_out + 16 * RT * a.wr - 1) / (16 * RT * a.wr);
   a.turns = EXP && a.wk == 1 && tiles * likely >= 2048 ? 2 : 1;
   const long tile_blocks = (tiles + a.turns - 1) / a.turns;
-  const size_t lds = a.wk > 1 ? (size_t)a.wr * a.wk * RT * NT * 256 * sizeof(float) : 0;
+  const size_t lds = (a.wk > 1 ? (size_t)a.wr * a.wk * RT * NT * 256 * sizeof(float) : 0) +
+                     (XL ? x_lds_bytes(a.N < a.size ? (int)a.N : a.size, a.n_in) : 0);
   const long per = kMaxBlocks / tile_blocks > 0 ? kMaxBlocks / tile_blocks : 1;        // chunks a launch
   for (a.chunk0 = 0; a.chunk0 < a.chunks; a.chunk0 += per) {
     const long c = a.chunks - a.chunk0 < per ? a.chunks - a.chunk0 : per;
-    linear_int4_kernel<GROUP, NT, RT, U, EXP><<<(unsigned)(c * tile_blocks), 64 * a.wr * a.wk, lds, s>>>(a);
+    linear_int4_kernel<GROUP, NT, RT, U, EXP, XL><<<(unsigned)(c * tile_blocks), 64 * a.wr * a.wk, lds, s>>>(a);
     MOE_HIP(hipGetLastError());
   }
   return MOE_OK;
@@ -332,7 +368,10 @@ int launch(LinArgs a, int wk, long likely, hipStream_t s) {
 //                 T = 64: RT 2 13.2, RT 4 11.5   T = 1024: RT 4 94, NT 4 RT 4 76
 //   2048 x 8192   T = 1: RT 2 5.1, RT 1 5.3      T = 64: RT 4 11.5
 //   4096 x 16384  T = 8: RT 2 10.6, RT 4 11.4    T = 16: RT 2 13.2, RT 4 11.9
-//   256 experts of 512 x 2048, 512 rows: RT 4 35.6, RT 2 37.2
+//   2048 x 100003, T = 1: RT 2 28.1, with x in LDS 24.5 (4.7 TB/s)
+//   256 experts of 512 x 2048, 512 rows: RT 4 35.6, RT 2 37.2, with x in LDS 33.4
+// x in LDS (where a block's rows of it fit 32 KB) takes its loads, a fifth of
+// a wave's, off the path of the weights.
 // Inputs are split over the waves of a block (8 shares where blocks are few, 4
 // or none where they are many), which keeps more loads in flight per CU than
 // more steps per wave: 2048 x 2048, T = 1: 4.3 with four shares, 5.1 with two.
@@ -346,16 +385,32 @@ int by_rows(LinArgs a, hipStream_t s) {
   };
   const long wide = chunks(64, false);
   if (rows > 32 && t16 / 4 * wide >= 256) {
+    a.size = 64;
     a.chunks = chunks(64, true);
-    return launch<GROUP, 4, 4, 1, EXP>(a, t16 / 4 * wide >= 1024 ? 1 : 4, wide, s);
+    return launch<GROUP, 4, 4, 1, EXP, false>(a, t16 / 4 * wide >= 1024 ? 1 : 4, wide, s);
   }
-  a.chunks = chunks(16, true);
-  const long likely = chunks(16, false), units = t16 * likely;
-  if (EXP && units > 16384) return launch<GROUP, 1, 4, 2, EXP>(a, 1, likely, s);
-  if (units > 512 && rows > 8) return launch<GROUP, 1, 4, 2, EXP>(a, units > 8192 ? 1 : units > 1024 ? 4 : 8, likely, s);
-  if (units > 256) return launch<GROUP, 1, 2, 2, EXP>(a, units > 16384 ? 1 : units > 1024 ? 4 : 8, likely, s);
-  if (a.n_in >= 4096) return launch<GROUP, 1, 1, 4, EXP>(a, 8, likely, s);
-  return launch<GROUP, 1, 1, 2, EXP>(a, 4, likely, s);
+  // rows a chunk: 16, or fewer for experts with few rows if x then fits LDS
+  constexpr size_t kXlMax = 32768;
+  a.size = 16;
+  if (EXP)
+    while (a.size > 4 && a.size >= 4 * rows && x_lds_bytes(a.size, a.n_in) > kXlMax) a.size /= 2;
+  a.chunks = chunks(a.size, true);
+  const long likely = chunks(a.size, false), units = t16 * likely;
+  // (a few blocks only wait longer for it: ten expert rows 7.1 against 7.6)
+  const bool xl = units > 512 && x_lds_bytes(a.N < a.size ? (int)a.N : a.size, a.n_in) <= kXlMax;
+  if (xl && rows <= 8 && units > 4096) return launch<GROUP, 1, 2, EXP ? 3 : 2, EXP, true>(a, 1, likely, s);
+  if (EXP && units > 16384)
+    return xl ? launch<GROUP, 1, 4, 2, EXP, true>(a, 1, likely, s) : launch<GROUP, 1, 4, 2, EXP, false>(a, 1, likely, s);
+  if (units > 512 && rows > 8) {
+    const int wk = units > 8192 ? 1 : units > 1024 ? 4 : 8;
+    return xl ? launch<GROUP, 1, 4, 2, EXP, true>(a, wk, likely, s) : launch<GROUP, 1, 4, 2, EXP, false>(a, wk, likely, s);
+  }
+  if (units > 256) {
+    const int wk = units > 16384 ? 1 : units > 1024 ? 4 : 8;
+    return xl ? launch<GROUP, 1, 2, 2, EXP, true>(a, wk, likely, s) : launch<GROUP, 1, 2, 2, EXP, false>(a, wk, likely, s);
+  }
+  if (a.n_in >= 4096) return launch<GROUP, 1, 1, 4, EXP, false>(a, 8, likely, s);
+  return launch<GROUP, 1, 1, 2, EXP, false>(a, 4, likely, s);
 }
 
 template <bool EXP> int linear_launch(const LinArgs& a, int group, hipStream_t s) {
