@@ -19,7 +19,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kXCols = 256;     // columns a wave of the dx role
-constexpr int kWCols = 512;     // columns a block of the expert rows
+// Columns a block of the expert rows: 256 keep x's columns of an XCD in its L2
+// for prompts (33.4 against 31.7 us), 512 make fewer blocks of few rows (5.3
+// against 8.6).
+constexpr int w_cols(bool prompt) { return prompt ? 256 : 512; }
 constexpr int kECols = 64;      // columns a block of row E
 // Up to this many pairs each role forms their g itself; more take a launch of
 // their own first (4.6 us), which saves every column slab the k products of
@@ -124,14 +127,16 @@ __device__ void row_e(const GradArgs& a, int slab, float* red, float* lg) {
 // dW[e], kWCols columns (and db[e]): the waves take the bucket's pairs in turn.
 template <bool G>
 __device__ void row_expert(const GradArgs& a, int e, int slab, float* red, float* lg, int* lt) {
-  constexpr int kB = 8, kTile = kThreads;   // pairs of a bucket at a time
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int kB = 8, kTile = kThreads;       // pairs of a bucket at a time
+  constexpr int kWCols = w_cols(G);
+  constexpr int kL = kWCols / 8, kG = kThreads / kL;    // lanes a row, rows at once
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int grp = kL == 64 ? __builtin_amdgcn_readfirstlane(wave) : tid / kL;
   const long n = (long)a.T * a.k;
   long lo = a.offsets[e], hi = a.offsets[e + 1];
   lo = lo < 0 ? 0 : lo;                         // offsets of other pairs reach no memory past these
   hi = hi > n ? n : hi;
-  const int c = slab * kWCols + lane * 8;
+  const int c = slab * kWCols + tid % kL * 8;
   const uint16_t* x = a.x + (c < a.d ? c : a.d - 8);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float bias = 0.f;
@@ -149,26 +154,28 @@ __device__ void row_expert(const GradArgs& a, int e, int slab, float* red, float
     }
     __syncthreads();
     if (a.dW) {
-      for (int q0 = wave; q0 < m; q0 += kWaves * kB) {
+      for (int q0 = grp; q0 < m; q0 += kG * kB) {
         uint4 v[kB];
 #pragma unroll
         for (int u = 0; u < kB; ++u)
-          if (q0 + u * kWaves < m)
-            v[u] = *reinterpret_cast<const uint4*>(x + (size_t)__builtin_amdgcn_readfirstlane(lt[q0 + u * kWaves]) * a.d);
+          if (q0 + u * kG < m) {
+            const int t = kL == 64 ? __builtin_amdgcn_readfirstlane(lt[q0 + u * kG]) : lt[q0 + u * kG];
+            v[u] = *reinterpret_cast<const uint4*>(x + (size_t)t * a.d);
+          }
 #pragma unroll
         for (int u = 0; u < kB; ++u)
-          if (q0 + u * kWaves < m) fma8(acc, lg[q0 + u * kWaves], v[u]);
+          if (q0 + u * kG < m) fma8(acc, lg[q0 + u * kG], v[u]);
       }
     }
   }
   if (a.dW) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[wave * kWCols + i * 64 + lane] = acc[i];
+    for (int i = 0; i < 8; ++i) red[grp * kWCols + i * kL + tid % kL] = acc[i];
     __syncthreads();
     for (int o = tid; o < kWCols; o += kThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < kWaves; ++q) v += red[q * kWCols + (o & 7) * 64 + (o >> 3)];
+      for (int q = 0; q < kG; ++q) v += red[q * kWCols + (o & 7) * kL + (o >> 3)];
       if (slab * kWCols + o < a.d) a.dW[(size_t)e * a.d + slab * kWCols + o] = v;
     }
   }
@@ -244,7 +251,7 @@ __device__ void token_x(const GradArgs& a, int t, int slab) {
 template <bool G>
 __global__ __launch_bounds__(kThreads) void router_grad_kernel(GradArgs a) {
   __shared__ float red[kThreads / 8 * 65];
-  static_assert(kThreads / 8 * 65 >= kWaves * kWCols, "a row of partial sums a wave");
+  static_assert(kThreads / 8 * 65 >= kThreads * 8, "eight columns a thread");
   __shared__ float lg[kThreads];
   __shared__ int lt[kThreads];
   unsigned b = blockIdx.x;
@@ -254,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(GradArgs a) {
   }
   b -= a.blocks_e;
   if (b < a.blocks_w) {
-    const int slabs = a.dW ? (a.d + kWCols - 1) / kWCols : 1;
+    const int slabs = a.dW ? (a.d + w_cols(G) - 1) / w_cols(G) : 1;
     row_expert<G>(a, (int)(b / slabs), (int)(b % slabs), red, lg, lt);
     return;
   }
@@ -302,7 +309,8 @@ extern "C" int moe_router_topk_backward(const uint16_t* x, int32_t T, int32_t d,
     a.g = g;
   }
   a.blocks_e = dW ? (unsigned)(d / kECols) : 0;
-  a.blocks_w = dW ? (unsigned)(E * ((d + kWCols - 1) / kWCols)) : dbias ? (unsigned)E : 0;
+  const int cols = w_cols(a.g != nullptr);
+  a.blocks_w = dW ? (unsigned)(E * ((d + cols - 1) / cols)) : dbias ? (unsigned)E : 0;
   const unsigned blocks_x = dx ? (unsigned)((T + kWaves - 1) / kWaves) * (unsigned)((d + kXCols - 1) / kXCols) : 0;
   const unsigned blocks = a.blocks_e + a.blocks_w + blocks_x;
   if (blocks == 0) return MOE_OK;               // dx of no tokens
