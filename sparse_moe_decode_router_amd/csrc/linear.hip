@@ -41,17 +41,6 @@ struct LinArgs {
   int32_t size;                 // rows a chunk, at most 16 NT
 };
 
-// Inclusive sum over the lanes of a wave (row shifts, then the row totals).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
-
 // Sorted rows are cut into chunks of `size` that do not cross an expert's
 // border, numbered in expert order.
 struct RowChunk {

@@ -131,16 +131,12 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
   if (wave == 0 && lane < mine) key = idx[first + lane];
   __syncthreads();
   const uint32_t c = tid < E ? cnt[tid] : 0;
-  uint32_t incl = c & 0xFFFFu;
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const uint32_t v = __shfl_up(incl, s, 64);
-    if (lane >= s) incl += v;
-  }
+  const uint32_t incl = (uint32_t)wave_scan((int)(c & 0xFFFFu));
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
   uint32_t before = 0;
-  for (int q = 0; q < wave; ++q) before += wsum[q];
+#pragma unroll
+  for (int q = 0; q < kOneThreads / 64; ++q) before += q < wave ? wsum[q] : 0;
   if (tid < E) {
     const uint32_t lo = before + incl - (c & 0xFFFFu);
     cnt[tid] = lo + (c >> 16);
