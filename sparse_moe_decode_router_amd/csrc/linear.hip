@@ -155,12 +155,13 @@ __global__ __launch_bounds__(512) void linear_int4_kernel(LinArgs a) {
   if (EXP) {
     const RowChunk rc = find_chunk(a.offsets, a.slot_table, a.E, a.N, chunk, a.size);
     if (!rc.any) return;                        // past the last chunk
+    if (rc.n == 0) return;                      // rows that x does not have
     start = rc.start;
     n = rc.n;
     const int slot = rc.slot;
     missing = slot < 0 || slot >= a.n_slots;
     if (missing) {
-      if (threadIdx.x == 0 && a.err && n > 0) atomicOr(a.err, 1);
+      if (threadIdx.x == 0 && a.err) atomicOr(a.err, 1);
     } else {
       w += (uint64_t)slot * a.w_stride;
     }

@@ -48,7 +48,9 @@ def _check(y, x, m, what=""):
     (1, 64, 1, 64), (1, 32, 3, 32), (1, 128, 17, 128), (1, 2048, 512, 64), (2, 320, 100, 64), (7, 96, 33, 32),
     (8, 2048, 130, 64), (15, 192, 16, 64), (16, 1024, 47, 128), (17, 256, 65, 64), (31, 512, 40, 32),
     (33, 4096, 72, 128), (48, 640, 129, 64), (64, 64, 64, 64), (65, 1088, 31, 64), (130, 32, 20, 32),
-    (200, 448, 50, 64), (3, 8192, 24, 64), (1, 65536, 5, 64), (300, 128, 1, 128), (5, 1920, 1000, 128)])
+    (200, 448, 50, 64), (3, 8192, 24, 64), (1, 65536, 5, 64), (300, 128, 1, 128), (5, 1920, 1000, 128),
+    (300, 64, 4100, 64), (1100, 128, 1000, 128), (16, 256, 9000, 64), (3, 128, 20000, 32), (2, 64, 70000, 64),
+    (12, 2048, 4200, 128), (40, 96, 3100, 32)])
 def test_linear(T, n_in, n_out, group):
     rng = np.random.default_rng([T, n_in, n_out, group])
     m = _matrix(rng, n_out, n_in, group)
@@ -58,6 +60,53 @@ def test_linear(T, n_in, n_out, group):
     _check(y, x, m)
     # the same row of x gives the same bits wherever it sits among rows of the same number
     assert torch.equal(moe.moe_linear_int4(w, xd.flip(0).contiguous(), n_out, group), y.flip(0))
+
+
+def _packed_f64(w, n_in, n_out, group):
+    """fp64 [n_out][n_in] of a packed matrix on the device."""
+    nb = n_in * n_out // 2
+    byte = w[:nb].view(n_in // 32, n_out, 16)
+    q = torch.stack([byte & 15, byte >> 4], -1).view(n_in // 32, n_out, 32).permute(1, 0, 2).reshape(n_out, n_in).double()
+    sb = w[nb:nb + n_in // group * n_out * 4].view(torch.float16).view(n_in // group, n_out, 2).double()
+    s, b = sb[..., 0].t().repeat_interleave(group, 1), sb[..., 1].t().repeat_interleave(group, 1)
+    return q, s, b
+
+
+def test_experts_whose_rows_do_not_fit_lds():
+    """Long rows and many experts (280 MB of matrices, random bytes made on the
+    device): sampled experts against fp64, same tolerance."""
+    E, k, T, n_in, n_out = 256, 8, 160, 2112, 1040
+    g = torch.Generator(device="cuda").manual_seed(5)
+    nb = n_in * n_out // 2
+    w = torch.randint(0, 256, (E, moe.moe_linear_bytes(n_in, n_out)), dtype=torch.uint8, generator=g, device="cuda")
+    s = torch.empty(E, n_in // 64, n_out, 1, device="cuda").uniform_(0.002, 0.02, generator=g)
+    w[:, nb:] = torch.cat([s, -8 * s], -1).half().view(E, -1).view(torch.uint8)
+    x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda").int()
+    X, off, _, _ = moe.moe_sort_tokens(x, idx, E)
+    y = moe.moe_expert_linear_int4(w, None, X, off, n_out)
+    o = off.tolist()
+    for e in range(0, E, 17):
+        if o[e + 1] > o[e]:
+            q, sc, b = _packed_f64(w[e], n_in, n_out, 64)
+            xe = X[o[e]:o[e + 1]].double()
+            mag = xe.abs() @ (sc.abs() * (16 + q) + (b - 16 * sc).abs()).t()
+            err = (y[o[e]:o[e + 1]].double() - xe @ (sc * q + b).t()).abs()
+            assert (err <= (128 + 3 + n_in // 64 + 16) * 2.0 ** -23 * mag).all(), e
+
+
+def test_linear_small_and_large_values():
+    """Subnormal fp16 scales, and activations from 2^-60 to 2^110 in one row."""
+    rng = np.random.default_rng(6)
+    c, s, b = _matrix(rng, 33, 256, 64)
+    s = (s.astype(np.float32) * 2.0 ** -12).astype(np.float16)
+    b = (b.astype(np.float32) * 2.0 ** -12).astype(np.float16)
+    assert (s.astype(np.float32) < 2.0 ** -14).all()
+    w = torch.from_numpy(moe.moe_pack_linear_int4(c, s, b)).cuda()
+    x, xd = _x(rng, 5, 256)
+    scale = 2.0 ** rng.integers(-60, 110, (5, 1))
+    y = moe.moe_linear_int4(w, (xd.float() * torch.from_numpy(scale).float().cuda()).bfloat16(), 33)
+    _check(y, x * scale, (c, s, b))
 
 
 def test_linear_no_rows_and_non_finite_rows():
@@ -101,7 +150,8 @@ def test_linear_unaligned_weights_and_streams():
 
 @pytest.mark.parametrize("T,k,E,n_in,n_out,group", [
     (1, 1, 1, 64, 16, 64), (1, 10, 512, 256, 32, 64), (3, 2, 16, 96, 33, 32), (64, 8, 64, 128, 48, 128),
-    (40, 6, 20, 320, 65, 64), (200, 3, 4, 64, 20, 64), (900, 2, 5, 64, 17, 32), (9, 4, 1024, 64, 40, 64)])
+    (40, 6, 20, 320, 65, 64), (200, 3, 4, 64, 20, 64), (900, 2, 5, 64, 17, 32), (9, 4, 1024, 64, 40, 64),
+    (64, 8, 64, 128, 1100, 64), (400, 3, 4, 128, 2100, 32), (30, 8, 16, 192, 600, 64)])
 def test_experts(T, k, E, n_in, n_out, group):
     rng = np.random.default_rng([T, k, E, n_in])
     mats = [_matrix(rng, n_out, n_in, group) for _ in range(E)]

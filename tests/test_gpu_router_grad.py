@@ -72,7 +72,8 @@ def _check(got, x, W, idx, w, s, dw, ds):
 @pytest.mark.parametrize("T,d,E,k,kw", [
     (1, 64, 1, 1, {}), (1, 2048, 512, 10, {}), (3, 192, 7, 7, {}), (64, 576, 16, 4, dict(drop=True)),
     (65, 64, 4, 2, {}), (200, 512, 32, 3, dict(skew=True)), (129, 8192, 9, 2, {}), (300, 128, 1024, 16, {}),
-    (1000, 320, 5, 3, dict(drop=True)), (40, 64, 128, 100, {})])
+    (1000, 320, 5, 3, dict(drop=True)), (40, 64, 128, 100, {}),
+    (1500, 704, 16, 8, dict(drop=True, skew=True)), (5000, 64, 2, 1, {})])
 def test_router_gradient(T, d, E, k, kw):
     x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, **kw)
     xd, Wd, idxd, wd, sd, dwd, dsd = _dev(bits, W, idx, w, s, dw, ds)
