@@ -71,7 +71,12 @@ __global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
 // (LDS histogram; the low half of a counter takes every pair, the high half
 // those before the block's own), scans the counts over the experts, ranks its
 // pairs among themselves by ballots and adds the three.  The first row of each
-// wave is on its way meanwhile.
+// wave is on its way meanwhile, and a wave takes consecutive pairs: those of a
+// token share one load, and a store waits for no load behind it (loads and
+// stores return in order; rows strided over the waves took 46 us).
+// 4096 tokens of 2048 bf16, ten pairs each: 42 us for 185 MB (4.4 TB/s), some
+// 5 of it the count; histogram, scan, scatter and copy in four launches took 68.
+// One token: 4.3 us against 7.3 in two launches.
 constexpr int kOneMax = 65535;
 constexpr int kOneThreads = 1024;
 struct __attribute__((packed, aligned(4))) Key4 { int32_t v[4]; };
@@ -264,7 +269,8 @@ __global__ __launch_bounds__(64 * kWaves) void unsort_kernel(
 }
 
 // One wave per (token, rank), and one more a token for the shared rows: reads
-// dy[t] and its row once, writes the row's gradient and their dot product.
+// dy[t] (from L2 for all ranks but one) and its row, writes the row's gradient
+// and their dot product.  HBM-bound: 390 MB in 79 us (4.9 TB/s).
 template <int TYPE, int VN>
 __global__ __launch_bounds__(64 * kWaves) void unsort_grad_kernel(
     const typename El<TYPE>::raw* __restrict__ dy, const typename El<TYPE>::raw* __restrict__ rows,
