@@ -675,24 +675,16 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 # device whatever the current one, and allocate what they return on the
 # stream that they launch on.  The checks and the call itself are in
 # csrc/binding.cpp.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _rowops.bind(*(C.cast(getattr(_lib, _n), C.c_void_p).value for _n in (
     "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_combine",
     "moe_unsort_combine_backward", "moe_linear_bytes", "moe_linear_int4", "moe_expert_linear_int4",
     "moe_pool_linear_int4", "moe_router_topk_backward")))
 
 
-def _elsewhere(x, stream):
-    """None where tensor x is on the current device and no stream is named; else a context that makes its device
-    and the stream current."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("a device tensor is wanted")
-    dev = x.get_device()
-    if stream is None:
-        return None if _current_device() == dev else torch.cuda.device(dev)
-    if stream.device.index != dev:
-        raise ValueError("the stream is of another device than the tensors")
+def _stream_of(x, stream):
+    """A context that makes the stream, which has to be of tensor x's device, the current one."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or stream.device.index != x.get_device():
+        raise ValueError("a device tensor, and a stream of its device, are wanted")
     return torch.cuda.stream(stream)
 
 
@@ -711,9 +703,8 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
     Returns (x_sorted [T*k, d], offsets int32 [E+1], pair_ids int32 [T*k],
     row_of int32 [T, k]); rows of x_sorted and entries of pair_ids from
     offsets[E] on keep what they held (out: that tuple, to write into)."""
-    away = _elsewhere(x, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(x, stream):
             return moe_sort_tokens(x, topk_idx, E, workspace, out)
     if out is None or workspace is None:
         (T, d), k = _matrix(x, "x"), _matrix(topk_idx, "topk_idx")[1]
@@ -724,7 +715,7 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
         if workspace is None:
             workspace = torch.empty(moe_sort_workspace_bytes(T, k, E), dtype=torch.uint8, device=x.device)
     rows, offsets, pairs, row_of = out
-    st = _rowops.sort(x, topk_idx, E, rows, offsets, pairs, row_of, workspace, _raw_stream(x.get_device()))
+    st = _rowops.sort(x, topk_idx, E, rows, offsets, pairs, row_of, workspace)
     if st:
         _check(st, "moe_sort_tokens")
     return out
@@ -732,14 +723,13 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
 
 def moe_sort_tokens_backward(dx_sorted, row_of, out=None, stream=None):
     """Gradient of moe_sort_tokens with respect to x: dx [T, d] from dx_sorted [T*k, d]."""
-    away = _elsewhere(dx_sorted, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(dx_sorted, stream):
             return moe_sort_tokens_backward(dx_sorted, row_of, out)
     if out is None:
         out = torch.empty((_matrix(row_of, "row_of")[0], _matrix(dx_sorted, "dx_sorted")[1]), dtype=dx_sorted.dtype,
                           device=dx_sorted.device)
-    st = _rowops.sort_grad(dx_sorted, row_of, out, _raw_stream(dx_sorted.get_device()))
+    st = _rowops.sort_grad(dx_sorted, row_of, out)
     if st:
         _check(st, "moe_sort_tokens_backward")
     return out
@@ -748,14 +738,13 @@ def moe_sort_tokens_backward(dx_sorted, row_of, out=None, stream=None):
 def moe_unsort_combine(rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
     """y [T, d] = sum over a token's pairs of topk_w * rows[row_of], plus
     shared_gate * shared_out; rows [T*k, d], y and shared_out [T, d] of one type."""
-    away = _elsewhere(rows, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(rows, stream):
             return moe_unsort_combine(rows, row_of, topk_w, shared_out, shared_gate, out)
     if out is None:
         out = torch.empty((_matrix(row_of, "row_of")[0], _matrix(rows, "rows")[1]), dtype=rows.dtype,
                           device=rows.device)
-    st = _rowops.unsort(rows, row_of, topk_w, shared_out, shared_gate, out, _raw_stream(rows.get_device()))
+    st = _rowops.unsort(rows, row_of, topk_w, shared_out, shared_gate, out)
     if st:
         _check(st, "moe_unsort_combine")
     return out
@@ -765,16 +754,15 @@ def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, share
     """Gradients of moe_unsort_combine from dy [T, d]: (drows [T*k, d], dtopk_w
     fp32 [T, k], dshared_out [T, d], dshared_gate fp32 [T]), the last two None
     without shared rows; rows of drows that no pair has keep what they held."""
-    away = _elsewhere(rows, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(rows, stream):
             return moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out, shared_gate, out)
     if out is None:
         (T, k), has = _matrix(row_of, "row_of"), shared_out is not None
         out = (torch.empty_like(rows), torch.empty((T, k), dtype=torch.float32, device=rows.device),
                torch.empty_like(shared_out) if has else None,
                torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
-    st = _rowops.unsort_grad(dy, rows, row_of, topk_w, shared_out, shared_gate, *out, _raw_stream(rows.get_device()))
+    st = _rowops.unsort_grad(dy, rows, row_of, topk_w, shared_out, shared_gate, *out)
     if st:
         _check(st, "moe_unsort_combine_backward")
     return out
@@ -816,13 +804,12 @@ def moe_unpack_linear_int4(packed: np.ndarray, n_in: int, n_out: int, group: int
 
 def moe_linear_int4(packed, x, n_out: int, group: int = 64, out=None, stream=None):
     """y fp32 [T, n_out] = x W^T; x bf16 [T, n_in], packed uint8 [moe_linear_bytes]."""
-    away = _elsewhere(x, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(x, stream):
             return moe_linear_int4(packed, x, n_out, group, out)
     if out is None:
         out = torch.empty((_matrix(x, "x")[0], n_out), dtype=torch.float32, device=x.device)
-    st = _rowops.linear(packed, x, n_out, group, out, _raw_stream(x.get_device()))
+    st = _rowops.linear(packed, x, n_out, group, out)
     if st:
         _check(st, "moe_linear_int4")
     return out
@@ -835,14 +822,12 @@ def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, gr
     [n_slots, bytes] (rows may be apart: a view into larger blobs), slot_table
     int32 [E] or None (expert e in slot e); error: int32 [1] or None.  Rows
     from offsets[E] on keep what they held."""
-    away = _elsewhere(x_sorted, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(x_sorted, stream):
             return moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out, group, error, out)
     if out is None:
         out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
-    st = _rowops.expert_linear(packed, slot_table, x_sorted, offsets, n_out, group, out, error,
-                               _raw_stream(x_sorted.get_device()))
+    st = _rowops.expert_linear(packed, slot_table, x_sorted, offsets, n_out, group, out, error)
     if st:
         _check(st, "moe_expert_linear_int4")
     return out
@@ -853,14 +838,12 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
     if matrix not in _MATS:
         raise ValueError(f"matrix must be one of {_MATS}")
     n_in, n_out = (pool.I, pool.d) if matrix == "down" else (pool.d, pool.I)
-    away = _elsewhere(x_sorted, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(x_sorted, stream):
             return moe_pool_linear_int4(pool, matrix, x_sorted, offsets, out)
     if out is None:
         out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
-    st = _rowops.pool_linear(pool.handle.value, _MATS.index(matrix), n_in, n_out, pool.E, x_sorted, offsets, out,
-                             _raw_stream(x_sorted.get_device()))
+    st = _rowops.pool_linear(pool.handle.value, _MATS.index(matrix), n_in, n_out, pool.E, x_sorted, offsets, out)
     if st:
         _check(st, "moe_pool_linear_int4")
     return out
@@ -877,9 +860,8 @@ def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w
     dw_router fp32 [E+1, d], dlogit_bias fp32 [E]).  offsets and pair_ids from
     moe_bucket_tokens or moe_sort_tokens on topk_idx; dshared_gate None: no
     gradient.  out: that triple to write into, None for each not wanted."""
-    away = _elsewhere(x, stream)
-    if away is not None:
-        with away:
+    if stream is not None:
+        with _stream_of(x, stream):
             return moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate,
                                             offsets, pair_ids, workspace, out)
     if out is None or workspace is None:
@@ -891,7 +873,7 @@ def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w
             workspace = torch.empty(moe_router_backward_workspace_bytes(T, d, E, k), dtype=torch.uint8,
                                     device=x.device)
     st = _rowops.router_grad(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids,
-                             *out, workspace, _raw_stream(x.get_device()))
+                             *out, workspace)
     if st:
         _check(st, "moe_router_topk_backward")
     return out

@@ -58,7 +58,7 @@ def _binding() -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
            f"-I{os.path.join(os.path.dirname(os.path.dirname(HIPCC)), 'include')}",
            "-I" + sysconfig.get_paths()["include"], *("-isystem" + p for p in cpp_extension.include_paths()),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: binding.cpp\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -11,6 +11,8 @@
 #include <initializer_list>
 #include <string>
 
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe355.h"
@@ -103,11 +105,31 @@ int number32(PyObject* o, const char* name) {
   if (v < INT32_MIN) return size32(INT64_MAX, name);
   return size32(v, name);
 }
-hipStream_t stream_of(PyObject* o) {
+void* address(PyObject* o) {
   void* p = PyLong_AsVoidPtr(o);
   if (p == nullptr && PyErr_Occurred()) throw PyError{};
-  return (hipStream_t)p;
+  return p;
 }
+
+// The tensors' device as the current one for the call, and its current stream.
+class On {
+ public:
+  explicit On(int dev) : back_(c10::hip::current_device()) {
+    if (back_ == dev)
+      back_ = -1;
+    else
+      c10::hip::set_device((c10::DeviceIndex)dev);
+    stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
+  }
+  ~On() {
+    if (back_ >= 0) c10::hip::set_device((c10::DeviceIndex)back_);
+  }
+  On(const On&) = delete;
+  hipStream_t stream;
+
+ private:
+  int back_;
+};
 uint8_t* workspace(PyObject* o, int dev, size_t* bytes) {
   const at::Tensor& v = tensor(o, "workspace");
   uint8_t* p = static_cast<uint8_t*>(need(v, "workspace", kU8, {v.numel()}, dev));
@@ -132,61 +154,65 @@ PyObject* entry(PyObject* const* a, Py_ssize_t n, F body) {
   }
 }
 
-// x, topk_idx, E, x_sorted, offsets, pair_ids, row_of, workspace, stream
+// x, topk_idx, E, x_sorted, offsets, pair_ids, row_of, workspace
 PyObject* py_sort(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<9>(args, n, [](PyObject* const* a) {
-    int dev;
+  return entry<8>(args, n, [](PyObject* const* a) {
+    int dev, dev2;
     const at::Tensor& x = matrix(a[0], "x", &dev, true);
     const at::ScalarType t = x.scalar_type();
-    const int64_t T = x.size(0), d = x.size(1), k = tensor(a[1], "topk_idx").size(-1), E = number32(a[2], "E");
+    const int64_t T = x.size(0), d = x.size(1), k = matrix(a[1], "topk_idx", &dev2, false).size(1), E = number32(a[2], "E");
     size_t nws;
     uint8_t* ws = workspace(a[7], dev, &nws);
+    const On on(dev);
     return g.sort(need(x, "x", t, {T, d}, dev), type_code(t), size32(T, "T"), size32(d, "d"),
                   need<int32_t>(a[1], "topk_idx", kI32, {T, k}, dev), size32(k, "k"), (int)E,
                   need<void>(a[3], "x_sorted", t, {T * k, d}, dev), need<int32_t>(a[4], "offsets", kI32, {E + 1}, dev),
                   need<int32_t>(a[5], "pair_ids", kI32, {T * k}, dev), need<int32_t>(a[6], "row_of", kI32, {T, k}, dev),
-                  ws, nws, stream_of(a[8]));
+                  ws, nws, on.stream);
   });
 }
 
-// dx_sorted, row_of, dx, stream
+// dx_sorted, row_of, dx
 PyObject* py_sort_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<4>(args, n, [](PyObject* const* a) {
+  return entry<3>(args, n, [](PyObject* const* a) {
     int dev, dev2;
     const at::Tensor& x = matrix(a[0], "dx_sorted", &dev, true);
     const at::Tensor& r = matrix(a[1], "row_of", &dev2, false);
     const at::ScalarType t = x.scalar_type();
     const int64_t T = r.size(0), k = r.size(1), d = x.size(1);
+    const On on(dev);
     return g.sort_grad(need(x, "dx_sorted", t, {T * k, d}, dev), type_code(t), size32(T, "T"), size32(k, "k"),
                        size32(d, "d"), static_cast<int32_t*>(need(r, "row_of", kI32, {T, k}, dev)),
-                       need<void>(a[2], "out", t, {T, d}, dev), stream_of(a[3]));
+                       need<void>(a[2], "out", t, {T, d}, dev), on.stream);
   });
 }
 
-// rows, row_of, topk_w, shared_out, shared_gate, y, stream
+// rows, row_of, topk_w, shared_out, shared_gate, y
 PyObject* py_unsort(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<7>(args, n, [](PyObject* const* a) {
+  return entry<6>(args, n, [](PyObject* const* a) {
     int dev, dev2;
     const at::Tensor& x = matrix(a[0], "rows", &dev, true);
     const at::Tensor& r = matrix(a[1], "row_of", &dev2, false);
     const at::ScalarType t = x.scalar_type();
     const int64_t T = r.size(0), k = r.size(1), d = x.size(1);
+    const On on(dev);
     return g.unsort(need(x, "rows", t, {T * k, d}, dev), type_code(t), size32(T, "T"), size32(k, "k"), size32(d, "d"),
                     static_cast<int32_t*>(need(r, "row_of", kI32, {T, k}, dev)),
                     need<float>(a[2], "topk_w", kF32, {T, k}, dev), may<void>(a[3], "shared_out", t, {T, d}, dev),
                     may<float>(a[4], "shared_gate", kF32, {T}, dev), need<void>(a[5], "out", t, {T, d}, dev),
-                    stream_of(a[6]));
+                    on.stream);
   });
 }
 
-// dy, rows, row_of, topk_w, shared_out, shared_gate, drows, dtopk_w, dshared_out, dshared_gate, stream
+// dy, rows, row_of, topk_w, shared_out, shared_gate, drows, dtopk_w, dshared_out, dshared_gate
 PyObject* py_unsort_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<11>(args, n, [](PyObject* const* a) {
+  return entry<10>(args, n, [](PyObject* const* a) {
     int dev, dev2;
     const at::Tensor& x = matrix(a[1], "rows", &dev, true);
     const at::Tensor& r = matrix(a[2], "row_of", &dev2, false);
     const at::ScalarType t = x.scalar_type();
     const int64_t T = r.size(0), k = r.size(1), d = x.size(1);
+    const On on(dev);
     return g.unsort_grad(need<void>(a[0], "dy", t, {T, d}, dev), need(x, "rows", t, {T * k, d}, dev), type_code(t),
                          size32(T, "T"), size32(k, "k"), size32(d, "d"),
                          static_cast<int32_t*>(need(r, "row_of", kI32, {T, k}, dev)),
@@ -194,26 +220,27 @@ PyObject* py_unsort_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
                          may<float>(a[5], "shared_gate", kF32, {T}, dev),
                          need<void>(a[6], "drows", t, {T * k, d}, dev), need<float>(a[7], "dtopk_w", kF32, {T, k}, dev),
                          may<void>(a[8], "dshared_out", t, {T, d}, dev),
-                         may<float>(a[9], "dshared_gate", kF32, {T}, dev), stream_of(a[10]));
+                         may<float>(a[9], "dshared_gate", kF32, {T}, dev), on.stream);
   });
 }
 
-// packed, x, n_out, group, y, stream
+// packed, x, n_out, group, y
 PyObject* py_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<6>(args, n, [](PyObject* const* a) {
+  return entry<5>(args, n, [](PyObject* const* a) {
     int dev;
     const at::Tensor& x = matrix(a[1], "x", &dev, false);
     const int64_t T = x.size(0), n_in = x.size(1);
     const moe_linear_shape sh{size32(n_in, "n_in"), number32(a[2], "n_out"), number32(a[3], "group")};
+    const On on(dev);
     return g.linear(&sh, need<void>(a[0], "packed", kU8, {(int64_t)g.linear_bytes(&sh)}, dev),
                     static_cast<uint16_t*>(need(x, "x", kBf16, {T, n_in}, dev)), size32(T, "T"),
-                    need<float>(a[4], "out", kF32, {T, sh.n_out}, dev), stream_of(a[5]));
+                    need<float>(a[4], "out", kF32, {T, sh.n_out}, dev), on.stream);
   });
 }
 
-// packed, slot_table, x_sorted, offsets, n_out, group, y, error, stream
+// packed, slot_table, x_sorted, offsets, n_out, group, y, error
 PyObject* py_expert_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<9>(args, n, [](PyObject* const* a) {
+  return entry<8>(args, n, [](PyObject* const* a) {
     int dev, dev2;
     const at::Tensor& x = matrix(a[2], "x_sorted", &dev, false);
     const at::Tensor& w = matrix(a[0], "packed", &dev2, false);
@@ -228,32 +255,34 @@ PyObject* py_expert_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
       throw PyError{};
     }
     const size_t stride = w.size(0) > 1 ? (size_t)w.stride(0) : ((size_t)bytes + 3) / 4 * 4;
+    const On on(dev);
     return g.expert_linear(&sh, w.data_ptr(), stride, size32(w.size(0), "n_slots"),
                            may<int32_t>(a[1], "slot_table", kI32, {E}, dev), size32(E, "E"),
                            static_cast<uint16_t*>(need(x, "x_sorted", kBf16, {N, n_in}, dev)), size32(N, "N"),
                            need<int32_t>(a[3], "offsets", kI32, {E + 1}, dev),
                            need<float>(a[6], "out", kF32, {N, sh.n_out}, dev),
-                           may<int32_t>(a[7], "error", kI32, {1}, dev), stream_of(a[8]));
+                           may<int32_t>(a[7], "error", kI32, {1}, dev), on.stream);
   });
 }
 
-// pool handle, matrix, n_in, n_out, E, x_sorted, offsets, y, stream
+// pool handle, matrix, n_in, n_out, E, x_sorted, offsets, y
 PyObject* py_pool_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<9>(args, n, [](PyObject* const* a) {
+  return entry<8>(args, n, [](PyObject* const* a) {
     int dev;
     const at::Tensor& x = matrix(a[5], "x_sorted", &dev, false);
     const int64_t N = x.size(0), n_in = number(a[2]), n_out = number(a[3]), E = number(a[4]);
-    return g.pool_linear((const moe_pool*)stream_of(a[0]), number32(a[1], "matrix"),
+    const On on(dev);
+    return g.pool_linear((const moe_pool*)address(a[0]), number32(a[1], "matrix"),
                          static_cast<uint16_t*>(need(x, "x_sorted", kBf16, {N, n_in}, dev)), size32(N, "N"),
                          need<int32_t>(a[6], "offsets", kI32, {E + 1}, dev),
-                         need<float>(a[7], "out", kF32, {N, n_out}, dev), stream_of(a[8]));
+                         need<float>(a[7], "out", kF32, {N, n_out}, dev), on.stream);
   });
 }
 
 // x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids, dx, dw_router, dlogit_bias,
-// workspace, stream
+// workspace
 PyObject* py_router_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<14>(args, n, [](PyObject* const* a) {
+  return entry<13>(args, n, [](PyObject* const* a) {
     int dev, dev2;
     const at::Tensor& x = matrix(a[0], "x", &dev, false);
     const at::Tensor& W = matrix(a[1], "w_router", &dev2, false);
@@ -261,6 +290,7 @@ PyObject* py_router_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t T = x.size(0), d = x.size(1), E = W.size(0) - 1, k = idx.size(1);
     size_t nws;
     uint8_t* ws = workspace(a[12], dev, &nws);
+    const On on(dev);
     return g.router_grad(
         static_cast<uint16_t*>(need(x, "x", kBf16, {T, d}, dev)), size32(T, "T"), size32(d, "d"),
         static_cast<float*>(need(W, "w_router", kF32, {E + 1, d}, dev)), size32(E, "E"), size32(k, "k"),
@@ -269,14 +299,14 @@ PyObject* py_router_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
         may<float>(a[6], "dshared_gate", kF32, {T}, dev), may<int32_t>(a[7], "offsets", kI32, {E + 1}, dev),
         may<int32_t>(a[8], "pair_ids", kI32, {T * k}, dev), may<float>(a[9], "dx", kF32, {T, d}, dev),
         may<float>(a[10], "dw_router", kF32, {E + 1, d}, dev), may<float>(a[11], "dlogit_bias", kF32, {E}, dev), ws, nws,
-        stream_of(a[13]));
+        on.stream);
   });
 }
 
 PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return entry<10>(args, n, [](PyObject* const* a) {
     void** to = reinterpret_cast<void**>(&g);
-    for (int i = 0; i < 10; ++i) to[i] = (void*)stream_of(a[i]);
+    for (int i = 0; i < 10; ++i) to[i] = address(a[i]);
     return 0;
   });
 }

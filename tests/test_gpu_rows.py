@@ -173,7 +173,7 @@ def test_sort_matches_bucketing():
         assert torch.equal(off, off2) and torch.equal(pairs, pairs2)
 
 
-@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("T", [5, 300, 9000])
 def test_streams_and_graphs(T):
     """On another stream, and captured: every replay on new inputs equals the
     eager call, with the program's own work between."""
