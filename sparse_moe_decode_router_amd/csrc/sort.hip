@@ -66,6 +66,65 @@ __global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
   }
 }
 
+// The sort of a few decoded tokens (up to kFewMax pairs): a wave a pair, its
+// place counted by ballots over all the keys, which the wave's lanes hold; no
+// barrier.  offsets[e] counts the keys below e, a thread an entry.  One token
+// of ten pairs: 2.7 us, 4.3 in sort_one_kernel.
+constexpr int kFewMax = 256;
+template <int TYPE, int VN>
+__global__ __launch_bounds__(64 * kWaves) void sort_few_kernel(
+    const typename El<TYPE>::raw* __restrict__ x, const int32_t* __restrict__ idx, int n, int k, int d, int E,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ pair_ids, int32_t* __restrict__ row_of,
+    typename El<TYPE>::raw* __restrict__ out) {
+  constexpr int kK = kFewMax / 64, kA = 4;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int i = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pieces = (d + VN - 1) / VN;
+  int key[kK];
+#pragma unroll
+  for (int u = 0; u < kK; ++u) key[u] = 64 * u + lane < n ? idx[64 * u + lane] : -1;
+  const int e = i < n ? idx[i] : -1;
+  const typename El<TYPE>::raw* src = x + (size_t)((i < n ? i : 0) / k) * d;
+  Vec<TYPE, VN> v[kA];
+#pragma unroll
+  for (int u = 0; u < kA; ++u)
+    if (64 * u < pieces) v[u] = vec_load<TYPE, VN>(src + piece_start<VN>(64 * u + lane < pieces ? 64 * u + lane : pieces - 1, d));
+  for (int b = blockIdx.x * 64 * kWaves + tid; b <= E; b += gridDim.x * 64 * kWaves) {
+    int below = 0;
+#pragma unroll
+    for (int u = 0; u < kK; ++u)
+      for (int j = 0; j < 64 && 64 * u + j < n; ++j)
+        below += (unsigned)__builtin_amdgcn_readlane(key[u], j) < (unsigned)b;   // -1 is below none
+    offsets[b] = below;
+  }
+  if (i >= n) return;
+  if (e < 0 || e >= E) {
+    if (lane == 0) row_of[i] = -1;
+    return;
+  }
+  int row = 0;
+#pragma unroll
+  for (int u = 0; u < kK; ++u)
+    row += __popcll(__ballot((unsigned)key[u] < (unsigned)e || (key[u] == e && 64 * u + lane < i)));
+  if (lane == 0) {
+    row_of[i] = row;
+    pair_ids[row] = i;
+  }
+  typename El<TYPE>::raw* dst = out + (size_t)row * d;
+  for (int c0 = 0; c0 < pieces; c0 += 64 * kA) {
+#pragma unroll
+    for (int u = 0; u < kA; ++u) {
+      const int p = c0 + 64 * u + lane;
+      if (c0 > 0 && p < pieces) v[u] = vec_load<TYPE, VN>(src + piece_start<VN>(p, d));
+    }
+#pragma unroll
+    for (int u = 0; u < kA; ++u) {
+      const int p = c0 + 64 * u + lane;
+      if (p < pieces) vec_store<TYPE, VN>(dst + piece_start<VN>(p, d), v[u]);
+    }
+  }
+}
+
 // The whole sort in one launch, up to kOneMax pairs.  Each block places P
 // consecutive pairs and copies their rows.  It counts all the keys for itself
 // (LDS histogram; the low half of a counter takes every pair, the high half
@@ -76,7 +135,6 @@ __global__ __launch_bounds__(64 * kWaves) void gather_rows_kernel(
 // stores return in order; rows strided over the waves took 46 us).
 // 4096 tokens of 2048 bf16, ten pairs each: 42 us for 185 MB (4.4 TB/s), some
 // 5 of it the count; histogram, scan, scatter and copy in four launches took 68.
-// One token: 4.3 us against 7.3 in two launches.
 constexpr int kOneMax = 65535;
 constexpr int kOneThreads = 1024;
 struct __attribute__((packed, aligned(4))) Key4 { int32_t v[4]; };
@@ -405,6 +463,14 @@ extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d
   Carver c(ws, ws_bytes);
   SortWs w;
   if (!carve_sort(c, T, k, E, &w)) return MOE_ERR_INVALID_ARG;
+  if (n <= kFewMax)
+    return by_type(type, d, [&](auto ty, auto vn) -> int {
+      typedef typename El<decltype(ty)::v>::raw raw;
+      sort_few_kernel<decltype(ty)::v, decltype(vn)::v><<<wave_grid(n), 64 * kWaves, 0, s>>>(
+          static_cast<const raw*>(x), idx, (int)n, k, d, E, offsets, pair_ids, row_of, static_cast<raw*>(x_sorted));
+      MOE_HIP(hipGetLastError());
+      return MOE_OK;
+    });
   if (n <= kOneMax) {
     // pairs a block: a block for each of the 256 CUs, 16 pairs (one a wave) at least
     const int P = n <= 16 * 256 ? 16 : (int)((n + 255) / 256);
