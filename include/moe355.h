@@ -550,8 +550,8 @@ int moe_linear_int4(const moe_linear_shape* sh, const void* packed_dev,
 /* One matrix per expert, applied to rows in expert order (moe_sort_tokens):
  * y_sorted[p] = W_e x_sorted[p] for offsets[e] <= p < offsets[e+1].  Expert e's
  * matrix is at packed_dev + slot * stride_bytes (a multiple of 4), slot =
- * slot_table[e], or e without a table (then n_slots >= E).  N: rows of
- * x_sorted and y_sorted; rows of y_sorted from offsets[E] on keep what they
+ * slot_table[e], or e without a table (then n_slots >= E).  E <= 1024; N: rows
+ * of x_sorted and y_sorted, up to 2^30; rows of y_sorted from offsets[E] on keep what they
  * held.  An expert with rows whose slot is outside [0, n_slots) gives zeros
  * and sets bit 0 of error_dev (NULL: not reported). */
 int moe_expert_linear_int4(const moe_linear_shape* sh, const void* packed_dev,
@@ -578,8 +578,8 @@ int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
  * topk_w and shared_gate as moe_router_topk gave them (a pair whose index is
  * outside [0, E) has no logit); offsets_dev and pair_ids_dev of
  * moe_bucket_tokens or moe_sort_tokens on the same topk_idx, needed for dW
- * and dbias.  Sizes as moe_router_topk
- * with T * k <= 2^28 and T * d <= 2^33.  The workspace needs no fill. */
+ * and dbias.  Sizes as moe_router_topk, with T * k <= 2^28 and T * d <= 2^33.
+ * The workspace needs no fill. */
 size_t moe_router_backward_workspace_bytes(int32_t T, int32_t d, int32_t E,
                                            int32_t k);
 int moe_router_topk_backward(const uint16_t* x_dev, int32_t T, int32_t d,

@@ -471,7 +471,9 @@ extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d
       MOE_HIP(hipGetLastError());
       return MOE_OK;
     });
-  if (n <= kOneMax) {
+  // (few experts: the blocks' counters collide; 60000 pairs of one expert 65 us
+  // in one launch, of eight 27, as in the four below)
+  if (n <= kOneMax && (E >= 8 || n <= 8192)) {
     // pairs a block: a block for each of the 256 CUs, 16 pairs (one a wave) at least
     const int P = n <= 16 * 256 ? 16 : (int)((n + 255) / 256);
     return by_type(type, d, [&](auto ty, auto vn) -> int {

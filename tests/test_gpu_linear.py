@@ -95,6 +95,31 @@ def test_experts_whose_rows_do_not_fit_lds():
             assert (err <= (128 + 3 + n_in // 64 + 16) * 2.0 ** -23 * mag).all(), e
 
 
+@pytest.mark.parametrize("T", [1, 20])
+def test_a_matrix_past_2_gib(T):
+    """Byte offsets past 2^31 (random bytes made on the device): output rows
+    across the matrix against fp64, same tolerance."""
+    n_in, n_out = 4096, 1_100_003
+    g = torch.Generator(device="cuda").manual_seed(T)
+    nb = n_in * n_out // 2
+    w = torch.empty(moe.moe_linear_bytes(n_in, n_out), dtype=torch.uint8, device="cuda")
+    assert w.numel() > 1 << 31
+    w[:nb].random_(0, 256, generator=g)
+    s = torch.empty(n_in // 64, n_out, 1, device="cuda").uniform_(0.002, 0.02, generator=g)
+    w[nb:] = torch.cat([s, -8 * s], -1).half().view(-1).view(torch.uint8)
+    x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
+    y = moe.moe_linear_int4(w, x, n_out)
+    rows = torch.tensor([0, 1, 17, n_out // 2, n_out - 18, n_out - 2, n_out - 1], device="cuda")
+    byte = w[:nb].view(n_in // 32, n_out, 16)[:, rows]
+    q = torch.stack([byte & 15, byte >> 4], -1).view(n_in // 32, len(rows), 32).permute(1, 0, 2).reshape(len(rows), n_in)
+    sb = w[nb:].view(torch.float16).view(n_in // 64, n_out, 2)[:, rows].double()
+    sc, b = sb[..., 0].t().repeat_interleave(64, 1), sb[..., 1].t().repeat_interleave(64, 1)
+    mag = x.double().abs() @ (sc.abs() * (16 + q.double()) + (b - 16 * sc).abs()).t()
+    err = (y[:, rows].double() - x.double() @ (sc * q.double() + b).t()).abs()
+    assert (err <= (128 + 3 + n_in // 64 + 16) * 2.0 ** -23 * mag).all()
+    assert torch.isfinite(y).all()
+
+
 def test_linear_small_and_large_values():
     """Subnormal fp16 scales, and activations from 2^-60 to 2^110 in one row."""
     rng = np.random.default_rng(6)

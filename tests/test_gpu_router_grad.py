@@ -128,6 +128,34 @@ def test_router_gradient_in_a_graph_and_on_a_stream():
         assert all(torch.equal(a, b) for a, b in zip(got, step())), rep
 
 
+def test_two_streams_at_once():
+    """The same calls on two streams, nothing waiting between them, give each stream its own results."""
+    T, d, E, k = 120, 512, 24, 4
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets, want = [], []
+    w4 = torch.from_numpy(moe.moe_pack_linear_int4(
+        np.full((96, d), 7, np.uint8), np.full((96, d // 64), 0.01, np.float16), np.full((96, d // 64), -0.05, np.float16))).cuda()
+    for seed in (1, 2):
+        x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, seed=seed, skew=True)
+        sets.append(_dev(bits, W, idx, w, s, dw, ds))
+
+    def step(a, stream=None):
+        xd, Wd, idxd, wd, sd, dwd, dsd = a
+        X, off, pairs, row = moe.moe_sort_tokens(xd, idxd, E, stream=stream)
+        y = moe.moe_unsort_combine(X, row, wd, xd, sd, stream=stream)
+        return (y, moe.moe_linear_int4(w4, y, 96, stream=stream), moe.moe_sort_tokens_backward(X, row, stream=stream),
+                *moe.moe_unsort_combine_backward(y, X, row, wd, xd, sd, stream=stream)[1:],
+                *moe.moe_router_topk_backward(xd, Wd, idxd, wd, sd, dwd, dsd, off, pairs, stream=stream))
+
+    want = [step(a) for a in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [step(a, st) for a, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for g, r in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, r))
+
+
 # ------------------------------------------------------------- all together
 def test_the_layer_from_its_parts():
     """router -> sort -> gate, up, down products -> back equals the layer: the

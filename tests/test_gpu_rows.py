@@ -22,7 +22,7 @@ TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 SHAPES = [  # T, k, E, d
     (1, 1, 1, 1), (1, 10, 512, 2048), (3, 2, 4, 7), (5, 3, 16, 8), (64, 8, 256, 129), (128, 8, 64, 64),
     (129, 8, 64, 1001), (257, 10, 512, 40), (33, 40, 1024, 33), (700, 3, 8, 515), (2, 300, 512, 24),
-    (32, 8, 64, 257), (43, 6, 30, 65), (20, 5, 512, 1500), (1100, 2, 8, 1100), (1030, 3, 4, 3), (13107, 5, 16, 8), (16384, 4, 16, 9), (7000, 10, 3, 2),
+    (32, 8, 64, 257), (43, 6, 30, 65), (20, 5, 512, 1500), (1100, 2, 8, 1100), (1030, 3, 4, 3), (13107, 5, 16, 8), (16384, 4, 16, 9), (7000, 10, 3, 2), (5000, 2, 4, 8), (4500, 2, 8, 40),
 ]
 
 
@@ -208,6 +208,29 @@ def test_streams_and_graphs(T):
         got = [a.clone() for a in held]
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, step())), rep
+
+
+def test_more_than_2_31_elements():
+    """Rows past 4 GiB and 2^31 elements.  Sixteen equal bf16 rows sum to an
+    exact sixteenfold, and with weights of 1/16 to the row itself."""
+    T, k, E, d = 66000, 16, 32, 2048
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    X, off, pairs, row = moe.moe_sort_tokens(x, idx, E)
+    assert X.numel() > 1 << 31 and int(off[E]) == T * k
+    for a in range(0, T * k, 1 << 17):
+        b = min(a + (1 << 17), T * k)
+        assert torch.equal(X[a:b], x[pairs[a:b].long() // k])
+    assert torch.equal(moe.moe_sort_tokens_backward(X, row), x * 16)
+    w = torch.full((T, k), 1 / 16, device="cuda")
+    assert torch.equal(moe.moe_unsort_combine(X, row, w), x)
+    dX, dw, _, _ = moe.moe_unsort_combine_backward(x, X, row, w)
+    at = torch.tensor([0, T * k // 2, T * k - 1], device="cuda")
+    assert torch.equal(dX[at], x[pairs[at].long() // k] / 16)
+    t = torch.tensor([0, T // 2, T - 1], device="cuda")
+    n2 = x[t].double().square().sum(1, keepdim=True)
+    assert ((dw[t].double() - n2).abs() <= (d + 2) * U * n2).all()
 
 
 def test_tensors_that_do_not_fit_are_refused():
