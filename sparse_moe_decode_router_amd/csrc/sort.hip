@@ -125,29 +125,31 @@ __global__ __launch_bounds__(64 * kWaves) void sort_few_kernel(
   }
 }
 
-// The whole sort in one launch, up to kOneMax pairs.  Each block places P
+// The whole sort in one launch, up to kWideMax pairs.  Each block places P
 // consecutive pairs and copies their rows.  It counts all the keys for itself
 // (LDS histogram; the low half of a counter takes every pair, the high half
-// those before the block's own), scans the counts over the experts, ranks its
+// those before the block's own; WIDE, past 65535 pairs: two counters), scans the counts over the experts, ranks its
 // pairs among themselves by ballots and adds the three.  The first row of each
 // wave is on its way meanwhile, and a wave takes consecutive pairs: those of a
 // token share one load, and a store waits for no load behind it (loads and
 // stores return in order; rows strided over the waves took 46 us).
 // 4096 tokens of 2048 bf16, ten pairs each: 42 us for 185 MB (4.4 TB/s), some
 // 5 of it the count; histogram, scan, scatter and copy in four launches took 68.
-constexpr int kOneMax = 65535;
+constexpr int kOnePlaces = 256, kWidePlaces = 4096;     // pairs a block
+constexpr int kOneMax = 65535, kWideMax = 256 * kWidePlaces;
 constexpr int kOneThreads = 1024;
 struct __attribute__((packed, aligned(4))) Key4 { int32_t v[4]; };
 
-template <int TYPE, int VN>
+template <int TYPE, int VN, bool WIDE>
 __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
     const typename El<TYPE>::raw* __restrict__ x, const int32_t* __restrict__ idx, int n, int k, int d, int E, int P,
     int32_t* __restrict__ offsets, int32_t* __restrict__ pair_ids, int32_t* __restrict__ row_of,
     typename El<TYPE>::raw* __restrict__ out) {
   constexpr int kA = 4;                         // pieces a lane holds ahead
   __shared__ uint32_t cnt[1024];                // counts, then the next free row of each expert
+  __shared__ uint32_t earlier[WIDE ? 1024 : 1];
   __shared__ uint32_t wsum[16];
-  __shared__ int place[256];                    // P <= 256
+  __shared__ int place[WIDE ? kWidePlaces : kOnePlaces];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int first = blockIdx.x * P;
@@ -167,9 +169,16 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
   };
   if (q0 < q1) load((first + q0) / k, 0);
   if (tid < E) cnt[tid] = 0;
+  if (WIDE && tid < E) earlier[tid] = 0;
   __syncthreads();
   auto count = [&](int j, int key) {
-    if (key >= 0 && key < E) atomicAdd(&cnt[key], j < first ? 0x10001u : 1u);
+    if (key < 0 || key >= E) return;
+    if (WIDE) {
+      atomicAdd(&cnt[key], 1u);
+      if (j < first) atomicAdd(&earlier[key], 1u);
+    } else {
+      atomicAdd(&cnt[key], j < first ? 0x10001u : 1u);
+    }
   };
   constexpr int kQ = 4;                         // loads in flight
   const int quads = n >> 2;
@@ -193,16 +202,18 @@ __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(
   int key = -1;
   if (wave == 0 && lane < mine) key = idx[first + lane];
   __syncthreads();
-  const uint32_t c = tid < E ? cnt[tid] : 0;
-  const uint32_t incl = (uint32_t)wave_scan((int)(c & 0xFFFFu));
+  const uint32_t both = tid < E ? cnt[tid] : 0;
+  const uint32_t c = WIDE ? both : both & 0xFFFFu;
+  const uint32_t own = WIDE ? (tid < E ? earlier[tid] : 0) : both >> 16;     // before the block's pairs
+  const uint32_t incl = (uint32_t)wave_scan((int)c);
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
   uint32_t before = 0;
 #pragma unroll
   for (int q = 0; q < kOneThreads / 64; ++q) before += q < wave ? wsum[q] : 0;
   if (tid < E) {
-    const uint32_t lo = before + incl - (c & 0xFFFFu);
-    cnt[tid] = lo + (c >> 16);
+    const uint32_t lo = before + incl - c;
+    cnt[tid] = lo + own;
     if (blockIdx.x == 0) {
       offsets[tid] = (int32_t)lo;
       if (tid == E - 1) offsets[E] = (int32_t)(before + incl);
@@ -471,15 +482,18 @@ extern "C" int moe_sort_tokens(const void* x, int32_t type, int32_t T, int32_t d
       MOE_HIP(hipGetLastError());
       return MOE_OK;
     });
-  // (few experts: the blocks' counters collide; 60000 pairs of one expert 65 us
-  // in one launch, of eight 27, as in the four below)
-  if (n <= kOneMax && (E >= 8 || n <= 8192)) {
+  // (few experts: the blocks' counters collide.  60000 pairs of one expert 65 us
+  // in one launch, 25 in the four below; of eight 27 in both; 70000 of eight 43
+  // and 27, of 512 25 and 71)
+  if (n <= kWideMax && (n <= 8192 || E >= (n <= kOneMax ? 8 : 32))) {
     // pairs a block: a block for each of the 256 CUs, 16 pairs (one a wave) at least
     const int P = n <= 16 * 256 ? 16 : (int)((n + 255) / 256);
     return by_type(type, d, [&](auto ty, auto vn) -> int {
       typedef typename El<decltype(ty)::v>::raw raw;
-      sort_one_kernel<decltype(ty)::v, decltype(vn)::v><<<(unsigned)((n + P - 1) / P), kOneThreads, 0, s>>>(
-          static_cast<const raw*>(x), idx, (int)n, k, d, E, P, offsets, pair_ids, row_of, static_cast<raw*>(x_sorted));
+      auto* kernel = n <= kOneMax ? sort_one_kernel<decltype(ty)::v, decltype(vn)::v, false>
+                                  : sort_one_kernel<decltype(ty)::v, decltype(vn)::v, true>;
+      kernel<<<(unsigned)((n + P - 1) / P), kOneThreads, 0, s>>>(static_cast<const raw*>(x), idx, (int)n, k, d, E, P,
+                                                               offsets, pair_ids, row_of, static_cast<raw*>(x_sorted));
       MOE_HIP(hipGetLastError());
       return MOE_OK;
     });

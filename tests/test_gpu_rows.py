@@ -23,6 +23,7 @@ SHAPES = [  # T, k, E, d
     (1, 1, 1, 1), (1, 10, 512, 2048), (3, 2, 4, 7), (5, 3, 16, 8), (64, 8, 256, 129), (128, 8, 64, 64),
     (129, 8, 64, 1001), (257, 10, 512, 40), (33, 40, 1024, 33), (700, 3, 8, 515), (2, 300, 512, 24),
     (32, 8, 64, 257), (43, 6, 30, 65), (20, 5, 512, 1500), (1100, 2, 8, 1100), (1030, 3, 4, 3), (13107, 5, 16, 8), (16384, 4, 16, 9), (7000, 10, 3, 2), (5000, 2, 4, 8), (4500, 2, 8, 40),
+    (21850, 3, 1024, 2), (35000, 2, 7, 5), (33000, 2, 40, 3),
 ]
 
 
