@@ -1,7 +1,8 @@
 """Python binding for libmoe355 (routed-expert MoE layer on MI355X / gfx950).
 
 Argument marshalling only: every step of the layer runs in the HIP kernels of
-``libmoe355.so`` behind the C ABI declared in ``include/moe355.h``.  torch is
+``libmoe355.so`` behind the C ABI declared in ``include/moe355.h`` (called
+through ctypes, and for the row operators through ``_rowops.so``).  torch is
 used for device memory and streams.  Importing this package does not need a
 GPU; calling the device entry points does.  If the shared library has not
 been built the import fails loudly (there is no fallback path).

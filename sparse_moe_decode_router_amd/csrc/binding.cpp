@@ -122,7 +122,11 @@ class On {
     stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
   }
   ~On() {
-    if (back_ >= 0) c10::hip::set_device((c10::DeviceIndex)back_);
+    if (back_ < 0) return;
+    try {
+      c10::hip::set_device((c10::DeviceIndex)back_);
+    } catch (...) {                             // the next device call reports it
+    }
   }
   On(const On&) = delete;
   hipStream_t stream;
