@@ -575,8 +575,10 @@ int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
  *   dW[e] = sum over pairs of e of g x[t], dW[E] = sum_t g_s x[t]   [E+1][d]
  *   dbias[e] = sum over pairs of e of g                             [E]
  * all written whole; each output may be NULL (not all three).  topk_idx,
- * topk_w and shared_gate as moe_router_topk gave them (a pair whose index is
- * outside [0, E) has no logit); offsets_dev and pair_ids_dev of
+ * topk_w and shared_gate as moe_router_topk gave them.  A pair whose index is
+ * outside [0, E) has no logit: its weight and dtopk_w, whatever they hold, are
+ * in no sum (where the softmax took such a pair in, give the router's own
+ * topk_idx, its bucket lists and 0 in dtopk_w).  offsets_dev and pair_ids_dev of
  * moe_bucket_tokens or moe_sort_tokens on the same topk_idx, needed for dW
  * and dbias.  Sizes as moe_router_topk, with T * k <= 2^28 and T * d <= 2^33.
  * The workspace needs no fill. */

@@ -10,7 +10,8 @@ gradients are those of the formulas in layer.py:
   unsort   y[t] = sum_r w[t,r] Y[row(t,r)] + s_t o[t]
            dY[row] = w dy[t], dw = <dy[t], Y[row]>, do = s dy, ds = <dy, o>
   router   w = softmax of the chosen logits, s = sigmoid of the shared logit;
-           g = w (dw - sum_j w_j dw_j), g_s = s (1 - s) ds;
+           g = w (dw - sum_j w_j dw_j), g_s = s (1 - s) ds,
+           over the chosen logits: a pair without an expert is not among them;
            dx = sum_r g W[e_r] + g_s W[E], dW, db the same by expert.
 """
 from __future__ import annotations
@@ -77,10 +78,10 @@ def router_logit_grad(idx, w, gate, dw, dgate, E: int):
     T, k = w.shape
     dl = np.zeros((T, E + 1))
     for t in range(T):
-        z = w[t] @ dw[t]
-        for r in range(k):
-            if 0 <= idx[t, r] < E:
-                dl[t, idx[t, r]] += w[t, r] * (dw[t, r] - z)
+        chosen = [r for r in range(k) if 0 <= idx[t, r] < E]
+        z = w[t, chosen] @ dw[t, chosen]
+        for r in chosen:
+            dl[t, idx[t, r]] += w[t, r] * (dw[t, r] - z)
     if dgate is not None:
         s = np.asarray(gate, np.float64)
         dl[:, E] = s * (1 - s) * np.asarray(dgate, np.float64)

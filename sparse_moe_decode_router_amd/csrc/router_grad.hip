@@ -4,13 +4,15 @@
 //     dx[t]  = sum_r g[t,r] W[e_r] + g_s[t] W[E]
 //     dW[e]  = sum over the pairs of bucket e of g x[t],   dW[E] = sum_t g_s[t] x[t]
 //     db[e]  = sum over the pairs of bucket e of g
+// A dropped pair (index outside [0, E)) is in no softmax: its w and dw, which
+// may be anything, are in no sum (w is then the softmax over the others).
 // Only k + 1 of E + 1 logits of a token have a gradient, so both products are
 // weighted sums of rows: dx gathers router rows per token, dW gathers token
 // rows per bucket (the stable lists of moe_bucket_tokens).  One launch, its
 // blocks in three roles; fp32 throughout, fixed order, no atomics.  4096 tokens
 // of 2048, 10 of 512 experts: 32 us with the pairs' launch, bound by the rows
 // gathered through L2 (369 MB for dx, 184 MB for dW); three launches with
-// partial sums joined in the last took 94.  64 tokens, 8 of 256: 4.7 us.
+// partial sums joined in the last took 94.  64 tokens, 8 of 256: 5.0 us.
 #include "internal.h"
 #include "device.h"
 
@@ -56,23 +58,35 @@ __device__ __forceinline__ float gate_grad(const GradArgs& a, int t) {
   return a.dsgate[t] * (s * (1.f - s));
 }
 
-// g of pair i of token t (one thread).
+__device__ __forceinline__ bool has_logit(const GradArgs& a, int e) { return (unsigned)e < (unsigned)a.E; }
+// v, or 0 whatever v holds (bits, so that no load of v waits behind the test).
+__device__ __forceinline__ float keep_if(bool ok, float v) {
+  return __uint_as_float(__float_as_uint(v) & (ok ? ~0u : 0u));
+}
+
+// g of pair i, which has a logit, of token t (one thread).
 __device__ __forceinline__ float pair_grad(const GradArgs& a, long i, int t) {
   const float* w = a.w + (size_t)t * a.k;
   const float* dw = a.dw + (size_t)t * a.k;
+  const int32_t* idx = a.idx + (size_t)t * a.k;
   constexpr int kB = 10;                        // loads in flight
   const float wi = a.w[i], di = a.dw[i];
   float z = 0.f;
   for (int r0 = 0; r0 < a.k; r0 += kB) {
     float u[kB], v[kB];
+    int e[kB];
 #pragma unroll
     for (int q = 0; q < kB; ++q) {
       const int r = r0 + q < a.k ? r0 + q : a.k - 1;
       u[q] = w[r];
       v[q] = dw[r];
+      e[q] = idx[r];
     }
 #pragma unroll
-    for (int q = 0; q < kB; ++q) z = r0 + q < a.k ? fmaf(u[q], v[q], z) : z;
+    for (int q = 0; q < kB; ++q) {
+      const bool ok = r0 + q < a.k && has_logit(a, e[q]);
+      z = fmaf(keep_if(ok, u[q]), keep_if(ok, v[q]), z);
+    }
   }
   return wi * (di - z);
 }
@@ -204,7 +218,11 @@ __device__ void token_x(const GradArgs& a, int t, int slab) {
   const float* W = a.W + (c < a.d ? c : a.d - 4);
   float z = 0.f;
   if (!G) {
-    for (int r = lane; r < a.k; r += 64) z = fmaf(a.w[(size_t)t * a.k + r], a.dw[(size_t)t * a.k + r], z);
+    for (int r = lane; r < a.k; r += 64) {
+      const size_t i = (size_t)t * a.k + r;
+      const bool ok = has_logit(a, a.idx[i]);
+      z = fmaf(keep_if(ok, a.w[i]), keep_if(ok, a.dw[i]), z);
+    }
     z = wave_sum(z);
   }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -214,8 +232,7 @@ __device__ void token_x(const GradArgs& a, int t, int slab) {
     int el = -1;
     if (r < a.k) {
       const size_t i = (size_t)t * a.k + r;
-      el = a.idx[i];
-      if (el >= a.E) el = -1;
+      el = has_logit(a, a.idx[i]) ? a.idx[i] : -1;
       gl = G ? a.g[i + t] : a.w[i] * (a.dw[i] - z);
     } else if (r == a.k) {
       el = a.E;
@@ -250,9 +267,11 @@ __device__ void token_x(const GradArgs& a, int t, int slab) {
 // Blocks of row E first (they take longest), then the expert rows, then dx.
 // Blocks go to the 8 XCDs in turn, so numbering the column slabs fastest keeps
 // one XCD's L2 on the same columns of x and W where their number divides 8.
-// G: the pairs' g are in a.g.
+// G: the pairs' g are in a.g.  Without, five waves a SIMD (90 registers; left
+// alone the compiler takes 116, and the 1184 blocks of 64 tokens of 8 of 256,
+// d = 2048, need a second round: 6.4 against 5.0 us).
 template <bool G>
-__global__ __launch_bounds__(kThreads) void router_grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(kThreads, G ? 8 : 5) void router_grad_kernel(GradArgs a) {
   __shared__ float red[kThreads / 8 * 65];
   static_assert(kThreads / 8 * 65 >= kThreads * 8, "eight columns a thread");
   __shared__ float lg[kThreads];

@@ -100,6 +100,39 @@ def test_router_gradient_without_tokens():
     assert (dW == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("T,d,E,k", [(90, 128, 8, 3), (40, 64, 128, 100), (1500, 128, 8, 4), (60, 64, 256, 130)])
+def test_router_gradient_does_not_read_dropped_pairs(T, d, E, k):
+    """Weights and their gradients at pairs without an expert change no bit of
+    the results, whatever they hold (the pairs' g in the roles and, past 4096
+    pairs, in a launch of their own)."""
+    x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, drop=True)
+    idx[0] = E
+    out = (idx < 0) | (idx >= E)
+    w, dw = np.where(out, 0, w).astype(np.float32), np.where(out, 0, dw).astype(np.float32)
+    xd, Wd, idxd, wd, sd, dwd, dsd = _dev(bits, W, idx, w, s, dw, ds)
+    _, off, pairs = moe.moe_bucket_tokens(idxd, E)
+    want = moe.moe_router_topk_backward(xd, Wd, idxd, wd, sd, dwd, dsd, off, pairs)
+    _check(want, x, W, idx, w, s, dw, ds)
+    z, nan, inf = torch.from_numpy(out).cuda(), float("nan"), float("inf")
+    for a, b in [(nan, 0.0), (0.5, 2.0), (nan, nan), (inf, -inf)]:
+        got = moe.moe_router_topk_backward(xd, Wd, idxd, wd.masked_fill(z, a), sd, dwd.masked_fill(z, b), dsd, off, pairs)
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), (a, b)
+
+
+@pytest.mark.parametrize("T", [60, 2100])
+def test_dropped_pairs_through_the_way_back_and_the_router(T):
+    """sort -> way back's gradient -> router's gradient with NaN in the weights
+    of dropped pairs: the gradients of the same step without those weights."""
+    d, E, k = 64, 16, 2
+    x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, drop=True)
+    xd, Wd, idxd, wd, sd, dwd, dsd = _dev(bits, W, idx, np.where(idx < 0, np.nan, w).astype(np.float32), s, dw, ds)
+    X, off, pairs, row = moe.moe_sort_tokens(xd, idxd, E)
+    _, dw2, _, ds2 = moe.moe_unsort_combine_backward(xd, X, row, wd, xd, sd)
+    got = moe.moe_router_topk_backward(xd, Wd, idxd, wd, sd, dw2, ds2, off, pairs)
+    assert all(torch.isfinite(a).all() for a in got)
+    _check(got, x, W, idx, np.where(idx < 0, 0, w), s, dw2.cpu().numpy(), ds2.cpu().numpy())
+
+
 def test_router_gradient_in_a_graph_and_on_a_stream():
     T, d, E, k = 150, 256, 12, 3
     x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, skew=True)

@@ -93,6 +93,32 @@ def test_oracle_router_gradient_against_differences():
     assert np.allclose(_differences(lambda a: loss(x, W, a), b), gb, atol=1e-7)
 
 
+def test_oracle_router_gradient_with_dropped_pairs_against_differences():
+    """With some of the chosen pairs dropped, the weights are the softmax over
+    the others; what a dropped pair's weight and gradient hold is not used.
+    Tolerance as above."""
+    rng = np.random.default_rng(3)
+    T, k, E, d = 6, 3, 7, 4
+    x, W = rng.standard_normal((T, d)), rng.standard_normal((E + 1, d))
+    idx, dw = _routing(rng, T, k, E, drop=0.4), rng.standard_normal((T, k))
+    idx[2], idx[3, 1] = -1, E
+    live = (idx >= 0) & (idx < E)
+    assert live.any(1).sum() >= 4 and (~live[live.any(1)]).any()
+
+    def weights(x_, W_):
+        l = np.take_along_axis(x_ @ W_[:E].T, np.where(live, idx, 0), 1)
+        e = np.where(live, np.exp(l), 0)
+        return e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+
+    loss = lambda x_, W_: np.sum(np.where(live, dw, 0) * weights(x_, W_))
+    w, g = np.where(live, weights(x, W), np.nan), np.where(live, dw, np.inf)
+    gx, gW, gb = orows.router_grad(x, W, idx, w, None, g, None)
+    assert np.allclose(_differences(lambda a: loss(a, W), x), gx, atol=1e-7)
+    assert np.allclose(_differences(lambda a: loss(x, a), W), gW, atol=1e-7)
+    # moving all logits of a token alike changes no weight
+    assert np.allclose(orows.router_logit_grad(idx, w, None, g, None, E).sum(1), 0, atol=1e-14) and abs(gb.sum()) < 1e-13
+
+
 # ------------------------------------------------------------------ packing
 def _matrix(rng, out, n_in, group):
     codes = rng.integers(0, 16, (out, n_in), dtype=np.uint8)
