@@ -569,7 +569,8 @@ int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
 
 /* ------------------------------------------------- gradient of the router
  * From the gradients of moe_router_topk's weights (dtopk_w_dev [T][k]) and
- * shared gate (dshared_gate_dev [T], or NULL: none): with g[t,r] = w (dw -
+ * shared gate (dshared_gate_dev [T], or NULL: none, dW[E] is zeros and row E of
+ * W is not used, whatever x and W hold): with g[t,r] = w (dw -
  * sum_j w_j dw_j) and g_s = s (1 - s) ds,
  *   dx[t] = sum_r g[t,r] W[idx[t,r]] + g_s W[E]              fp32 [T][d]
  *   dW[e] = sum over pairs of e of g x[t], dW[E] = sum_t g_s x[t]   [E+1][d]

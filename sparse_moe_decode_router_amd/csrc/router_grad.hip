@@ -53,7 +53,7 @@ struct GradArgs {
 };
 
 __device__ __forceinline__ float gate_grad(const GradArgs& a, int t) {
-  if (!a.dsgate) return 0.f;
+  if (!a.dsgate) return 0.f;                    // its row of W is then not read either
   const float s = a.sgate[t];
   return a.dsgate[t] * (s * (1.f - s));
 }
@@ -114,6 +114,10 @@ template <bool G>
 __device__ void row_e(const GradArgs& a, int slab, float* red, float* lg) {
   constexpr int kB = 8, kG = kThreads / 8;
   const int tid = threadIdx.x, grp = tid >> 3;
+  if (!a.dsgate) {                              // no gradient: zeros, whatever x and the gate hold
+    if (tid < kECols) a.dW[(size_t)a.E * a.d + slab * kECols + tid] = 0.f;
+    return;
+  }
   const uint16_t* x = a.x + slab * kECols + (tid & 7) * 8;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int t0 = 0; t0 < a.T; t0 += kG * kB) {
@@ -235,7 +239,7 @@ __device__ void token_x(const GradArgs& a, int t, int slab) {
       el = has_logit(a, a.idx[i]) ? a.idx[i] : -1;
       gl = G ? a.g[i + t] : a.w[i] * (a.dw[i] - z);
     } else if (r == a.k) {
-      el = a.E;
+      el = a.dsgate ? a.E : -1;
       gl = G ? a.g[(size_t)t * (a.k + 1) + a.k] : gate_grad(a, t);
     }
     const int m = a.k + 1 - r0 < 64 ? a.k + 1 - r0 : 64;

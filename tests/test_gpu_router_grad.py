@@ -133,6 +133,24 @@ def test_dropped_pairs_through_the_way_back_and_the_router(T):
     _check(got, x, W, idx, np.where(idx < 0, 0, w), s, dw2.cpu().numpy(), ds2.cpu().numpy())
 
 
+@pytest.mark.parametrize("T", [40, 2100])
+def test_router_gradient_without_a_gate_gradient(T):
+    """No gradient of the shared gate: its row gets zeros and adds nothing, also
+    with NaN in the token rows of padding and in the gate's own weights."""
+    d, E, k = 192, 8, 2
+    x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k)
+    idx[3] = -1
+    xd, Wd, idxd, wd, sd, dwd, _ = _dev(bits, W, idx, w, s, dw, ds)
+    _, off, pairs = moe.moe_bucket_tokens(idxd, E)
+    for gate in (None, sd):
+        want = moe.moe_router_topk_backward(xd, Wd, idxd, wd, gate, dwd, None, off, pairs)
+        bad_x, bad_W = xd.clone(), Wd.clone()
+        bad_x[3], bad_W[E] = float("nan"), float("inf")
+        got = moe.moe_router_topk_backward(bad_x, bad_W, idxd, wd, gate, dwd, None, off, pairs)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and (got[1][E] == 0).all()
+        assert (got[0][3] == 0).all()
+
+
 def test_router_gradient_in_a_graph_and_on_a_stream():
     T, d, E, k = 150, 256, 12, 3
     x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, skew=True)
