@@ -774,12 +774,29 @@ def moe_linear_bytes(n_in: int, n_out: int, group: int = 64) -> int:
     return int(_lib.moe_linear_bytes(C.byref(moe_linear_shape(n_in, n_out, group))))
 
 
+def _codes_u8(a) -> np.ndarray:
+    a = np.asarray(a)
+    with np.errstate(invalid="ignore"):
+        c = np.ascontiguousarray(a.astype(np.uint8))
+    if not np.array_equal(c, a):                # 256 would wrap to 0, 7.9 become 7
+        raise ValueError("codes: whole numbers from 0 to 15 are wanted")
+    return c
+
+
+def _f16_bits(a, name: str) -> np.ndarray:
+    a = np.asarray(a)
+    with np.errstate(over="ignore"):
+        h = np.ascontiguousarray(a.astype(np.float16))
+    if np.any(np.isinf(h) & np.isfinite(a)):
+        raise ValueError(f"{name}: a value past the largest float16")
+    return h.view(np.uint16)
+
+
 def moe_pack_linear_int4(codes, scales, biases) -> np.ndarray:
     """Packed uint8 bytes of a 4-bit matrix: codes [n_out][n_in] (0..15), scales
-    and biases fp16 [n_out][n_in / group]; the group is n_in / scales.shape[1]."""
-    c = np.ascontiguousarray(codes, dtype=np.uint8)
-    s = np.ascontiguousarray(np.asarray(scales, np.float16)).view(np.uint16)
-    b = np.ascontiguousarray(np.asarray(biases, np.float16)).view(np.uint16)
+    and biases [n_out][n_in / group], rounded to fp16 if they are not; the group
+    is n_in / scales.shape[1].  Values that do not fit are refused."""
+    c, s, b = _codes_u8(codes), _f16_bits(scales, "scales"), _f16_bits(biases, "biases")
     if c.ndim != 2 or s.ndim != 2 or s.shape != b.shape or s.shape[0] != c.shape[0] or s.shape[1] < 1 \
             or c.shape[1] % s.shape[1]:
         raise ValueError(f"codes {c.shape}, scales {s.shape} and biases {b.shape} do not belong together")
@@ -793,7 +810,9 @@ def moe_pack_linear_int4(codes, scales, biases) -> np.ndarray:
 def moe_unpack_linear_int4(packed: np.ndarray, n_in: int, n_out: int, group: int = 64):
     """(codes, scales, biases) of moe_pack_linear_int4."""
     sh = moe_linear_shape(n_in, n_out, group)
-    p = np.ascontiguousarray(packed, dtype=np.uint8)
+    p = np.ascontiguousarray(packed)
+    if p.dtype != np.uint8:
+        raise ValueError(f"packed: uint8 bytes are wanted, got {p.dtype}")
     if p.size != int(_lib.moe_linear_bytes(C.byref(sh))) or p.size == 0:
         raise ValueError(f"{p.size} bytes are no packed {n_out} x {n_in} matrix with groups of {group}")
     codes = np.empty((n_out, n_in), np.uint8)

@@ -162,6 +162,30 @@ def test_pack_linear_refusals():
         assert moe.moe_linear_bytes(n_in, out, g) == 0
 
 
+@pytest.mark.parametrize("bad", [256, 16 + 256, -256, 7.5, np.nan])
+def test_pack_linear_refuses_codes_that_do_not_fit_a_byte(bad):
+    """Codes that a conversion to bytes would turn into other codes."""
+    c, s, b = _matrix(np.random.default_rng(2), 4, 64, 64)
+    wide = c.astype(np.float64 if isinstance(bad, float) else np.int64)
+    assert np.array_equal(moe.moe_pack_linear_int4(wide, s, b), moe.moe_pack_linear_int4(c, s, b))
+    wide[2, 5] = bad
+    with pytest.raises(ValueError):
+        moe.moe_pack_linear_int4(wide, s, b)
+
+
+def test_pack_linear_refuses_scales_that_do_not_fit_fp16():
+    c, s, b = _matrix(np.random.default_rng(2), 4, 64, 64)
+    assert np.array_equal(moe.moe_pack_linear_int4(c, s.astype(np.float64), b.astype(np.float32)),
+                          moe.moe_pack_linear_int4(c, s, b))
+    for i in range(2):
+        a = [s.astype(np.float32), b.astype(np.float32)]
+        a[i][1, 0] = 65520.0                           # halfway past the largest fp16: rounds to infinity
+        with pytest.raises(ValueError):
+            moe.moe_pack_linear_int4(c, *a)
+    with pytest.raises(ValueError):
+        moe.moe_unpack_linear_int4(moe.moe_pack_linear_int4(c, s, b).astype(np.int32), 64, 4)
+
+
 # ----------------------------------------------------------------- refusals
 def test_sort_refusals():
     def call(x=P, ty=moe.MOE_TYPE_BF16, T=4, d=8, idx=P, k=2, E=4, out=P, off=P, pairs=P, row=P, ws=P, nws=WS):
