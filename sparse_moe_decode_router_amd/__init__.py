@@ -695,8 +695,13 @@ def _matrix(x, name):
     return x.shape
 
 
+def _fit_i32(*sizes) -> bool:
+    """Sizes that the C calls' 32-bit arguments hold (ctypes would keep their low bits)."""
+    return all(-(1 << 31) <= v < 1 << 31 for v in sizes)
+
+
 def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
-    return int(_lib.moe_sort_workspace_bytes(T, k, E))
+    return int(_lib.moe_sort_workspace_bytes(T, k, E)) if _fit_i32(T, k, E) else 0
 
 
 def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
@@ -771,6 +776,8 @@ def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, share
 
 # ----------------------------------------------------------- 4-bit products
 def moe_linear_bytes(n_in: int, n_out: int, group: int = 64) -> int:
+    if not _fit_i32(n_in, n_out, group):
+        return 0
     return int(_lib.moe_linear_bytes(C.byref(moe_linear_shape(n_in, n_out, group))))
 
 
@@ -813,7 +820,7 @@ def moe_unpack_linear_int4(packed: np.ndarray, n_in: int, n_out: int, group: int
     p = np.ascontiguousarray(packed)
     if p.dtype != np.uint8:
         raise ValueError(f"packed: uint8 bytes are wanted, got {p.dtype}")
-    if p.size != int(_lib.moe_linear_bytes(C.byref(sh))) or p.size == 0:
+    if p.size != moe_linear_bytes(n_in, n_out, group) or p.size == 0:
         raise ValueError(f"{p.size} bytes are no packed {n_out} x {n_in} matrix with groups of {group}")
     codes = np.empty((n_out, n_in), np.uint8)
     s, b = np.empty((n_out, n_in // group), np.float16), np.empty((n_out, n_in // group), np.float16)
@@ -871,7 +878,7 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
 
 # ------------------------------------------------------ gradient of the router
 def moe_router_backward_workspace_bytes(T: int, d: int, E: int, k: int) -> int:
-    return int(_lib.moe_router_backward_workspace_bytes(T, d, E, k))
+    return int(_lib.moe_router_backward_workspace_bytes(T, d, E, k)) if _fit_i32(T, d, E, k) else 0
 
 
 def moe_router_topk_backward(x, w_router, topk_idx, topk_w, shared_gate, dtopk_w, dshared_gate, offsets, pair_ids,

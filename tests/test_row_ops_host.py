@@ -260,6 +260,18 @@ def test_router_backward_refusals():
     assert f(4096, 2048, 512, 10) < 24 << 20
 
 
+def test_sizes_past_32_bits_are_not_those_of_their_low_bits():
+    big = 1 << 32
+    for f, a in [(moe.moe_linear_bytes, (64, 8, 64)), (moe.moe_sort_workspace_bytes, (4, 2, 4)),
+                 (moe.moe_router_backward_workspace_bytes, (4, 64, 8, 2))]:
+        assert f(*a) > 0
+        for i in range(len(a)):
+            for v in (a[i] + big, a[i] - big):
+                assert f(*a[:i], v, *a[i + 1:]) == 0, (f, i, v)
+    with pytest.raises(ValueError):
+        moe.moe_unpack_linear_int4(np.zeros(moe.moe_linear_bytes(64, 8), np.uint8), 64, 8 + big)
+
+
 def test_host_tensors_are_refused():
     torch = pytest.importorskip("torch")
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
