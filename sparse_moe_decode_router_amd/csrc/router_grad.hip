@@ -33,6 +33,10 @@ constexpr int kECols = 64;      // columns a block of row E
 // their own first (4.6 us), which saves every column slab the k products of
 // each pair (4096 tokens of 10: dW alone 29 against 36 us).
 constexpr long kPairsMax = 4096;
+// Blocks of the dx role in a launch (its threads are counted in 32 bits; 2^26
+// tokens of 64 columns are 2^24 blocks).  A loop in the kernel instead cost a
+// prompt 0.8 us.
+constexpr unsigned kMaxXBlocks = 1u << 22;
 
 struct GradArgs {
   const uint16_t* x;
@@ -50,6 +54,7 @@ struct GradArgs {
   float* dbias;
   int T, d, E, k;
   unsigned blocks_e, blocks_w;  // blocks of row E, of the expert rows; the rest: dx
+  unsigned block0_x;            // this launch's first one of dx
 };
 
 __device__ __forceinline__ float gate_grad(const GradArgs& a, int t) {
@@ -292,6 +297,7 @@ __global__ __launch_bounds__(kThreads, G ? 8 : 5) void router_grad_kernel(GradAr
     return;
   }
   b -= a.blocks_w;
+  b += a.block0_x;
   const int slabs = (a.d + kXCols - 1) / kXCols;
   const int t = (int)(b / slabs) * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (t < a.T) token_x<G>(a, t, (int)(b % slabs));
@@ -326,7 +332,7 @@ extern "C" int moe_router_topk_backward(const uint16_t* x, int32_t T, int32_t d,
   }
   MOE_CHECK(aligned(x, 16) && aligned(W, 16) && aligned(dx, 16) && aligned(dW, 16) && aligned(ws, 256));
   MOE_CHECK(T == 0 || ws_bytes >= pairs_bytes(T, k));
-  GradArgs a{x, W, idx, w, sgate, dw, dsgate, offsets, pair_ids, nullptr, dx, dW, dbias, T, d, E, k, 0, 0};
+  GradArgs a{x, W, idx, w, sgate, dw, dsgate, offsets, pair_ids, nullptr, dx, dW, dbias, T, d, E, k, 0, 0, 0};
   if ((long)T * k > kPairsMax) {
     float* g = static_cast<float*>(ws);
     const long blocks = ((long)T * (k + 1) + 255) / 256;
@@ -338,12 +344,17 @@ extern "C" int moe_router_topk_backward(const uint16_t* x, int32_t T, int32_t d,
   const int cols = w_cols(a.g != nullptr);
   a.blocks_w = dW ? (unsigned)(E * ((d + cols - 1) / cols)) : dbias ? (unsigned)E : 0;
   const unsigned blocks_x = dx ? (unsigned)((T + kWaves - 1) / kWaves) * (unsigned)((d + kXCols - 1) / kXCols) : 0;
-  const unsigned blocks = a.blocks_e + a.blocks_w + blocks_x;
-  if (blocks == 0) return MOE_OK;               // dx of no tokens
-  if (a.g)
-    router_grad_kernel<true><<<blocks, kThreads, 0, s>>>(a);
-  else
-    router_grad_kernel<false><<<blocks, kThreads, 0, s>>>(a);
-  MOE_HIP(hipGetLastError());
+  do {
+    const unsigned n = blocks_x - a.block0_x < kMaxXBlocks ? blocks_x - a.block0_x : kMaxXBlocks;
+    const unsigned blocks = a.blocks_e + a.blocks_w + n;
+    if (blocks == 0) return MOE_OK;             // dx of no tokens
+    if (a.g)
+      router_grad_kernel<true><<<blocks, kThreads, 0, s>>>(a);
+    else
+      router_grad_kernel<false><<<blocks, kThreads, 0, s>>>(a);
+    MOE_HIP(hipGetLastError());
+    a.blocks_e = a.blocks_w = 0;
+    a.block0_x += n;
+  } while (a.block0_x < blocks_x);
   return MOE_OK;
 }

@@ -151,6 +151,27 @@ def test_router_gradient_without_a_gate_gradient(T):
         assert (got[0][3] == 0).all()
 
 
+def test_router_gradient_of_more_tokens_than_blocks():
+    """dx of 2^26 tokens and some (2^24 blocks of four if each had its own,
+    more threads than a launch counts), offsets past 2^32 elements.  One expert
+    a token, so g = w (dw - w dw) and dx = g W[e] + g_s W[E]: two products and
+    a sum on values off as in the tolerance above, 8 u of the magnitudes."""
+    T, d, E = (1 << 26) + 5, 64, 2
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.rand(*s, generator=gen, device="cuda")
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    W, w, s, dw, ds = rand(E + 1, d) - 0.5, rand(T, 1), rand(T), rand(T, 1) - 0.5, rand(T) - 0.5
+    idx = torch.randint(0, E, (T, 1), generator=gen, device="cuda", dtype=torch.int32)
+    dx = torch.full((T, d), float("nan"), device="cuda")
+    moe.moe_router_topk_backward(x, W, idx, w, s, dw, ds, None, None, out=(dx, None, None))
+    for a in range(0, T, 1 << 22):
+        b = min(T, a + (1 << 22))
+        wd, dwd, sd, dsd, Wd = (t.double() for t in (w[a:b], dw[a:b], s[a:b, None], ds[a:b, None], W))
+        g, gs, We = wd * (dwd - wd * dwd), dsd * (sd - sd * sd), Wd[idx[a:b, 0].long()]
+        mag = wd * (dwd.abs() + (wd * dwd).abs()) * We.abs() + gs.abs() * Wd[E].abs()
+        assert ((dx[a:b].double() - (g * We + gs * Wd[E])).abs() <= 8 * U * mag).all(), a
+
+
 def test_router_gradient_in_a_graph_and_on_a_stream():
     T, d, E, k = 150, 256, 12, 3
     x, bits, W, idx, w, s, dw, ds = _inputs(T, d, E, k, skew=True)
