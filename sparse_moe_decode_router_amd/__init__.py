@@ -674,8 +674,10 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 # ------------------------------------------- rows in expert order, and back
 # These entry points check their tensors (ValueError), run on the tensors'
 # device whatever the current one, and allocate what they return on the
-# stream that they launch on.  The checks and the call itself are in
-# csrc/binding.cpp.
+# stream that they launch on.  Buffers with rows that a call may leave as they
+# were (behind the last bucket) are allocated as zeros, which costs a fill of
+# the buffer; give out= to keep buffers from call to call and spare it.  The
+# checks and the call itself are in csrc/binding.cpp.
 _rowops.bind(*(C.cast(getattr(_lib, _n), C.c_void_p).value for _n in (
     "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_combine",
     "moe_unsort_combine_backward", "moe_linear_bytes", "moe_linear_int4", "moe_expert_linear_int4",
@@ -708,7 +710,8 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
     """Token rows x [T, d] (float32, bfloat16 or float16) in expert order.
     Returns (x_sorted [T*k, d], offsets int32 [E+1], pair_ids int32 [T*k],
     row_of int32 [T, k]); rows of x_sorted and entries of pair_ids from
-    offsets[E] on keep what they held (out: that tuple, to write into)."""
+    offsets[E] on keep what they held (out: that tuple, to write into), or are
+    zeros and -1 in buffers allocated here."""
     if stream is not None:
         with _stream_of(x, stream):
             return moe_sort_tokens(x, topk_idx, E, workspace, out)
@@ -716,8 +719,8 @@ def moe_sort_tokens(x, topk_idx, E: int, workspace=None, out=None, stream=None):
         (T, d), k = _matrix(x, "x"), _matrix(topk_idx, "topk_idx")[1]
         if out is None:
             i32 = dict(dtype=torch.int32, device=x.device)
-            out = (torch.empty((T * k, d), dtype=x.dtype, device=x.device), torch.empty((max(E, 0) + 1,), **i32),
-                   torch.empty((T * k,), **i32), torch.empty((T, k), **i32))
+            out = (torch.zeros((T * k, d), dtype=x.dtype, device=x.device), torch.empty((max(E, 0) + 1,), **i32),
+                   torch.full((T * k,), -1, **i32), torch.empty((T, k), **i32))
         if workspace is None:
             workspace = torch.empty(moe_sort_workspace_bytes(T, k, E), dtype=torch.uint8, device=x.device)
     rows, offsets, pairs, row_of = out
@@ -759,13 +762,14 @@ def moe_unsort_combine(rows, row_of, topk_w, shared_out=None, shared_gate=None, 
 def moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out=None, shared_gate=None, out=None, stream=None):
     """Gradients of moe_unsort_combine from dy [T, d]: (drows [T*k, d], dtopk_w
     fp32 [T, k], dshared_out [T, d], dshared_gate fp32 [T]), the last two None
-    without shared rows; rows of drows that no pair has keep what they held."""
+    without shared rows; rows of drows that no pair has keep what they held, or
+    are zeros where drows is allocated here."""
     if stream is not None:
         with _stream_of(rows, stream):
             return moe_unsort_combine_backward(dy, rows, row_of, topk_w, shared_out, shared_gate, out)
     if out is None:
         (T, k), has = _matrix(row_of, "row_of"), shared_out is not None
-        out = (torch.empty_like(rows), torch.empty((T, k), dtype=torch.float32, device=rows.device),
+        out = (torch.zeros_like(rows), torch.empty((T, k), dtype=torch.float32, device=rows.device),
                torch.empty_like(shared_out) if has else None,
                torch.empty((T,), dtype=torch.float32, device=rows.device) if has else None)
     st = _rowops.unsort_grad(dy, rows, row_of, topk_w, shared_out, shared_gate, *out)
@@ -848,12 +852,12 @@ def moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out: int, gr
     order, offsets int32 [E+1]) times its expert's matrix.  packed uint8
     [n_slots, bytes] (rows may be apart: a view into larger blobs), slot_table
     int32 [E] or None (expert e in slot e); error: int32 [1] or None.  Rows
-    from offsets[E] on keep what they held."""
+    from offsets[E] on keep what they held, or are zeros in a y allocated here."""
     if stream is not None:
         with _stream_of(x_sorted, stream):
             return moe_expert_linear_int4(packed, slot_table, x_sorted, offsets, n_out, group, error, out)
     if out is None:
-        out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
+        out = torch.zeros((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
     st = _rowops.expert_linear(packed, slot_table, x_sorted, offsets, n_out, group, out, error)
     if st:
         _check(st, "moe_expert_linear_int4")
@@ -869,7 +873,7 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
         with _stream_of(x_sorted, stream):
             return moe_pool_linear_int4(pool, matrix, x_sorted, offsets, out)
     if out is None:
-        out = torch.empty((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
+        out = torch.zeros((_matrix(x_sorted, "x_sorted")[0], n_out), dtype=torch.float32, device=x_sorted.device)
     st = _rowops.pool_linear(pool.handle.value, _MATS.index(matrix), n_in, n_out, pool.E, x_sorted, offsets, out)
     if st:
         _check(st, "moe_pool_linear_int4")

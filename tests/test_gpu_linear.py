@@ -262,6 +262,17 @@ def test_pool_matrices():
     assert L.pool.check_error() == moe.MOE_ERR_NOT_RESIDENT
 
 
+def test_pool_rows_behind_the_last_bucket():
+    L = DeviceLayer(ms.CONFIGS["tiny"])
+    cfg = L.cfg
+    X = torch.zeros(50, cfg.d, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(cfg.E + 1, dtype=torch.int32, device="cuda")
+    off[1:] = 7                                       # rows 7 to 49 belong to no expert
+    left = torch.full((50, cfg.I), float("nan"), device="cuda")
+    del left
+    assert (moe.moe_pool_linear_int4(L.pool, "gate", X, off) == 0).all()
+
+
 def test_refusals_on_the_device():
     L8 = DeviceLayer(ms.CONFIGS["tiny_int8"])
     X = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")

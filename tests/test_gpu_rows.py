@@ -211,6 +211,32 @@ def test_streams_and_graphs(T):
         assert all(torch.equal(a, b) for a, b in zip(got, step())), rep
 
 
+def _leave_behind(*shape, dtype=torch.float32):
+    """A freed block of that size full of values nobody should see."""
+    del_me = torch.full(shape, float("nan") if dtype.is_floating_point else 1 << 30, dtype=dtype, device="cuda")
+    del del_me
+
+
+def test_rows_behind_the_last_bucket_of_allocated_outputs():
+    """Buffers that the calls allocate: zeros in the rows (and -1 in the pair
+    list) that no pair has, not what the memory held before."""
+    T, k, E, d, n_out = 300, 4, 8, 576, 40
+    idx = torch.randint(0, E, (T, k), device="cuda", dtype=torch.int32)
+    idx[200:] = -1
+    x, live = torch.randn(T, d, device="cuda").bfloat16(), 800
+    _leave_behind(T * k, d, dtype=torch.bfloat16)
+    _leave_behind(T * k, dtype=torch.int32)
+    X, off, pairs, row = moe.moe_sort_tokens(x, idx, E)
+    assert int(off[E]) == live and (X[live:] == 0).all() and (pairs[live:] == -1).all() and (pairs[:live] >= 0).all()
+    _leave_behind(T * k, d, dtype=torch.bfloat16)
+    dX = moe.moe_unsort_combine_backward(x, X, row, torch.rand(T, k, device="cuda"))[0]
+    assert (dX[live:] == 0).all()
+    packed = torch.zeros(E, moe.moe_linear_bytes(d, n_out), dtype=torch.uint8, device="cuda")
+    _leave_behind(T * k, n_out)
+    y = moe.moe_expert_linear_int4(packed, None, X, off, n_out)
+    assert (y == 0).all()
+
+
 def test_more_than_2_31_elements():
     """Rows past 4 GiB and 2^31 elements.  Sixteen equal bf16 rows sum to an
     exact sixteenfold, and with weights of 1/16 to the row itself."""
