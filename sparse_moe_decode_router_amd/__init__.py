@@ -676,8 +676,11 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 # device whatever the current one, and allocate what they return on the
 # stream that they launch on.  Buffers with rows that a call may leave as they
 # were (behind the last bucket) are allocated as zeros, which costs a fill of
-# the buffer; give out= to keep buffers from call to call and spare it.  The
-# checks and the call itself are in csrc/binding.cpp.
+# the buffer; give out= to keep buffers from call to call and spare it.  Nothing
+# is recorded for autograd: a tensor that requires a gradient is refused in grad
+# mode (call under torch.no_grad(), or from a torch.autograd.Function with the
+# *_backward call as its backward).  The checks and the call itself are in
+# csrc/binding.cpp.
 _rowops.bind(*(C.cast(getattr(_lib, _n), C.c_void_p).value for _n in (
     "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_combine",
     "moe_unsort_combine_backward", "moe_linear_bytes", "moe_linear_int4", "moe_expert_linear_int4",

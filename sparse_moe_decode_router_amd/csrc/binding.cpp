@@ -1,7 +1,7 @@
 // Tensor arguments of the row operators, 4-bit products and the router's
 // gradient: a CPython module that checks each torch tensor (device, type,
-// shape, contiguity; ValueError otherwise) and calls the C ABI with its
-// address.  The same checks in Python cost 0.4 us a tensor, more than half of
+// shape, contiguity, no gradient to record; ValueError otherwise) and calls the
+// C ABI with its address.  The same checks in Python cost 0.4 us a tensor, more than half of
 // a small call (nine tensors against a launch of 2.7 us); here about 0.03.
 //
 // The module holds no library of its own: bind() takes the addresses of the
@@ -11,6 +11,7 @@
 #include <initializer_list>
 #include <string>
 
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -52,6 +53,18 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// The calls record nothing for autograd: a tensor whose gradient or tangent
+// would be lost without a word is refused.  The backward calls are there for
+// torch.autograd.Function, whose forward and backward run without grad mode.
+void no_gradient(const at::Tensor& v, const char* name) {
+  const bool tangent = v._fw_grad(0).defined();
+  if (!tangent && !(v.requires_grad() && c10::GradMode::is_enabled())) return;
+  PyErr_Format(PyExc_ValueError, "%s: carries a %s, which this call does not record; detach it, or call under "
+               "torch.no_grad() or from a torch.autograd.Function",
+               name, tangent ? "forward-mode tangent" : "gradient (requires_grad)");
+  throw PyError{};
+}
+
 // The address of a contiguous tensor of that type and shape on device dev.
 void* need(const at::Tensor& v, const char* name, at::ScalarType type, Shape shape, int dev) {
   const c10::IntArrayRef want(shape.begin(), shape.size());
@@ -61,6 +74,7 @@ void* need(const at::Tensor& v, const char* name, at::ScalarType type, Shape sha
                  text(v.sizes()).c_str(), v.device().str().c_str(), text(v.strides()).c_str());
     throw PyError{};
   }
+  no_gradient(v, name);
   return v.data_ptr();
 }
 template <class T>

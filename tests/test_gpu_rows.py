@@ -279,3 +279,74 @@ def test_tensors_that_do_not_fit_are_refused():
                  lambda: moe.moe_sort_tokens(x, idx, 4, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))]:
         with pytest.raises(moe.MoeError):
             call()
+
+
+def _calls():
+    """Each call of this kind as (name, function of float tensors by name)."""
+    T, k, E, d = 6, 2, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = r(T, d)
+    _, off, pairs, row = moe.moe_sort_tokens(x, idx, E)
+    packed = torch.zeros(E, moe.moe_linear_bytes(d, 8), dtype=torch.uint8, device="cuda")
+    rows, w, sg, b16 = r(T * k, d), r(T, k), r(T), lambda *s: r(*s).bfloat16()
+    return [
+        (lambda x: moe.moe_sort_tokens(x, idx, E)[0], dict(x=x)),
+        (lambda dx: moe.moe_sort_tokens_backward(dx, row), dict(dx=rows)),
+        (lambda y, w, s, g: moe.moe_unsort_combine(y, row, w, s, g), dict(y=rows, w=w, s=x, g=sg)),
+        (lambda dy, y, w, s, g: moe.moe_unsort_combine_backward(dy, y, row, w, s, g)[0],
+         dict(dy=x, y=rows, w=w, s=x.clone(), g=sg)),
+        (lambda x: moe.moe_linear_int4(packed[0], x, 8), dict(x=b16(T, d))),
+        (lambda x, out: moe.moe_linear_int4(packed[0], x, 8, out=out), dict(x=b16(T, d), out=r(T, 8))),
+        (lambda x: moe.moe_expert_linear_int4(packed, None, x, off, 8), dict(x=b16(T * k, d))),
+        (lambda x, W, w, s, dw, ds: moe.moe_router_topk_backward(x, W, idx, w, s, dw, ds, off, pairs)[0],
+         dict(x=b16(T, d), W=r(E + 1, d), w=w, s=sg, dw=r(T, k), ds=r(T))),
+    ]
+
+
+def test_tensors_whose_gradient_would_be_lost_are_refused():
+    import torch.autograd.forward_ad as fwd
+    for f, args in _calls():
+        want = f(**args)
+        for name, v in args.items():
+            leaf = dict(args, **{name: v.clone().requires_grad_()})
+            with pytest.raises(ValueError, match="requires_grad"):
+                f(**leaf)
+            with torch.no_grad():
+                assert torch.equal(f(**leaf), want)
+            with fwd.dual_level(), pytest.raises(ValueError, match="tangent"):
+                f(**dict(args, **{name: fwd.make_dual(v.clone(), torch.ones_like(v))}))
+
+
+def test_sort_and_way_back_as_an_autograd_function():
+    """The calls as forward and backward of a torch.autograd.Function, against
+    autograd of the same in fp64; tolerance as above: dx is a sum of k rounded
+    products, dw one of d products."""
+    T, k, E, d = 50, 3, 6, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+
+    class Route(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w):
+            X, _, _, row = moe.moe_sort_tokens(x, idx, E)
+            ctx.save_for_backward(X, row, w)
+            return moe.moe_unsort_combine(X, row, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            X, row, w = ctx.saved_tensors
+            dX, dw, _, _ = moe.moe_unsort_combine_backward(dy.contiguous(), X, row, w)
+            return moe.moe_sort_tokens_backward(dX, row), dw
+
+    x = torch.randn(T, d, generator=g, device="cuda").requires_grad_()
+    w = torch.randn(T, k, generator=g, device="cuda").requires_grad_()
+    dy = torch.randn(T, d, generator=g, device="cuda")
+    (Route.apply(x, w) * dy).sum().backward()
+    x64, w64 = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
+    ((w64.sum(1, keepdim=True) * x64) * dy.double()).sum().backward()
+    live_x = (w64.abs().sum(1, keepdim=True) * dy.double().abs()).detach()
+    live_w = (x64.abs() * dy.double().abs()).sum(1, keepdim=True).detach()
+    assert ((x.grad.double() - x64.grad).abs() <= (k + 2) * U * live_x).all()
+    assert ((w.grad.double() - w64.grad).abs() <= (d + 2) * U * live_w).all()
