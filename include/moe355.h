@@ -169,6 +169,7 @@ int32_t* moe_pool_slot_table(const moe_pool* pool);     /* device, [E] */
 uint32_t* moe_pool_usage(const moe_pool* pool);         /* device, [E] */
 int32_t moe_pool_num_experts(const moe_pool* pool);
 int32_t moe_pool_num_slots(const moe_pool* pool);
+int32_t moe_pool_device(const moe_pool* pool);          /* its memory's; -1: no pool */
 
 /* Copy one blob into a slot and make `expert` resident there (evicting any
  * previous holder of the slot).  blob is host memory (pinned for a truly
@@ -561,7 +562,8 @@ int moe_expert_linear_int4(const moe_linear_shape* sh, const void* packed_dev,
                            const int32_t* offsets_dev, float* y_sorted_dev,
                            int32_t* error_dev, hipStream_t stream);
 /* The same with a matrix (0 gate, 1 up, 2 down) of the blobs in a pool, through
- * its slot table and error word; 4-bit pools (others MOE_ERR_UNSUPPORTED). */
+ * its slot table and error word; 4-bit pools (others MOE_ERR_UNSUPPORTED), with
+ * the pool's device current (MOE_ERR_INVALID_ARG otherwise). */
 int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix,
                          const uint16_t* x_sorted_dev, int32_t N,
                          const int32_t* offsets_dev, float* y_sorted_dev,

@@ -106,6 +106,7 @@ _SIGS = {
     "moe_pool_usage": (_P, [_P]),
     "moe_pool_num_experts": (_I, [_P]),
     "moe_pool_num_slots": (_I, [_P]),
+    "moe_pool_device": (_I, [_P]),
     "moe_pool_load": (C.c_int, [_P, _I, _I, _P, _P]),
     "moe_pool_load_device": (C.c_int, [_P, _I, _I, _P, _P]),
     "moe_pool_plan": (C.c_int, [_P, _P, _I, _P, _P, _P, _P]),
@@ -319,6 +320,7 @@ class Pool:
         _check(_lib.moe_pool_create(E, n_slots, C.byref(shape(d, I, bits)), C.byref(h)), "moe_pool_create")
         self.handle = h
         self.stride = int(_lib.moe_pool_stride(h))
+        self.device = int(_lib.moe_pool_device(h))
 
     def close(self):
         if self.handle:
@@ -872,6 +874,8 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
     if matrix not in _MATS:
         raise ValueError(f"matrix must be one of {_MATS}")
     n_in, n_out = (pool.I, pool.d) if matrix == "down" else (pool.d, pool.I)
+    if isinstance(x_sorted, torch.Tensor) and x_sorted.is_cuda and x_sorted.get_device() != pool.device:
+        raise ValueError(f"x_sorted is on cuda:{x_sorted.get_device()}, the pool on cuda:{pool.device}")
     if stream is not None:
         with _stream_of(x_sorted, stream):
             return moe_pool_linear_int4(pool, matrix, x_sorted, offsets, out)

@@ -307,6 +307,7 @@ extern "C" int moe_lfu_plan(moe_lfu* p, const int32_t* sel, int32_t n, int32_t* 
 // ------------------------------------------------------------------- pool
 struct moe_pool {
   int32_t E = 0, n_slots = 0;
+  int device = 0;               // that the memory below is on
   moe_ffn_shape sh{};
   size_t stride = 0;
   uint8_t* slab = nullptr;
@@ -395,6 +396,7 @@ bool pool_view(const moe_pool* p, PoolView* v) {
   v->slot_table = p->table;
   v->err = p->err;
   v->E = p->E;
+  v->device = p->device;
   return true;
 }
 bool pool_shape(const moe_pool* p, moe_ffn_shape* sh) {
@@ -421,7 +423,8 @@ extern "C" int moe_pool_create(int32_t E, int32_t n_slots, const moe_ffn_shape* 
     p->stride = blob_layout(sh->d, sh->I, shape_bits(sh)).stride;
     p->lfu.E = E;
     p->lfu.n_slots = n_slots;
-    hipError_t e = hipMalloc(&p->slab, p->stride * (size_t)n_slots);
+    hipError_t e = hipGetDevice(&p->device);
+    if (e == hipSuccess) e = hipMalloc(&p->slab, p->stride * (size_t)n_slots);
     if (e == hipSuccess) e = hipMalloc(&p->table, sizeof(int32_t) * E);
     if (e == hipSuccess) e = hipMalloc(&p->usage, sizeof(uint32_t) * E);
     if (e == hipSuccess) e = hipMalloc(&p->err, 256);
@@ -459,6 +462,7 @@ extern "C" int32_t* moe_pool_slot_table(const moe_pool* p) { return p ? p->table
 extern "C" uint32_t* moe_pool_usage(const moe_pool* p) { return p ? p->usage : nullptr; }
 extern "C" int32_t moe_pool_num_experts(const moe_pool* p) { return p ? p->E : 0; }
 extern "C" int32_t moe_pool_num_slots(const moe_pool* p) { return p ? p->n_slots : 0; }
+extern "C" int32_t moe_pool_device(const moe_pool* p) { return p ? p->device : -1; }
 
 static void host_place(moe_lfu* p, int32_t e, int32_t slot, std::vector<int32_t>* te,
                        std::vector<int32_t>* ts) {

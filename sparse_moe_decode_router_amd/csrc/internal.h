@@ -61,6 +61,7 @@ struct PoolView {
   const int32_t* slot_table;
   int32_t* err;
   int32_t E;
+  int device;                   // that all of it is on
 };
 bool pool_view(const moe_pool* p, PoolView* v);
 bool pool_shape(const moe_pool* p, moe_ffn_shape* sh);

@@ -523,6 +523,9 @@ extern "C" int moe_pool_linear_int4(const moe_pool* pool, int32_t matrix, const 
   moe_ffn_shape fs;
   PoolView v;
   MOE_CHECK(pool_view(pool, &v) && pool_shape(pool, &fs));
+  int dev = -1;
+  MOE_HIP(hipGetDevice(&dev));
+  MOE_CHECK(dev == v.device);                   // another device would read the pool's memory as its own
   if (shape_bits(&fs) != 4) return MOE_ERR_UNSUPPORTED;
   const moe_linear_shape sh{matrix == 2 ? fs.I : fs.d, matrix == 2 ? fs.d : fs.I, 64};
   // a blob's matrix is its codes followed by its (scale, bias) words: the layout of one packed matrix

@@ -273,6 +273,19 @@ def test_pool_rows_behind_the_last_bucket():
     assert (moe.moe_pool_linear_int4(L.pool, "gate", X, off) == 0).all()
 
 
+def test_a_pool_of_another_device_is_refused():
+    """The pool's device is compared before the launch (a pool that claims
+    another device: nothing runs)."""
+    L = DeviceLayer(ms.CONFIGS["tiny"])
+    X = torch.zeros(4, L.cfg.d, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(L.cfg.E + 1, dtype=torch.int32, device="cuda")
+    assert L.pool.device == X.get_device()
+    moe.moe_pool_linear_int4(L.pool, "gate", X, off)
+    L.pool.device = X.get_device() + 1
+    with pytest.raises(ValueError, match="the pool on"):
+        moe.moe_pool_linear_int4(L.pool, "gate", X, off)
+
+
 def test_refusals_on_the_device():
     L8 = DeviceLayer(ms.CONFIGS["tiny_int8"])
     X = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
