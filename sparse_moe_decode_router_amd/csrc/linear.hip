@@ -385,15 +385,20 @@ int by_rows(LinArgs a, hipStream_t s) {
     a.chunks = chunks(64, true);
     return launch<GROUP, 4, 4, 1, EXP, false>(a, t16 / 4 * wide >= 1024 ? 1 : 4, wide, s);
   }
-  // rows a chunk: 16, or fewer for experts with few rows if x then fits LDS
+  // rows a chunk: 16, or fewer for experts with few rows where x then fits LDS
+  // and is held there; smaller chunks only read the matrix of a full bucket
+  // more often (64 tokens, 8 of 256 experts, Zipf 1: 4096 x 2048 131 us with 16
+  // rows, 164 with 4, 4096 x 512 28.5 against 44.6; even routing 249 and 247)
   constexpr size_t kXlMax = 32768;
+  const auto fits = [&](int size) { return x_lds_bytes(a.N < size ? (int)a.N : size, a.n_in) <= kXlMax; };
   a.size = 16;
   if (EXP)
     while (a.size > 4 && a.size >= 4 * rows && x_lds_bytes(a.size, a.n_in) > kXlMax) a.size /= 2;
+  // (a few blocks only wait longer for it: ten expert rows 7.1 against 7.6)
+  const bool xl = t16 * chunks(a.size, false) > 512 && fits(a.size);
+  if (!xl) a.size = 16;
   a.chunks = chunks(a.size, true);
   const long likely = chunks(a.size, false), units = t16 * likely;
-  // (a few blocks only wait longer for it: ten expert rows 7.1 against 7.6)
-  const bool xl = units > 512 && x_lds_bytes(a.N < a.size ? (int)a.N : a.size, a.n_in) <= kXlMax;
   if (xl && rows <= 8 && units > 4096) return launch<GROUP, 1, 2, EXP ? 3 : 2, EXP, true>(a, 1, likely, s);
   if (EXP && units > 16384)
     return xl ? launch<GROUP, 1, 4, 2, EXP, true>(a, 1, likely, s) : launch<GROUP, 1, 4, 2, EXP, false>(a, 1, likely, s);
