@@ -528,9 +528,13 @@ int moe_unsort_combine_backward(const void* dy_dev, const void* rows_dev,
  * [n_in/group][n_out], the layout of one matrix of an expert blob.  n_in a
  * multiple of group, up to 65536; n_out 1 to 2^24; a matrix below 4 GiB; packed
  * matrices 4-byte and x 16-byte aligned.  x bf16, y fp32: every product exact, sums in fp32 in a
- * fixed order that depends on the sizes alone (values of x below 2^115: a
- * group's sum of 16 + code times x must stay finite).  A row of x that is not
- * finite gives a row of y that is not, and touches no other. */
+ * fixed order that depends on the sizes alone.  A group's share is formed as
+ * scale sum((16 + code) x) + (bias - 16 scale) sum(x), so fp32 has to hold the
+ * sums of these magnitudes, not only their difference: with m the largest |x|
+ * of a row, 31 group m and, over all groups, the sum of (31 |scale| +
+ * |bias - 16 scale|) group m below 2^127 (scales up to 16 with biases up to 128:
+ * |x| up to 2^100).  Past it a row may come out infinite or NaN.  A row of x
+ * that is not finite gives a row of y that is not, and touches no other. */
 typedef struct moe_linear_shape {
   int32_t n_in, n_out;
   int32_t group;

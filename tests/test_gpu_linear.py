@@ -134,6 +134,31 @@ def test_linear_small_and_large_values():
     _check(y, x * scale, (c, s, b))
 
 
+@pytest.mark.parametrize("T,n_in,n_out,group", [(3, 1024, 40, 128), (3, 65536, 17, 32), (20, 512, 8200, 64), (70, 256, 16500, 32)])
+def test_linear_at_the_largest_values(T, n_in, n_out, group):
+    """Scales up to 16 and biases up to 128 against the largest x that the
+    documented bound admits, the sums of magnitudes just below 2^127; the first
+    rows of W are zeros made of the largest scale (16 * 8 - 128)."""
+    rng = np.random.default_rng([T, n_in])
+    c, s, b = _matrix(rng, n_out, n_in, group)
+    s = (s.astype(np.float32) * 800).astype(np.float16)
+    b = (-8 * s.astype(np.float32)).astype(np.float16)
+    c[:4], s[:4], b[:4] = 8, 16.0, -128.0
+    assert s.max() <= 16 and np.abs(b).max() <= 128
+    x, _ = _x(rng, T, n_in)
+    x = np.sign(x) * np.exp2(np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -8))))
+    x[0] = 1.0                                          # every term of the same sign
+    s64, b64 = s.astype(np.float64), b.astype(np.float64)
+    per = ((31 * np.abs(s64) + np.abs(b64 - 16 * s64)).sum(1).max()) * group * np.abs(x).max(1)
+    x *= np.exp2(126 - np.ceil(np.log2(per)))[:, None]
+    assert (per * np.exp2(126 - np.ceil(np.log2(per))) < 2.0 ** 127).all() and np.abs(x).max() > 2.0 ** 95
+    xd = torch.from_numpy(x.astype(np.float32)).cuda().bfloat16()
+    assert np.array_equal(xd.double().cpu().numpy(), x)
+    y = moe.moe_linear_int4(torch.from_numpy(moe.moe_pack_linear_int4(c, s, b)).cuda(), xd, n_out, group)
+    _check(y, x, (c, s, b))
+    assert (y[0, :4] == 0).all()                        # equal terms: the two sums cancel exactly
+
+
 def test_linear_no_rows_and_non_finite_rows():
     rng = np.random.default_rng(3)
     m = _matrix(rng, 40, 256, 64)
