@@ -72,6 +72,67 @@ def _packed_f64(w, n_in, n_out, group):
     return q, s, b
 
 
+def _device_matrices(g, lead, n_in, n_out, group):
+    """Random packed matrices made on the device, scales as in _matrix."""
+    nb = n_in * n_out // 2
+    w = torch.randint(0, 256, (lead, moe.moe_linear_bytes(n_in, n_out, group)), dtype=torch.uint8, generator=g, device="cuda")
+    s = torch.empty(lead, n_in // group, n_out, device="cuda").uniform_(0.002, 0.02, generator=g)
+    b = -8 * s * torch.empty_like(s).uniform_(0.9, 1.1, generator=g)
+    w[:, nb:] = torch.stack([s, b], -1).half().view(lead, -1).view(torch.uint8)
+    return w
+
+
+def _check_on_device(y, x, w, n_in, n_out, group, what=""):
+    q, s, b = _packed_f64(w, n_in, n_out, group)
+    mag = x.double().abs() @ (s.abs() * (16 + q) + (b - 16 * s).abs()).t()
+    err = (y.double() - x.double() @ (s * q + b).t()).abs()
+    assert (err <= (128 + 3 + n_in // group + 16) * 2.0 ** -23 * mag).all(), what
+
+
+# Sizes by the form that they take: weight rows a wave (16 or 32 or 64), rows of
+# x a chunk, shares of the inputs joined through LDS, x in LDS, two tiles a block.
+@pytest.mark.parametrize("T,n_in,n_out,group", [
+    (2, 96, 4187, 32), (5, 512, 4210, 64), (7, 1152, 4157, 64),             # 32 weight rows; 1, 2, 4 shares
+    (3, 288, 8201, 32), (6, 1024, 8442, 64), (7, 2048, 8917, 64),           # and x in LDS; 2, 4, 8 shares
+    (33, 1024, 2827, 128), (19, 1024, 4121, 32),                            # 64 weight rows; 4, 8 shares
+    (36, 256, 2738, 32), (50, 512, 2192, 32), (10, 1152, 9163, 32), (12, 1024, 16390, 64),      # and x in LDS
+    (72, 288, 9603, 32), (200, 1024, 4100, 64), (65, 2176, 8200, 128)])     # 64 rows of x; 2, 4, 4 shares
+def test_linear_forms(T, n_in, n_out, group):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = _device_matrices(g, 1, n_in, n_out, group)[0]
+    x = torch.randn(T, n_in, generator=g, device="cuda").bfloat16()
+    _check_on_device(moe.moe_linear_int4(w, x, n_out, group), x, w, n_in, n_out, group)
+
+
+@pytest.mark.parametrize("N,n_in,n_out,group,E", [
+    (9, 384, 5, 32, 3), (40, 1088, 33, 64, 9), (70, 4224, 40, 128, 30),      # 16 weight rows; 2, 4, 8 shares
+    (460, 32, 1, 32, 276), (654, 256, 3, 32, 268), (473, 512, 5, 32, 449), (2866, 1120, 7, 32, 152),    # 32; 1, 2, 4, 8
+    (590, 64, 9, 64, 601), (661, 256, 12, 32, 516), (991, 512, 16, 32, 657), (5, 1536, 9609, 32, 1),   # and x in LDS
+    (417, 2048, 36, 128, 393), (737, 1152, 1, 64, 585), (643, 2048, 15, 32, 546), (1541, 1088, 3, 32, 522),  # chunks of 4, 8
+    (91, 2048, 1076, 64, 63), (20, 1024, 8300, 64, 10), (1432, 32, 272, 32, 764),   # no shares; chunks of 4, 8, 16
+    (9, 2048, 37760, 32, 7), (19, 1024, 14287, 32, 19),                     # two tiles a block; chunks of 4, 8
+    (512, 128, 2056, 64, 256), (512, 2048, 520, 64, 256), (512, 4096, 520, 64, 256), (768, 2048, 530, 64, 256),
+    (2724, 1216, 21, 64, 135), (3919, 1216, 17, 32, 166), (21, 1024, 105927, 128, 5),      # 64 weight rows
+    (3830, 288, 17, 32, 232), (35, 512, 2184, 32, 2), (13, 1184, 12309, 32, 1), (3674, 32, 1031, 32, 229),    # and x in LDS
+    (3217, 256, 250, 32, 16), (417, 608, 1578, 32, 11), (359, 32, 47761, 32, 11)])        # 64 rows of x
+def test_expert_forms(N, n_in, n_out, group, E):
+    """Buckets from empty to many chunks, and rows behind the last one."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w = _device_matrices(g, E, n_in, n_out, group)
+    x = torch.randn(N, n_in, generator=g, device="cuda").bfloat16()
+    rng = np.random.default_rng(N)
+    p = rng.permutation(1.0 / np.arange(1, E + 1) ** 1.2)
+    counts = rng.multinomial(N - N // 9, p / p.sum())
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    slots = rng.permutation(E).astype(np.int32)
+    out = torch.full((N, n_out), float("nan"), device="cuda")
+    y = moe.moe_expert_linear_int4(w, torch.from_numpy(slots).cuda(), x, torch.from_numpy(off).cuda(), n_out, group,
+                                   out=out)
+    for e in np.nonzero(counts)[0]:
+        _check_on_device(y[off[e]:off[e + 1]], x[off[e]:off[e + 1]], w[int(slots[e])], n_in, n_out, group, (e, counts[e]))
+    assert torch.isnan(y[off[-1]:]).all()
+
+
 def test_experts_whose_rows_do_not_fit_lds():
     """Long rows and many experts (280 MB of matrices, random bytes made on the
     device): sampled experts against fp64, same tolerance."""
