@@ -211,6 +211,34 @@ def test_streams_and_graphs(T):
         assert all(torch.equal(a, b) for a, b in zip(got, step())), rep
 
 
+@pytest.mark.parametrize("T,k,E,d,skew", [
+    (104857, 10, 512, 2, False), (65536, 16, 32, 3, False),       # up to 2^20 pairs, 4096 a block
+    (200003, 2, 1024, 1, False), (131072, 8, 64, 1, True),        # one expert of most pairs
+    (65537, 16, 40, 1, False)])                                   # one token past one launch
+def test_sort_of_many_pairs(T, k, E, d, skew):
+    """The sort near the border of one launch, which has two counters an expert
+    and up to 64 rounds of ranks a block: whole numbers and copies are equal."""
+    g = np.random.default_rng([T, k])
+    idx = g.integers(0, E, (T, k)).astype(np.int32)
+    if skew:
+        idx[g.random((T, k)) < 0.9] = E - 3
+    idx[g.random((T, k)) < 0.1] = -1
+    idx[-1], idx[T // 2] = E, -7
+    n, key = T * k, np.where((idx.ravel() >= 0) & (idx.ravel() < E), idx.ravel(), E)
+    order = np.argsort(key, kind="stable")
+    live = int((key < E).sum())
+    row = np.full(n, -1, np.int32)
+    row[order[:live]] = np.arange(live)
+    x = torch.randn(T, d, device="cuda")
+    out = (torch.full((n, d), float("nan"), device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+           torch.full((n,), -9, dtype=torch.int32, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda"))
+    X, off, pairs, row_of = moe.moe_sort_tokens(x, torch.from_numpy(idx).cuda(), E, out=out)
+    assert np.array_equal(_np(off), np.searchsorted(key[order], np.arange(E + 1)))
+    assert np.array_equal(_np(pairs)[:live], order[:live]) and (pairs[live:] == -9).all()
+    assert np.array_equal(_np(row_of).ravel(), row)
+    assert torch.equal(X[:live], x[torch.from_numpy(order[:live] // k).cuda()]) and torch.isnan(X[live:]).all()
+
+
 def _leave_behind(*shape, dtype=torch.float32):
     """A freed block of that size full of values nobody should see."""
     del_me = torch.full(shape, float("nan") if dtype.is_floating_point else 1 << 30, dtype=dtype, device="cuda")
