@@ -14,9 +14,12 @@
 //
 // One row is bound by HBM where the matrix is large (2048 x 100003: 24.7 us,
 // 4.7 TB/s) and by the launch and two dependent loads where it is small (2048 x
-// 2048: 4.3 us); tens of rows by x, which every block reads again from L2 (48
-// rows of 4096 x 4096: 10.2 us); thousands by the vector work of the codes and
-// folds (4096 rows of 2048 x 8192: 330 us, 415 TFLOP/s).
+// 2048: 4.1 us); tens of rows by latency, too few waves for it (48 rows of 4096
+// x 4096: 10.2 us; 1.5 waves a SIMD, 44 % of their cycles waiting, and W read
+// and decoded for every 16 rows; L2 gives 5 TB/s there, 20 elsewhere);
+// thousands by one wave a SIMD with each step's loads directly before its sums,
+// and the codes decoded by every wave (4096 rows of 2048 x 8192: 299 us, 460
+// TFLOP/s).
 #include "internal.h"
 #include "device.h"
 
@@ -358,8 +361,8 @@ int launch(LinArgs a, int wk, long likely, hipStream_t s) {
 
 // Tile shapes by the number of 16 x 16 output tiles, about a block for each of
 // the 256 CUs first.  A block reads its rows of x and of W once, so beyond that
-// wider tiles save reads: x is re-read for every row tile (from L2, which is
-// what bounds more than a few rows of x), W for every 16 rows.  Measured, us:
+// wider tiles save reads: x is re-read for every row tile (from L2), W for
+// every 16 rows.  Measured, us:
 //   4096 x 4096   T = 1: RT 1 5.6, RT 2 6.8    T = 32: RT 1 13, RT 2 8.6, RT 4 11.2
 //                 T = 64: RT 2 13.2, RT 4 11.5   T = 1024: RT 4 94, NT 4 RT 4 76
 //   2048 x 8192   T = 1: RT 2 5.1, RT 1 5.3      T = 64: RT 4 11.5
