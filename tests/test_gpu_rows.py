@@ -265,6 +265,35 @@ def test_rows_behind_the_last_bucket_of_allocated_outputs():
     assert (y == 0).all()
 
 
+def test_two_graphs_that_share_a_workspace():
+    """The four launches of many pairs of few experts, captured twice with one
+    workspace and replayed in turn on new inputs."""
+    T, k, E, d = 35000, 2, 3, 5
+    g = torch.Generator(device="cuda").manual_seed(9)
+    ws = torch.empty(moe.moe_sort_workspace_bytes(T, k, E), dtype=torch.uint8, device="cuda").random_(0, 256, generator=g)
+    sets = []
+    for _ in range(2):
+        x, idx = torch.randn(T, d, generator=g, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda")
+        bufs = (torch.zeros(T * k, d, device="cuda"), torch.zeros(E + 1, dtype=torch.int32, device="cuda"),
+                torch.full((T * k,), -1, dtype=torch.int32, device="cuda"), torch.zeros(T, k, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_sort_tokens(x, idx, E, workspace=ws, out=bufs)
+        sets.append((x, idx, bufs, graph))
+    for rep in range(3):
+        for x, idx, bufs, graph in sets:
+            x.normal_(generator=g)
+            idx.random_(0, E, generator=g)
+        for x, idx, bufs, graph in sets:
+            graph.replay()
+        for x, idx, bufs, graph in sets:
+            want = moe.moe_sort_tokens(x, idx, E)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(bufs, want)), rep
+            assert torch.equal(bufs[0], x[bufs[2].long() // k])
+
+
 def test_more_than_2_31_elements():
     """Rows past 4 GiB and 2^31 elements.  Sixteen equal bf16 rows sum to an
     exact sixteenfold, and with weights of 1/16 to the row itself."""
