@@ -604,6 +604,93 @@ int moe_router_topk_backward(const uint16_t* x_dev, int32_t T, int32_t d,
                              void* workspace_dev, size_t workspace_bytes,
                              hipStream_t stream);
 
+/* ------------------------------------------- products of 16-bit matrices
+ * The experts' products in the types that they are trained in, with their
+ * gradients: rows and matrices in bf16 or fp16 (`type`), row-major and
+ * contiguous, matrices [n_out][n_in].  offsets_dev NULL (E 1): one matrix for
+ * all N rows.  Otherwise rows in expert order (moe_sort_tokens): expert e's
+ * matrix, at w_dev + e * w_stride_bytes, for rows offsets[e] .. offsets[e+1]-1;
+ * rows outside the buckets keep what the output held, and what the inputs hold
+ * there is not used.  E <= 1024.  Sizes from 1 to 2^20, N up to 2^30
+ * (MOE_ERR_UNSUPPORTED beyond), any alignment of the element; rows of whole 16-byte pieces at 16-byte addresses (sizes that are
+ * multiples of 8) are faster.  Products exact, sums in fp32 in an order that
+ * depends on the sizes alone, each output rounded once: y and dx to `type` or
+ * (y) to fp32, gradients of matrices to dw_type, `type` or MOE_TYPE_F32.  A row
+ * that is not finite touches no row of another, and only its own expert's
+ * gradient.  Outputs must not overlap inputs. */
+int moe_linear(const void* w_dev, size_t w_stride_bytes, int32_t E,
+               const void* x_dev, int32_t type, int32_t N, int32_t n_in,
+               int32_t n_out, const int32_t* offsets_dev, void* y_dev,
+               int32_t y_type, hipStream_t stream);
+/* dx = dy W [N][n_in]; dW = sum over the expert's rows of dy^T x, written whole
+ * (zeros for an expert without rows).  Either may be NULL, not both; dx NULL:
+ * w_dev is not used, dw NULL: x_dev is not. */
+int moe_linear_backward(const void* dy_dev, const void* w_dev,
+                        size_t w_stride_bytes, int32_t E, const void* x_dev,
+                        int32_t type, int32_t N, int32_t n_in, int32_t n_out,
+                        const int32_t* offsets_dev, void* dx_dev, void* dw_dev,
+                        size_t dw_stride_bytes, int32_t dw_type,
+                        hipStream_t stream);
+
+/* The gated block: with g = x Wg^T and u = x Wu^T (Wg, Wu [I][d] an expert),
+ *   h = act(g) u   [N][I],
+ * g and u in fp32 until h is rounded.  act: MOE_ACT_SILU g / (1 + e^-g),
+ * MOE_ACT_GELU g (1 + erf(g / sqrt 2)) / 2, MOE_ACT_GELU_TANH
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.  pre_dev (or NULL): g | u
+ * [N][2 I] in `type`, what the gradients need. */
+enum {
+  MOE_ACT_SILU = 0,
+  MOE_ACT_GELU = 1,
+  MOE_ACT_GELU_TANH = 2
+};
+int moe_gated(const void* w_gate_dev, size_t gate_stride_bytes,
+              const void* w_up_dev, size_t up_stride_bytes, int32_t E,
+              const void* x_dev, int32_t type, int32_t N, int32_t d, int32_t I,
+              const int32_t* offsets_dev, int32_t act, void* h_dev,
+              void* pre_dev, hipStream_t stream);
+/* From dh [N][I] and the saved pre: dg = dh u act'(g) and du = dh act(g)
+ * (rounded to `type` in the workspace), dx = dg Wg + du Wu, dWg = dg^T x,
+ * dWu = du^T x; dx, or both gradients of matrices, may be NULL.  The workspace
+ * (16-byte aligned) needs no fill. */
+size_t moe_gated_backward_workspace_bytes(int32_t N, int32_t I);
+int moe_gated_backward(const void* dh_dev, const void* pre_dev,
+                       const void* w_gate_dev, size_t gate_stride_bytes,
+                       const void* w_up_dev, size_t up_stride_bytes, int32_t E,
+                       const void* x_dev, int32_t type, int32_t N, int32_t d,
+                       int32_t I, const int32_t* offsets_dev, int32_t act,
+                       void* dx_dev, void* dw_gate_dev,
+                       size_t dw_gate_stride_bytes, void* dw_up_dev,
+                       size_t dw_up_stride_bytes, int32_t dw_type,
+                       void* workspace_dev, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/* ------------------------------- products in 8-bit floating point
+ * Numbers in e4m3 (OCP: 3 bits of mantissa, largest 448, no infinity) with one
+ * fp32 scale for a block of them: 128 inputs of a row of x, 128 x 128 of W.
+ * Quantisation: with a the largest |v| of the block (2^-96 where it is smaller),
+ *   scale = a / 448,   code = e4m3(448 v / a)   (nearest, ties to even).
+ * x [count][rows][n] of `type` (fp32, bf16, fp16), codes the same shape,
+ * scales [count][ceil(rows / block_rows)][ceil(n / 128)]; block_rows 1 or 128.
+ * fp32 values up to 2^100.  A block with a value that is not finite gets codes
+ * or a scale that are not, so that its products are not. */
+int moe_quantize_fp8(const void* x_dev, int32_t type, int32_t count,
+                     int32_t rows, int32_t n, int32_t block_rows,
+                     void* codes_dev, float* scales_dev, hipStream_t stream);
+/* y[p][o] = sum over blocks b of 128 inputs of
+ *   x_scales[p][b] w_scales[o / 128][b] sum_{j in b} x[p][j] w[o][j],
+ * rows, experts and E as moe_linear; n_in a multiple of 16, codes 16-byte
+ * aligned (w_stride a multiple of 16), w_scales of an expert
+ * ceil(n_out / 128) * ceil(n_in / 128) apart or w_scales_stride (in floats).
+ * A block's products are summed before they are scaled: 8 consecutive ones at
+ * once by the matrix core, which drops of each what is below 2^-13 of the
+ * largest's power of two, then in fp32.  y_type any. */
+int moe_linear_fp8(const void* w_dev, size_t w_stride_bytes,
+                   const float* w_scales_dev, size_t w_scales_stride,
+                   int32_t E, const void* x_dev, const float* x_scales_dev,
+                   int32_t N, int32_t n_in, int32_t n_out,
+                   const int32_t* offsets_dev, void* y_dev, int32_t y_type,
+                   hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,8 +26,9 @@ Modules:
   bucket  — token -> expert bucketing (counting sort)
   lfu     — LFU + recency slot-pool simulation
   rows    — rows in expert order and back, router gradient, single 4-bit matrices
+  products — the experts' products in 16-bit types with gradients, and in e4m3
 
 Parity status of every function is pinned by ``tests/test_oracle_pins.py``;
 none is "parity unpinned".
 """
-from . import quant, layer, bucket, lfu, rows  # noqa: F401
+from . import quant, layer, bucket, lfu, products, rows  # noqa: F401

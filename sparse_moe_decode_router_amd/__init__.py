@@ -147,6 +147,14 @@ _SIGS = {
     "moe_pack_linear_int4": (C.c_int, [_P, _P, _P, _P, _P]),
     "moe_unpack_linear_int4": (C.c_int, [_P, _P, _P, _P, _P]),
     "moe_linear_int4": (C.c_int, [_P, _P, _P, _I, _P, _P]),
+    "moe_linear": (C.c_int, [_P, _S, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "moe_linear_backward": (C.c_int, [_P, _P, _S, _I, _P, _I, _I, _I, _I, _P, _P, _P, _S, _I, _P]),
+    "moe_gated": (C.c_int, [_P, _S, _P, _S, _I, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P]),
+    "moe_gated_backward_workspace_bytes": (_S, [_I, _I]),
+    "moe_gated_backward": (C.c_int, [_P, _P, _P, _S, _P, _S, _I, _P, _I, _I, _I, _I, _P, _I, _P, _P, _S, _P, _S, _I,
+                                     _P, _S, _P]),
+    "moe_quantize_fp8": (C.c_int, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_linear_fp8": (C.c_int, [_P, _S, _P, _S, _I, _P, _P, _I, _I, _I, _P, _P, _I, _P]),
     "moe_expert_linear_int4": (C.c_int, [_P, _P, _S, _I, _P, _I, _P, _I, _P, _P, _P, _P]),
     "moe_pool_linear_int4": (C.c_int, [_P, _I, _P, _I, _P, _P, _P]),
     "moe_router_backward_workspace_bytes": (_S, [_I, _I, _I, _I]),
@@ -686,7 +694,8 @@ def moe_chain_forward(chain: Chain, x, path: int = MOE_PATH_AUTO, trace: bool = 
 _rowops.bind(*(C.cast(getattr(_lib, _n), C.c_void_p).value for _n in (
     "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_combine",
     "moe_unsort_combine_backward", "moe_linear_bytes", "moe_linear_int4", "moe_expert_linear_int4",
-    "moe_pool_linear_int4", "moe_router_topk_backward")))
+    "moe_pool_linear_int4", "moe_router_topk_backward", "moe_linear", "moe_linear_backward", "moe_gated",
+    "moe_gated_backward", "moe_quantize_fp8", "moe_linear_fp8")))
 
 
 def _stream_of(x, stream):
@@ -884,6 +893,157 @@ def moe_pool_linear_int4(pool: Pool, matrix: str, x_sorted, offsets, out=None, s
     st = _rowops.pool_linear(pool.handle.value, _MATS.index(matrix), n_in, n_out, pool.E, x_sorted, offsets, out)
     if st:
         _check(st, "moe_pool_linear_int4")
+    return out
+
+
+# ------------------------------------------------ products of 16-bit matrices
+# Rows bfloat16 or float16, matrices of the same type [n_out, n_in]: one for all
+# rows, or with offsets int32 [E+1] one per expert, [E, n_out, n_in], over rows
+# in expert order (moe_sort_tokens).  Experts' matrices may be apart: views into
+# larger tensors, such as the two halves of a fused [E, 2 I, d].
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
+MOE_ACT_GELU_TANH = 2
+_ACTS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH}
+
+
+def _act(act) -> int:
+    if not isinstance(act, str) or act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}")
+    return _ACTS[act]
+
+
+def _rows_out(x, cols, offsets, dtype=None):
+    """An output [rows of x, cols]: zeros where rows may lie behind the last bucket."""
+    return (torch.empty if offsets is None else torch.zeros)((x.shape[0], cols), dtype=dtype or x.dtype, device=x.device)
+
+
+def _matrices(w, name, offsets):
+    dim = 2 if offsets is None else 3
+    if not isinstance(w, torch.Tensor) or w.dim() != dim:
+        raise ValueError(f"{name}: a {dim}-d device tensor is wanted")
+    return w.shape[-2:]
+
+
+def moe_linear(w, x, offsets=None, out=None, stream=None):
+    """y [N, n_out] = x W^T: x [N, n_in], w [n_out, n_in], or with offsets
+    [E, n_out, n_in].  out: of x's type, or float32.  Rows outside the buckets
+    keep what they held, or are zeros in a y allocated here."""
+    if stream is not None:
+        with _stream_of(x, stream):
+            return moe_linear(w, x, offsets, out)
+    if out is None:
+        _matrix(x, "x")
+        out = _rows_out(x, _matrices(w, "w", offsets)[0], offsets)
+    st = _rowops.product(w, x, offsets, out)
+    if st:
+        _check(st, "moe_linear")
+    return out
+
+
+def moe_linear_backward(dy, w, x, offsets=None, out=None, stream=None):
+    """Gradients of moe_linear from dy [N, n_out]: (dx [N, n_in], dw like w).
+    out: that pair to write into, None for one not wanted; dw of x's type or
+    float32, written whole (zeros for an expert without rows)."""
+    if stream is not None:
+        with _stream_of(dy, stream):
+            return moe_linear_backward(dy, w, x, offsets, out)
+    if out is None:
+        _matrix(dy, "dy")
+        n_out, n_in = _matrices(w, "w", offsets)
+        out = (_rows_out(dy, n_in, offsets), torch.empty(w.shape, dtype=w.dtype, device=w.device))
+    st = _rowops.product_grad(dy, w, x, offsets, *out)
+    if st:
+        _check(st, "moe_linear_backward")
+    return out
+
+
+def moe_gated(w_gate, w_up, x, offsets=None, act: str = "silu", save: bool = False, out=None, stream=None):
+    """h [N, I] = act(x Wg^T) * (x Wu^T): x [N, d], w_gate and w_up [I, d], or
+    with offsets [E, I, d]; act "silu", "gelu" or "gelu_tanh".  With save
+    (h, pre): pre [N, 2 I] holds both products for moe_gated_backward.  out: h,
+    or that pair.  Rows outside the buckets keep what they held, or are zeros in
+    buffers allocated here."""
+    if stream is not None:
+        with _stream_of(x, stream):
+            return moe_gated(w_gate, w_up, x, offsets, act, save, out)
+    if out is None:
+        _matrix(x, "x")
+        I = _matrices(w_gate, "w_gate", offsets)[0]
+        out = _rows_out(x, I, offsets)
+        if save:
+            out = (out, _rows_out(x, 2 * I, offsets))
+    h, pre = out if save else (out, None)
+    if save and pre is None:
+        raise ValueError("pre: a device tensor is wanted")
+    st = _rowops.gated(w_gate, w_up, x, offsets, _act(act), h, pre)
+    if st:
+        _check(st, "moe_gated")
+    return out
+
+
+def moe_gated_backward_workspace_bytes(N: int, I: int) -> int:
+    return int(_lib.moe_gated_backward_workspace_bytes(N, I)) if _fit_i32(N, I) else 0
+
+
+def moe_gated_backward(dh, pre, w_gate, w_up, x, offsets=None, act: str = "silu", workspace=None, out=None, stream=None):
+    """Gradients of moe_gated from dh [N, I] and what it saved: (dx [N, d],
+    dw_gate, dw_up like the matrices).  out: that triple to write into, None for
+    dx, or for both gradients of matrices, where not wanted; those of x's type
+    or float32, written whole."""
+    if stream is not None:
+        with _stream_of(dh, stream):
+            return moe_gated_backward(dh, pre, w_gate, w_up, x, offsets, act, workspace, out)
+    if out is None or workspace is None:
+        N, I = _matrix(dh, "dh")
+        if out is None:
+            d = _matrices(w_gate, "w_gate", offsets)[1]
+            out = (_rows_out(dh, d, offsets), torch.empty(w_gate.shape, dtype=w_gate.dtype, device=dh.device),
+                   torch.empty(w_gate.shape, dtype=w_gate.dtype, device=dh.device))
+        if workspace is None:
+            workspace = torch.empty(moe_gated_backward_workspace_bytes(N, I), dtype=torch.uint8, device=dh.device)
+    st = _rowops.gated_grad(dh, pre, w_gate, w_up, x, offsets, _act(act), *out, workspace)
+    if st:
+        _check(st, "moe_gated_backward")
+    return out
+
+
+# --------------------------------------------- products in 8-bit floating point
+def moe_quantize_fp8(x, block_rows: int = 1, out=None, stream=None):
+    """(codes float8_e4m3fn like x, scales fp32): a scale for every 128 columns
+    of a row (block_rows 1, for activations) or of 128 rows (128, for matrices).
+    x [rows, n] or [count, rows, n], float32, bfloat16 or float16; scales
+    [.., ceil(rows / block_rows), ceil(n / 128)].  out: that pair."""
+    if stream is not None:
+        with _stream_of(x, stream):
+            return moe_quantize_fp8(x, block_rows, out)
+    if out is None:
+        if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3) or block_rows not in (1, 128):
+            raise ValueError("x: a 2-d or 3-d device tensor is wanted, and block_rows 1 or 128")
+        sizes = (*x.shape[:-2], -(-x.shape[-2] // block_rows), -(-x.shape[-1] // 128))
+        out = (torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
+               torch.empty(sizes, dtype=torch.float32, device=x.device))
+    st = _rowops.quantize(x, block_rows, *out)
+    if st:
+        _check(st, "moe_quantize_fp8")
+    return out
+
+
+def moe_linear_fp8(w, w_scales, x, x_scales, offsets=None, out=None, stream=None):
+    """y [N, n_out] = x W^T of e4m3 codes with their scales (moe_quantize_fp8: w
+    with block_rows 128, x with 1); w [n_out, n_in], or with offsets
+    [E, n_out, n_in]; n_in a multiple of 16.  out: float32 (the default),
+    bfloat16 or float16.  Rows outside the buckets keep what they held, or are
+    zeros in a y allocated here."""
+    if stream is not None:
+        with _stream_of(x, stream):
+            return moe_linear_fp8(w, w_scales, x, x_scales, offsets, out)
+    if out is None:
+        _matrix(x, "x")
+        out = _rows_out(x, _matrices(w, "w", offsets)[0], offsets, torch.float32)
+    st = _rowops.product_fp8(w, w_scales, x, x_scales, offsets, out)
+    if st:
+        _check(st, "moe_linear_fp8")
     return out
 
 

@@ -23,7 +23,7 @@ ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["router.hip", "bucket.hip", "ffn_gemv.hip", "ffn_mfma.hip", "combine.hip", "chain.hip", "offload.hip", "noalloc.hip", "ceiling.hip",
-           "sort.hip", "linear.hip", "router_grad.hip", "host.cpp"]
+           "sort.hip", "linear.hip", "router_grad.hip", "product.hip", "gated.hip", "grads.hip", "fp8.hip", "host.cpp"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -1,4 +1,4 @@
-// Tensor arguments of the row operators, 4-bit products and the router's
+// Tensor arguments of the row operators, products and the router's
 // gradient: a CPython module that checks each torch tensor (device, type,
 // shape, contiguity, no gradient to record; ValueError otherwise) and calls the
 // C ABI with its address.  The same checks in Python cost 0.4 us a tensor, more than half of
@@ -31,6 +31,12 @@ struct Entry {
   decltype(&moe_expert_linear_int4) expert_linear;
   decltype(&moe_pool_linear_int4) pool_linear;
   decltype(&moe_router_topk_backward) router_grad;
+  decltype(&moe_linear) product;
+  decltype(&moe_linear_backward) product_grad;
+  decltype(&moe_gated) gated;
+  decltype(&moe_gated_backward) gated_grad;
+  decltype(&moe_quantize_fp8) quantize;
+  decltype(&moe_linear_fp8) product_fp8;
 } g;
 
 using Shape = std::initializer_list<int64_t>;
@@ -321,14 +327,184 @@ PyObject* py_router_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// Matrices [n_out][n_in] of one type: 2-d, or (with offsets) 3-d [E][n_out][n_in],
+// each contiguous, the experts' at any distance.
+struct Matrices {
+  void* p;
+  int E;
+  int64_t n_out, n_in;
+  size_t stride;                // bytes
+};
+Matrices matrices(PyObject* o, const char* name, at::ScalarType type, bool experts, int dev) {
+  const at::Tensor& v = tensor(o, name);
+  const int dim = experts ? 3 : 2;
+  if (!v.is_cuda() || v.get_device() != dev || v.scalar_type() != type || v.dim() != dim ||
+      (v.size(dim - 1) > 1 && v.stride(dim - 1) != 1) || (v.size(dim - 2) > 1 && v.stride(dim - 2) != v.size(dim - 1)) ||
+      (experts && v.size(0) > 1 && v.stride(0) < v.size(1) * v.size(2))) {
+    PyErr_Format(PyExc_ValueError, "%s: a %s tensor %s of contiguous matrices on cuda:%d wanted, got %s %s on %s, strides %s",
+                 name, c10::toString(type), experts ? "[E, n_out, n_in]" : "[n_out, n_in]", dev,
+                 c10::toString(v.scalar_type()), text(v.sizes()).c_str(), v.device().str().c_str(),
+                 text(v.strides()).c_str());
+    throw PyError{};
+  }
+  no_gradient(v, name);
+  Matrices m{v.data_ptr(), 1, v.size(dim - 2), v.size(dim - 1), 0};
+  m.stride = (size_t)(m.n_out * m.n_in) * v.element_size();
+  if (experts) {
+    m.E = size32(v.size(0), "E");
+    if (m.E > 1) m.stride = (size_t)v.stride(0) * v.element_size();
+  }
+  return m;
+}
+// The same for an output or a second input of w's sizes; None passes as null.
+Matrices like(PyObject* o, const char* name, at::ScalarType type, bool experts, int dev, int E, int64_t n_out, int64_t n_in) {
+  if (o == Py_None) return Matrices{nullptr, E, n_out, n_in, 0};
+  const Matrices m = matrices(o, name, type, experts, dev);
+  if (m.E != E || m.n_out != n_out || m.n_in != n_in) {
+    PyErr_Format(PyExc_ValueError, "%s: %d matrices of %lld x %lld wanted, got %d of %lld x %lld", name, E, (long long)n_out,
+                 (long long)n_in, m.E, (long long)m.n_out, (long long)m.n_in);
+    throw PyError{};
+  }
+  return m;
+}
+at::ScalarType type_of(PyObject* o, const char* name) { return tensor(o, name).scalar_type(); }
+int32_t* borders(PyObject* o, int E, int dev) { return may<int32_t>(o, "offsets", kI32, {E + 1}, dev); }
+
+// w, x, offsets, y
+PyObject* py_product(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<4>(args, n, [](PyObject* const* a) {
+    int dev;
+    const at::Tensor& x = matrix(a[1], "x", &dev, true);
+    const at::ScalarType t = x.scalar_type(), ty = type_of(a[3], "out");
+    const bool experts = a[2] != Py_None;
+    const Matrices w = matrices(a[0], "w", t, experts, dev);
+    const int64_t N = x.size(0);
+    const On on(dev);
+    return g.product(w.p, w.stride, w.E, need(x, "x", t, {N, w.n_in}, dev), type_code(t), size32(N, "N"),
+                     size32(w.n_in, "n_in"), size32(w.n_out, "n_out"), borders(a[2], w.E, dev),
+                     need<void>(a[3], "out", ty == kF32 ? kF32 : t, {N, w.n_out}, dev), type_code(ty == kF32 ? kF32 : t), on.stream);
+  });
+}
+
+// dy, w, x, offsets, dx, dw
+PyObject* py_product_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<6>(args, n, [](PyObject* const* a) {
+    int dev;
+    const at::Tensor& dy = matrix(a[0], "dy", &dev, true);
+    const at::ScalarType t = dy.scalar_type(), td = a[5] != Py_None && type_of(a[5], "dw") == kF32 ? kF32 : t;
+    const bool experts = a[3] != Py_None;
+    const Matrices w = matrices(a[1], "w", t, experts, dev);
+    const int64_t N = dy.size(0);
+    const Matrices dw = like(a[5], "dw", td, experts, dev, w.E, w.n_out, w.n_in);
+    const On on(dev);
+    return g.product_grad(need(dy, "dy", t, {N, w.n_out}, dev), w.p, w.stride, w.E, need<void>(a[2], "x", t, {N, w.n_in}, dev),
+                          type_code(t), size32(N, "N"), size32(w.n_in, "n_in"), size32(w.n_out, "n_out"),
+                          borders(a[3], w.E, dev), may<void>(a[4], "dx", t, {N, w.n_in}, dev), dw.p, dw.stride,
+                          type_code(td), on.stream);
+  });
+}
+
+// w_gate, w_up, x, offsets, act, h, pre
+PyObject* py_gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<7>(args, n, [](PyObject* const* a) {
+    int dev;
+    const at::Tensor& x = matrix(a[2], "x", &dev, true);
+    const at::ScalarType t = x.scalar_type();
+    const bool experts = a[3] != Py_None;
+    const Matrices wg = matrices(a[0], "w_gate", t, experts, dev);
+    const Matrices wu = like(a[1], "w_up", t, experts, dev, wg.E, wg.n_out, wg.n_in);
+    const int64_t N = x.size(0), I = wg.n_out;
+    const On on(dev);
+    return g.gated(wg.p, wg.stride, wu.p, wu.stride, wg.E, need(x, "x", t, {N, wg.n_in}, dev), type_code(t), size32(N, "N"),
+                   size32(wg.n_in, "d"), size32(I, "I"), borders(a[3], wg.E, dev), number32(a[4], "act"),
+                   need<void>(a[5], "h", t, {N, I}, dev), may<void>(a[6], "pre", t, {N, 2 * I}, dev), on.stream);
+  });
+}
+
+// dh, pre, w_gate, w_up, x, offsets, act, dx, dw_gate, dw_up, workspace
+PyObject* py_gated_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<11>(args, n, [](PyObject* const* a) {
+    int dev;
+    const at::Tensor& dh = matrix(a[0], "dh", &dev, true);
+    const at::ScalarType t = dh.scalar_type(), td = a[8] != Py_None && type_of(a[8], "dw_gate") == kF32 ? kF32 : t;
+    const bool experts = a[5] != Py_None;
+    const Matrices wg = matrices(a[2], "w_gate", t, experts, dev);
+    const Matrices wu = like(a[3], "w_up", t, experts, dev, wg.E, wg.n_out, wg.n_in);
+    const int64_t N = dh.size(0), I = wg.n_out, d = wg.n_in;
+    const Matrices dg = like(a[8], "dw_gate", td, experts, dev, wg.E, I, d), du = like(a[9], "dw_up", td, experts, dev, wg.E, I, d);
+    size_t nws;
+    uint8_t* ws = workspace(a[10], dev, &nws);
+    const On on(dev);
+    return g.gated_grad(need(dh, "dh", t, {N, I}, dev), need<void>(a[1], "pre", t, {N, 2 * I}, dev), wg.p, wg.stride, wu.p,
+                        wu.stride, wg.E, need<void>(a[4], "x", t, {N, d}, dev), type_code(t), size32(N, "N"), size32(d, "d"),
+                        size32(I, "I"), borders(a[5], wg.E, dev), number32(a[6], "act"),
+                        may<void>(a[7], "dx", t, {N, d}, dev), dg.p, dg.stride, du.p, du.stride, type_code(td), ws, nws,
+                        on.stream);
+  });
+}
+
+// x [rows][n] or [count][rows][n], block_rows, codes, scales
+PyObject* py_quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<4>(args, n, [](PyObject* const* a) {
+    const at::Tensor& x = tensor(a[0], "x");
+    const at::ScalarType t = x.scalar_type();
+    if (!x.is_cuda() || (x.dim() != 2 && x.dim() != 3) || (t != kF32 && t != kBf16 && t != at::kHalf)) {
+      PyErr_Format(PyExc_ValueError, "x: a 2-d or 3-d device tensor of float32, bfloat16 or float16 wanted, got %s %s on %s",
+                   c10::toString(t), text(x.sizes()).c_str(), x.device().str().c_str());
+      throw PyError{};
+    }
+    const int dev = x.get_device();
+    const bool batch = x.dim() == 3;
+    const int64_t count = batch ? x.size(0) : 1, rows = x.size(-2), cols = x.size(-1);
+    const int br = number32(a[1], "block_rows");
+    const int64_t rb = br == 128 ? (rows + 127) / 128 : rows, cb = (cols + 127) / 128;
+    const On on(dev);
+    void *px, *pc, *ps;
+    if (batch) {
+      px = need(x, "x", t, {count, rows, cols}, dev);
+      pc = need<void>(a[2], "codes", at::kFloat8_e4m3fn, {count, rows, cols}, dev);
+      ps = need<void>(a[3], "scales", kF32, {count, rb, cb}, dev);
+    } else {
+      px = need(x, "x", t, {rows, cols}, dev);
+      pc = need<void>(a[2], "codes", at::kFloat8_e4m3fn, {rows, cols}, dev);
+      ps = need<void>(a[3], "scales", kF32, {rb, cb}, dev);
+    }
+    return g.quantize(px, type_code(t), size32(count, "count"), size32(rows, "rows"), size32(cols, "n"), br, pc,
+                      static_cast<float*>(ps), on.stream);
+  });
+}
+
+// w, w_scales, x, x_scales, offsets, y
+PyObject* py_product_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<6>(args, n, [](PyObject* const* a) {
+    int dev, dev2;
+    const at::Tensor& x = matrix(a[2], "x", &dev, false);
+    const at::ScalarType ty = matrix(a[5], "out", &dev2, true).scalar_type();
+    const bool experts = a[4] != Py_None;
+    const Matrices w = matrices(a[0], "w", at::kFloat8_e4m3fn, experts, dev);
+    const int64_t N = x.size(0), rb = (w.n_out + 127) / 128, cb = (w.n_in + 127) / 128;
+    const Matrices ws = like(a[1], "w_scales", kF32, experts, dev, w.E, rb, cb);
+    if (!ws.p && N > 0) {
+      PyErr_SetString(PyExc_ValueError, "w_scales: a device tensor is wanted");
+      throw PyError{};
+    }
+    const On on(dev);
+    return g.product_fp8(w.p, w.stride, static_cast<float*>(ws.p), ws.stride / sizeof(float), w.E,
+                         need(x, "x", at::kFloat8_e4m3fn, {N, w.n_in}, dev), need<float>(a[3], "x_scales", kF32, {N, cb}, dev),
+                         size32(N, "N"), size32(w.n_in, "n_in"), size32(w.n_out, "n_out"), borders(a[4], w.E, dev),
+                         need<void>(a[5], "out", ty, {N, w.n_out}, dev), type_code(ty), on.stream);
+  });
+}
+
+constexpr int kEntries = sizeof(Entry) / sizeof(void*);
 PyObject* py_bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return entry<10>(args, n, [](PyObject* const* a) {
+  return entry<kEntries>(args, n, [](PyObject* const* a) {
     void** to = reinterpret_cast<void**>(&g);
-    for (int i = 0; i < 10; ++i) to[i] = address(a[i]);
+    for (int i = 0; i < kEntries; ++i) to[i] = address(a[i]);
     return 0;
   });
 }
-static_assert(sizeof(Entry) == 10 * sizeof(void*), "one address an entry point");
+static_assert(sizeof(Entry) == 16 * sizeof(void*), "one address an entry point");
 
 #define METHOD(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
@@ -336,7 +512,10 @@ PyMethodDef methods[] = {
     METHOD("sort_grad", py_sort_grad), METHOD("unsort", py_unsort),
     METHOD("unsort_grad", py_unsort_grad), METHOD("linear", py_linear),
     METHOD("expert_linear", py_expert_linear), METHOD("pool_linear", py_pool_linear),
-    METHOD("router_grad", py_router_grad), {nullptr, nullptr, 0, nullptr}};
+    METHOD("router_grad", py_router_grad), METHOD("product", py_product),
+    METHOD("product_grad", py_product_grad), METHOD("gated", py_gated),
+    METHOD("gated_grad", py_gated_grad), METHOD("quantize", py_quantize),
+    METHOD("product_fp8", py_product_fp8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rowops", "Tensor arguments of the row operators.", -1, methods};
 
 }  // namespace

@@ -1,0 +1,357 @@
+// Products in 8-bit floating point (e4m3) with a scale for every 128 inputs of
+// a row of x and every 128 x 128 block of W, and the quantisation of both.
+//
+//     code = e4m3(448 v / a), scale = a / 448, a the block's largest |v|
+//     y[p][o] = sum_b sx[p][b] sw[o / 128][b] sum_{j in b} x[p][j] w[o][j]
+//
+// 448 v is exact for 16-bit v and the quotient is rounded once before it is
+// rounded to the code, so codes are those of exact arithmetic, ties included.
+// A block's sum of 128 products runs on v_mfma_f32_32x32x64_f8f6f4 (no scales
+// of its own), from zero, and is then added with its scales to the running fp32
+// sum.  The instruction adds the products of 8 consecutive inputs at once and
+// drops of each what is below 2^-13 of the largest's power of two (measured;
+// about 1e-5 of a random product, the codes' own rounding is 2^-4); its sums of
+// these are fp32.  It has twice the rate of the 16-bit products.
+#include "products.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = 128;
+constexpr float kMax = 448.f, kSmallest = 0x1p-96f, kLarge = 0x1p64f;
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// ------------------------------------------------------------ quantisation
+// What values of a block with the largest magnitude `top` are divided by: codes
+// are e4m3(448 (v m) / a).  m (a power of two) keeps 448 v below infinity.
+struct Block {
+  float a, m, scale;
+};
+__device__ __forceinline__ Block block_of(float top) {
+  Block b;
+  top = top < kSmallest ? kSmallest : top;
+  b.scale = top / kMax;
+  b.m = top > kLarge ? 0x1p-32f : 1.f;
+  b.a = top * b.m;
+  return b;
+}
+__device__ __forceinline__ float quotient(const Block& b, float v) { return kMax * (v * b.m) / b.a; }
+
+// A thread's 8 elements of a row: consecutive ones (VN 8), or every `step`th;
+// zeros past `have`.
+template <int TYPE, int VN>
+__device__ __forceinline__ void load8(const typename El<TYPE>::raw* p, int step, int have, float (&v)[8]) {
+  if constexpr (VN == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    if (have >= 8) {
+      constexpr int kN = El<TYPE>::kN;
+#pragma unroll
+      for (int h = 0; h < 8 / kN; ++h) {
+        const Vec<TYPE, kN> e = vec_load<TYPE, kN>(p + h * kN);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[h * kN + i] = El<TYPE>::up(e.e[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i * step < have ? El<TYPE>::up(p[i * step]) : 0.f;
+  }
+}
+template <int VN> __device__ __forceinline__ void store8(uint8_t* p, int step, int have, const Block& b, const float (&v)[8]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(b, v[4 * h]), quotient(b, v[4 * h + 1]), 0, false);
+    w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(b, v[4 * h + 2]), quotient(b, v[4 * h + 3]), c, true);
+  }
+  if constexpr (VN == 8) {
+    if (have >= 8) *reinterpret_cast<uint64_t*>(p) = w[0] | (uint64_t)w[1] << 32;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * step < have) p[i * step] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+  }
+}
+__device__ __forceinline__ float max16(float v) {               // over each 16 lanes
+#pragma unroll
+  for (int s = 1; s < 16; s *= 2) v = fmaxf(v, __shfl_xor(v, s, 64));
+  return v;
+}
+
+// Rows: 16 lanes a block of 128 inputs.
+template <int TYPE, int VN>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const typename El<TYPE>::raw* x, int n, int blocks,
+                                                            long total, uint8_t* codes, float* scales) {
+  const long first = (long)blockIdx.x * 16;
+  const long row0 = first / blocks;
+  const unsigned in = (unsigned)(first - row0 * blocks) + threadIdx.x / 16;
+  if (first + threadIdx.x / 16 >= total) return;
+  const long row = row0 + in / (unsigned)blocks;
+  const int b = (int)(in % (unsigned)blocks), j = threadIdx.x & 15;
+  const int c = b * kBlock + (VN == 8 ? 8 * j : j);
+  const int end = n < (b + 1) * kBlock ? n : (b + 1) * kBlock;
+  float v[8];
+  load8<TYPE, VN>(x + row * n + c, 16, end - c, v);
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+  const Block q = block_of(max16(top));
+  store8<VN>(codes + row * n + c, 16, end - c, q, v);
+  if (j == 0) scales[row * blocks + b] = q.scale;
+}
+
+// 128 x 128: a block of threads each, 16 lanes a row, 8 turns of 16 rows.
+template <int TYPE, int VN>
+__global__ __launch_bounds__(256) void quantize_blocks_kernel(const typename El<TYPE>::raw* x, int rows, int n,
+                                                              int row_blocks, int blocks, long block0, uint8_t* codes,
+                                                              float* scales) {
+  __shared__ float tops[4];
+  const long id = block0 + blockIdx.x;
+  const long m = id / ((long)row_blocks * blocks);
+  const int in = (int)(id - m * ((long)row_blocks * blocks));
+  const int rb = in / blocks, b = in - rb * blocks, j = threadIdx.x & 15;
+  const int c = b * kBlock + (VN == 8 ? 8 * j : j);
+  const int end = n < (b + 1) * kBlock ? n : (b + 1) * kBlock;
+  float v[8][8];
+  float top = 0.f;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const int row = rb * kBlock + 16 * t + threadIdx.x / 16;
+    load8<TYPE, VN>(x + (m * rows + row) * n + c, 16, row < rows ? end - c : 0, v[t]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[t][i]));
+  }
+  top = max16(top);
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  const Block q = block_of(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    const int row = rb * kBlock + 16 * t + threadIdx.x / 16;
+    store8<VN>(codes + (m * rows + row) * n + c, 16, row < rows ? end - c : 0, q, v[t]);
+  }
+  if (threadIdx.x == 0) scales[id] = q.scale;
+}
+
+template <int TYPE, int VN>
+int quantize(const void* xv, long count, int rows, int n, int block_rows, uint8_t* codes, float* scales, hipStream_t s) {
+  typedef typename El<TYPE>::raw raw;
+  const raw* x = static_cast<const raw*>(xv);
+  const int blocks = (n + kBlock - 1) / kBlock;
+  if (block_rows == 1) {
+    const long all = count * rows, per = (1l << 26) / blocks;   // rows a launch
+    for (long r = 0; r < all; r += per) {
+      const long total = (all - r < per ? all - r : per) * blocks;
+      quantize_rows_kernel<TYPE, VN><<<(unsigned)((total + 15) / 16), 256, 0, s>>>(x + r * n, n, blocks, total,
+                                                                                 codes + r * n, scales + r * blocks);
+      MOE_HIP(hipGetLastError());
+    }
+    return MOE_OK;
+  }
+  const int row_blocks = (rows + kBlock - 1) / kBlock;
+  const long total = count * row_blocks * blocks;
+  for (long b = 0; b < total; b += kMaxBlocks) {
+    const long c = total - b < kMaxBlocks ? total - b : kMaxBlocks;
+    quantize_blocks_kernel<TYPE, VN><<<(unsigned)c, 256, 0, s>>>(x, rows, n, row_blocks, blocks, b, codes, scales);
+    MOE_HIP(hipGetLastError());
+  }
+  return MOE_OK;
+}
+template <int TYPE>
+int quantize_typed(const void* x, long count, int rows, int n, int block_rows, uint8_t* codes, float* scales,
+                   hipStream_t s) {
+  return n % 8 == 0 && aligned(x, 16) && aligned(codes, 8)
+             ? quantize<TYPE, 8>(x, count, rows, n, block_rows, codes, scales, s)
+             : quantize<TYPE, 1>(x, count, rows, n, block_rows, codes, scales, s);
+}
+
+// ---------------------------------------------------------------- products
+struct Fp8Args {
+  const uint8_t* w;
+  uint64_t w_stride;            // bytes from expert to expert
+  const float* w_scales;
+  uint64_t w_scales_stride;     // floats
+  const uint8_t* x;
+  const float* x_scales;
+  int n_in, n_out, blocks;      // blocks of 128 inputs
+  const int32_t* offsets;
+  int E;
+  long N;
+  void* y;
+  Grid grid;
+};
+
+// WQ x WP waves of TQ x TP tiles of 32 x 32, 128 inputs a step: a row's 128
+// bytes lie in LDS as 64 elements of 16 bits do in tiles.h.
+template <int WQ_, int WP_, int TQ_, int TP_, int NS_> struct Fp8Shape {
+  static constexpr int WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, NS = NS_;
+  static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
+  typedef Tile<true, BQ, 64, NT, false> QT;
+  typedef Tile<true, BP, 64, NT, false> PT;
+  static constexpr int kStage = QT::kBytes + PT::kBytes, kLds = NS * kStage;
+};
+
+template <class T> __device__ __forceinline__ i32x8_t fp8_frag(const uint8_t* t, int r0, int half, int lane) {
+  const int row = r0 + (lane & 31), piece = 4 * half + 2 * (lane >> 5);
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(t + T::pos(row, piece));
+  const u32x4_t b = *reinterpret_cast<const u32x4_t*>(t + T::pos(row, piece + 1));
+  return (i32x8_t){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+}
+
+template <class S, int OUT>
+__global__ __launch_bounds__(S::NT) void linear_fp8_kernel(Fp8Args a) {
+  extern __shared__ uint8_t tile_lds[];
+  constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
+  int unit, tile;
+  if (!grid_place(a.grid, &unit, &tile)) return;
+  long start;
+  int n, e = 0;
+  if (a.offsets) {
+    const RowChunk c = find_chunk(a.offsets, nullptr, a.E, a.N, unit, S::BQ);
+    if (!c.any || c.n == 0) return;
+    start = c.start;
+    n = c.n;
+    e = c.slot;
+  } else {
+    start = (long)unit * S::BQ;
+    n = a.N - start < S::BQ ? (int)(a.N - start) : S::BQ;
+  }
+  const int p0 = tile * S::BP, cols = a.n_out - p0 < S::BP ? a.n_out - p0 : S::BP;
+  Operand q{}, p{};
+  q.base = a.x + start * a.n_in;
+  p.base = a.w + (uint64_t)e * a.w_stride + (uint64_t)p0 * a.n_in;
+  q.ld = p.ld = q.K = p.K = a.n_in / 2;
+  q.n = n;
+  p.n = cols;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wq = wave / S::WP, wp = wave % S::WP;
+  const int left = n - 32 * wq * S::TQ;
+  const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
+  const float* sx[S::TQ];
+  const float* sw[S::TP];
+#pragma unroll
+  for (int t = 0; t < S::TQ; ++t) {
+    const int r = 32 * (wq * S::TQ + t) + (lane & 31);
+    sx[t] = a.x_scales + (start + (r < n ? r : n - 1)) * a.blocks;
+  }
+#pragma unroll
+  for (int t = 0; t < S::TP; ++t) {
+    const int o = p0 + 32 * (wp * S::TP + t);
+    sw[t] = a.w_scales + (uint64_t)e * a.w_scales_stride + (uint64_t)((o < a.n_out ? o : a.n_out - 1) / kBlock) * a.blocks;
+  }
+  typename S::QT qt;
+  typename S::PT pt;
+  qt.plan(q);
+  pt.plan(p);
+  constexpr int kDma = S::QT::kPer + S::PT::kPer;
+  const auto issue = [&](int s) {
+    uint8_t* st = tile_lds + (s % S::NS) * S::kStage;
+    const int k0 = s < a.blocks ? s * 64 : q.K;
+    qt.dma(q, st, k0);
+    pt.dma(p, st + S::QT::kBytes, k0);
+  };
+  f32x16_t acc[S::TQ][S::TP] = {};
+#pragma unroll
+  for (int s = 0; s < S::NS - 1; ++s) issue(s);
+  for (int s = 0; s < a.blocks; ++s) {
+    float fx[S::TQ], fw[S::TP];
+#pragma unroll
+    for (int t = 0; t < S::TQ; ++t) fx[t] = sx[t][s];
+#pragma unroll
+    for (int t = 0; t < S::TP; ++t) fw[t] = sw[t][s];
+    stage_wait<(S::NS - 2) * kDma>();
+    issue(s + S::NS - 1);
+    const uint8_t* st = tile_lds + (s % S::NS) * S::kStage;
+    i32x8_t pf[S::TP][2];
+#pragma unroll
+    for (int t = 0; t < S::TP; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pf[t][h] = fp8_frag<typename S::PT>(st + S::QT::kBytes, 32 * (wp * S::TP + t), h, lane);
+#pragma unroll
+    for (int u = 0; u < S::TQ; ++u) {
+      if (u < live) {
+        const i32x8_t f0 = fp8_frag<typename S::QT>(st, 32 * (wq * S::TQ + u), 0, lane);
+        const i32x8_t f1 = fp8_frag<typename S::QT>(st, 32 * (wq * S::TQ + u), 1, lane);
+#pragma unroll
+        for (int t = 0; t < S::TP; ++t) {
+          f32x16_t part{};
+          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][0], f0, part, 0, 0, 0, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][1], f1, part, 0, 0, 0, 0, 0, 0);
+          const float f = fx[u] * fw[t];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[u][t][i] = fmaf(f, part[i], acc[u][t][i]);
+        }
+      }
+    }
+  }
+  stage_wait<0>();
+  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+#pragma unroll
+  for (int t = 0; t < S::TQ; ++t) {
+    if (t >= live) continue;
+    const long r0 = start + 32 * (wq * S::TQ + t);
+    const int c0 = 32 * S::TP * wp;
+    store_rows<OUT, S::TP, false>(mine, acc[t], static_cast<uint8_t*>(a.y) + kSize * (r0 * a.n_out + p0 + c0), a.n_out,
+                                  left - 32 * t < 32 ? left - 32 * t : 32, cols - c0);
+  }
+}
+
+template <int OUT> int product(Fp8Args& a, hipStream_t s) {
+  typedef Fp8Shape<2, 2, 2, 2, 2> S;
+  const long units = a.offsets ? max_chunks(a.N, a.E, S::BQ) : (a.N + S::BQ - 1) / S::BQ;
+  return grid_launch(units, (a.n_out + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
+    a.grid = g;
+    linear_fp8_kernel<S, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
+    MOE_HIP(hipGetLastError());
+    return (int)MOE_OK;
+  });
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_quantize_fp8(const void* x, int32_t type, int32_t count, int32_t rows, int32_t n,
+                                int32_t block_rows, void* codes, float* scales, hipStream_t s) {
+  MOE_CHECK(type_size(type) != 0 && count >= 0 && rows >= 0 && n >= 1 && (block_rows == 1 || block_rows == kBlock));
+  if (n > kMostSize || (long)count * rows > (1l << 30)) return MOE_ERR_UNSUPPORTED;
+  if (count == 0 || rows == 0) return MOE_OK;
+  MOE_CHECK(x && codes && scales && aligned(x, type_size(type)) && aligned(scales, 4));
+  uint8_t* c = static_cast<uint8_t*>(codes);
+  if (type == MOE_TYPE_F32) return quantize_typed<MOE_TYPE_F32>(x, count, rows, n, block_rows, c, scales, s);
+  return type == MOE_TYPE_BF16 ? quantize_typed<MOE_TYPE_BF16>(x, count, rows, n, block_rows, c, scales, s)
+                               : quantize_typed<MOE_TYPE_F16>(x, count, rows, n, block_rows, c, scales, s);
+}
+
+extern "C" int moe_linear_fp8(const void* w, size_t w_stride, const float* w_scales, size_t w_scales_stride, int32_t E,
+                              const void* x, const float* x_scales, int32_t N, int32_t n_in, int32_t n_out,
+                              const int32_t* offsets, void* y, int32_t y_type, hipStream_t s) {
+  MOE_TRY(product_check(E, MOE_TYPE_BF16, N, n_in, n_out, offsets));
+  const long blocks = (n_in + kBlock - 1) / kBlock;
+  MOE_CHECK(type_size(y_type) != 0 && n_in % 16 == 0 && aligned(w, 16) && w_stride % 16 == 0 && aligned(w_scales, 4));
+  MOE_CHECK(E == 1 || (w_stride >= (size_t)n_in * n_out &&
+                       w_scales_stride >= (size_t)blocks * ((n_out + kBlock - 1) / kBlock)));
+  if (N == 0) return MOE_OK;
+  MOE_CHECK(w && w_scales && x && x_scales && y && aligned(x, 16) && aligned(x_scales, 4) &&
+            aligned(y, type_size(y_type)));
+  Fp8Args a{};
+  a.w = static_cast<const uint8_t*>(w);
+  a.w_stride = w_stride;
+  a.w_scales = w_scales;
+  a.w_scales_stride = w_scales_stride;
+  a.x = static_cast<const uint8_t*>(x);
+  a.x_scales = x_scales;
+  a.n_in = n_in;
+  a.n_out = n_out;
+  a.blocks = (int)blocks;
+  a.offsets = offsets;
+  a.E = E;
+  a.N = N;
+  a.y = y;
+  if (y_type == MOE_TYPE_F32) return product<MOE_TYPE_F32>(a, s);
+  return y_type == MOE_TYPE_BF16 ? product<MOE_TYPE_BF16>(a, s) : product<MOE_TYPE_F16>(a, s);
+}

@@ -1,0 +1,30 @@
+// Gradients of the experts' matrices: dW[q][p] = sum over an expert's rows of
+// dy[row][q] x[row][p] (product.hip, gated.hip), an expert without rows zeros.
+// Both operands lie with k (the rows) apart: tiles.h reads them turned.
+#include "products.h"
+
+namespace moe {
+namespace {
+
+template <int TYPE, int OUT, bool AL> int launch(MatsArgs& a, hipStream_t s) {
+  typedef Shape<TYPE, false, false, 2, 2, 2, 2, 64, 2, false, AL> S;
+  a.q_tiles = (a.Q + S::BQ - 1) / S::BQ;
+  return grid_launch((long)a.E * a.mats * a.q_tiles, (a.P + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
+    a.grid = g;
+    mats_kernel<S, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
+    MOE_HIP(hipGetLastError());
+    return (int)MOE_OK;
+  });
+}
+template <int TYPE> int typed(MatsArgs& a, int out_type, bool al, hipStream_t s) {
+  if (out_type == MOE_TYPE_F32) return al ? launch<TYPE, MOE_TYPE_F32, true>(a, s) : launch<TYPE, MOE_TYPE_F32, false>(a, s);
+  return al ? launch<TYPE, TYPE, true>(a, s) : launch<TYPE, TYPE, false>(a, s);
+}
+
+}  // namespace
+
+int mats_launch(MatsArgs& a, int type, int out_type, bool al, hipStream_t s) {
+  return type == MOE_TYPE_BF16 ? typed<MOE_TYPE_BF16>(a, out_type, al, s) : typed<MOE_TYPE_F16>(a, out_type, al, s);
+}
+
+}  // namespace moe

@@ -21,6 +21,7 @@
 // and the codes decoded by every wave (4096 rows of 2048 x 8192: 299 us, 460
 // TFLOP/s).
 #include "internal.h"
+#include "chunks.h"
 #include "device.h"
 
 namespace moe {
@@ -49,67 +50,6 @@ struct LinArgs {
   int32_t wr, wk, turns;
   int32_t size;                 // rows a chunk, at most 16 NT
 };
-
-// Sorted rows are cut into chunks of `size` that do not cross an expert's
-// border, numbered in expert order.
-struct RowChunk {
-  bool any;     // false past the last chunk
-  int slot;     // of its expert
-  int start;    // first row
-  int n;        // rows (0..size)
-};
-
-// Chunk j.  Every wave finds its own: borders and slots of all experts in
-// coalesced loads, all in flight at once (lane l holds experts l, l + 64, ..),
-// chunks counted by wave scans of 64 experts.  Offsets that do not describe N
-// rows give no row outside them.
-__device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offsets,
-                                               const int32_t* __restrict__ slot_table, int E, long N, long j,
-                                               int size) {
-  constexpr int kU = 16;                        // E <= 1024
-  const int lane = threadIdx.x & 63;
-  int off[kU + 1], slots[kU];
-#pragma unroll
-  for (int u = 0; u <= kU; ++u) {
-    off[u] = 0;
-    if (u < kU) slots[u] = 64 * u + lane;
-    if (64 * u <= E) {
-      const int e = 64 * u + lane;
-      off[u] = offsets[e < E ? e : E];
-      if (u < kU && slot_table) slots[u] = slot_table[e < E ? e : E - 1];
-    }
-  }
-  RowChunk r{false, 0, 0, 0};
-  int before = 0;                               // chunks of the experts of earlier u
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    if (64 * u < E && !r.any) {
-      // the next lane's border (lane 63: the first of the next 64)
-      const int next = __builtin_amdgcn_update_dpp(__builtin_amdgcn_readlane(off[u + 1], 0), off[u], 0x130, 0xF, 0xF, false);
-      const int rows = 64 * u + 63 < E || lane < E - 64 * u ? next - off[u] : 0;
-      const int c = rows > 0 ? (int)((unsigned)(rows + size - 1) / (unsigned)size) : 0;
-      const int incl = wave_scan(c) + before;
-      const uint64_t past = __ballot((long)incl > j);
-      if (past != 0) {
-        const int owner = __ffsll((unsigned long long)past) - 1;
-        const int skip = ((int)j - __builtin_amdgcn_readlane(incl - c, owner)) * size;
-        const int left = __builtin_amdgcn_readlane(rows, owner) - skip;
-        r = RowChunk{true, __builtin_amdgcn_readlane(slots[u], owner), __builtin_amdgcn_readlane(off[u], owner) + skip,
-                     left < size ? left : size};
-      }
-      before = __builtin_amdgcn_readlane(incl, 63);
-    }
-  }
-  if (r.start < 0 || (long)r.start >= N || r.n < 0) r.start = r.n = 0;
-  if ((long)r.start + r.n > N) r.n = (int)(N - r.start);
-  return r;
-}
-
-// The most chunks that N rows in E buckets can make.
-inline long max_chunks(long N, int E, int size) {
-  const long ne = N < E ? N : E;                // each bucket with rows makes at most one short chunk
-  return ne + (N - ne) / size;
-}
 
 // Eight codes of a word as bf16 16 + q, pairs (q[u], q[u+4]), u = 0..3.
 __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t mask, uint32_t base) {

@@ -1,0 +1,90 @@
+// Products of 16-bit rows with 16-bit matrices, y = x W^T (one matrix, or one
+// per expert over rows in expert order), and their gradients
+//     dx = dy W,   dW = dy^T x
+// (the experts' second half beside gated.hip; "How it works" on the Swiftlet
+// pages applies k of E experts to each token).  Sums in fp32 on the matrix
+// cores; tiles.h has the tiles.
+#include "products.h"
+
+namespace moe {
+namespace {
+
+// y = x W^T: k and k; dx = dy W: k and p
+template <int TYPE, bool PK, int OUT, bool AL> int rows_launch(RowsArgs& a, hipStream_t s) {
+  typedef Shape<TYPE, true, PK, 2, 2, 2, 2, 64, 2, false, AL> S;
+  return rows_grid<S, 1, false, OUT>(a, s);
+}
+template <int TYPE, int OUT> int forward_typed(RowsArgs& a, bool al, hipStream_t s) {
+  return al ? rows_launch<TYPE, true, OUT, true>(a, s) : rows_launch<TYPE, true, OUT, false>(a, s);
+}
+template <int TYPE> int dx_typed(RowsArgs& a, bool al, hipStream_t s) {
+  return al ? rows_launch<TYPE, false, TYPE, true>(a, s) : rows_launch<TYPE, false, TYPE, false>(a, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_linear(const void* w, size_t w_stride, int32_t E, const void* x, int32_t type, int32_t N,
+                          int32_t n_in, int32_t n_out, const int32_t* offsets, void* y, int32_t y_type,
+                          hipStream_t s) {
+  MOE_TRY(product_check(E, type, N, n_in, n_out, offsets));
+  MOE_CHECK((y_type == type || y_type == MOE_TYPE_F32) && matrices_ok(w, w_stride, E, (long)n_in * n_out));
+  if (N == 0) return MOE_OK;
+  MOE_CHECK(w && x && y && aligned(x, 2) && aligned(y, type_size(y_type)));
+  RowsArgs a{};
+  a.q = static_cast<const uint8_t*>(x);
+  a.q_ld = a.p_ld = a.K = n_in;
+  a.p = static_cast<const uint8_t*>(w);
+  a.p_stride = w_stride;
+  a.P = n_out;
+  a.offsets = offsets;
+  a.E = E;
+  a.N = N;
+  a.out = y;
+  const bool al = whole_pieces({n_in, n_out}, {w, x, y}, {w_stride});
+  if (type == MOE_TYPE_BF16)
+    return y_type == type ? forward_typed<MOE_TYPE_BF16, MOE_TYPE_BF16>(a, al, s)
+                          : forward_typed<MOE_TYPE_BF16, MOE_TYPE_F32>(a, al, s);
+  return y_type == type ? forward_typed<MOE_TYPE_F16, MOE_TYPE_F16>(a, al, s)
+                        : forward_typed<MOE_TYPE_F16, MOE_TYPE_F32>(a, al, s);
+}
+
+extern "C" int moe_linear_backward(const void* dy, const void* w, size_t w_stride, int32_t E, const void* x,
+                                   int32_t type, int32_t N, int32_t n_in, int32_t n_out, const int32_t* offsets,
+                                   void* dx, void* dw, size_t dw_stride, int32_t dw_type, hipStream_t s) {
+  MOE_TRY(product_check(E, type, N, n_in, n_out, offsets));
+  MOE_CHECK(dx || dw);
+  MOE_CHECK(!dx || matrices_ok(w, w_stride, E, (long)n_in * n_out));
+  MOE_CHECK(!dw || ((dw_type == type || dw_type == MOE_TYPE_F32) &&
+                    matrices_ok(dw, dw_stride, E, (long)n_in * n_out, type_size(dw_type))));
+  MOE_CHECK(N == 0 || (dy && aligned(dy, 2) && (!dx || (w && aligned(dx, 2))) && (!dw || (x && aligned(x, 2)))));
+  if (dx && N > 0) {
+    RowsArgs a{};
+    a.q = static_cast<const uint8_t*>(dy);
+    a.q_ld = a.K = n_out;
+    a.p = static_cast<const uint8_t*>(w);
+    a.p_stride = w_stride;
+    a.p_ld = a.P = n_in;
+    a.offsets = offsets;
+    a.E = E;
+    a.N = N;
+    a.out = dx;
+    const bool al = whole_pieces({n_in, n_out}, {w, dy, dx}, {w_stride});
+    MOE_TRY(type == MOE_TYPE_BF16 ? dx_typed<MOE_TYPE_BF16>(a, al, s) : dx_typed<MOE_TYPE_F16>(a, al, s));
+  }
+  if (!dw) return MOE_OK;
+  MatsArgs m{};
+  m.q = static_cast<const uint8_t*>(dy);
+  m.p = static_cast<const uint8_t*>(x);
+  m.q_ld = m.Q = n_out;
+  m.p_ld = m.P = n_in;
+  m.mats = 1;
+  m.offsets = offsets;
+  m.E = E;
+  m.N = N;
+  m.out = dw;
+  m.out_stride = dw_stride;
+  return mats_launch(m, type, dw_type, whole_pieces({n_in, n_out}, {dy, x, dw}, {dw_stride}), s);
+}

@@ -1,0 +1,520 @@
+// Products of 16-bit matrices in tiles: out[q][p] = sum_k Q[q][k] P[p][k] with
+// fp32 sums on v_mfma_f32_32x32x16, for rows in expert order (a chunk of one
+// expert's rows by a tile of its matrix) and for the gradients of the matrices
+// (a tile of one expert's matrix, k over its rows).
+//
+// An operand's tile is held in LDS in one of two forms, by what is contiguous
+// in memory: k ("rows of k", read as fragments by 16-byte LDS reads), or q / p
+// itself ("rows of q", k apart, read by ds_read_b64_tr_b16, which turns four
+// rows of 16 elements into four k of each of 16 lanes).  So the products of the
+// way forward (both k), of dx = dy W (k; p) and of dW = dy^T x (q; p) take the
+// matrices as they lie in memory, none is transposed first.
+//
+// Pieces of 16 bytes are XOR-swizzled within their row, so that a fragment's
+// reads meet all banks evenly.
+#pragma once
+
+#include "chunks.h"
+#include "elem.h"
+#include "internal.h"
+
+namespace moe {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_v __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
+
+template <int TYPE>
+__device__ __forceinline__ f32x16_t mfma32(s16x8_t a, s16x8_t b, f32x16_t c) {
+  if constexpr (TYPE == MOE_TYPE_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_v, a), __builtin_bit_cast(bf16x8_v, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
+}
+
+// s_waitcnt vmcnt <= N, lgkmcnt == 0, then s_barrier, and no memory access
+// moved across it by the compiler.
+template <int N> __device__ __forceinline__ void stage_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (0 << 8));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// An operand of one block: R rows of q (or p), k in [0, K).
+struct Operand {
+  const uint8_t* base;          // KC: element (row 0, k 0); else (k 0, column 0)
+  const uint8_t* base2;         // PAIR: the second matrix's
+  const uint8_t* next;          // base in the second segment of k
+  long ld;                      // elements from row to row (KC), from k to k (else)
+  int n;                        // rows (KC) or columns (else) that exist, of R
+  int K;
+};
+
+constexpr uint32_t kNowhere = 0x80000000u;      // past the end of any buffer here
+
+// R rows of q by BK k of 16 bits: 2 R BK bytes, KC: [R][BK], else [BK][R].
+// PAIR (KC): rows come from two matrices in turns of 32 (32 of the first, the
+// same 32 of the second, ..).
+template <bool KC, int R, int BK, int NT, bool PAIR>
+struct Tile {
+  static constexpr int kBytes = 2 * R * BK;
+  static constexpr int kPieces = KC ? BK / 8 : R / 8;           // of a row
+  static constexpr int kPer = kBytes / 16 / NT;                 // pieces a thread
+  static_assert(kPer * NT * 16 == kBytes, "whole pieces a thread");
+  static constexpr int kRowsDma = 64 / kPieces > 0 ? 64 / kPieces : 1;
+
+  // swizzle of a row's pieces
+  static __device__ __forceinline__ int swz(int row) {
+    if constexpr (KC)
+      return BK == 64 ? (row & 7) ^ ((row >> 3) & 1) : (row >> 2) & 3;
+    else
+      return 4 * (row & 3 & (R / 32 - 1));
+  }
+  static __device__ __forceinline__ int pos(int row, int piece) {
+    return row * (16 * kPieces) + 16 * (piece ^ swz(row));
+  }
+
+  // Fragment of 32 rows of q from r0 and 16 k from 16 kk: lane l holds row
+  // l % 32 and k 8 (l / 32) .. + 7.
+  static __device__ __forceinline__ s16x8_t frag(const uint8_t* t, int r0, int kk, int lane) {
+    if constexpr (KC) {
+      return *reinterpret_cast<const s16x8_t*>(t + pos(r0 + (lane & 31), 2 * kk + (lane >> 5)));
+    } else {
+      typedef __attribute__((address_space(3))) s16x4_t lds4;
+      // lane i of 16: row i / 4 of four, four columns i % 4 of 16; lanes 16..31 the next 16 columns
+      const int i = lane & 15, row = 16 * kk + 8 * (lane >> 5) + (i >> 2);
+      const int piece = r0 / 8 + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+      const int at = pos(row, piece) + 8 * (i & 1);             // rows 4 apart: the same swizzle
+      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(t + at + 4 * 16 * kPieces));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+
+  // Row and piece of memory that go to the tile's 16 bytes number `at`.
+  static __device__ __forceinline__ void source(int at, int* row, int* piece) {
+    *row = at / kPieces;
+    *piece = (at % kPieces) ^ swz(*row);
+  }
+  // PAIR: row r of the tile is row `m` of matrix r / 32 % 2
+  static __device__ __forceinline__ int matrix_row(int row) { return PAIR ? (row >> 6) * 32 + (row & 31) : row; }
+
+  // ---- sizes of whole 16-byte pieces: memory to LDS by the buffer unit
+  uint32_t vo[kPer];
+  __device__ __forceinline__ void plan(const Operand& o) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      int row, piece;
+      source((int)(threadIdx.x >> 6) * (64 * kPer) + 64 * i + (threadIdx.x & 63), &row, &piece);
+      if constexpr (KC)
+        vo[i] = matrix_row(row) < o.n ? (uint32_t)(matrix_row(row) * o.ld * 2 + piece * 16) : kNowhere;
+      else
+        vo[i] = 8 * piece < o.n ? (uint32_t)(row * o.ld * 2 + piece * 16) : kNowhere;
+    }
+  }
+  // k0 .. k0 + BK of the operand (all zeros where k0 >= K)
+  __device__ __forceinline__ void dma(const Operand& o, uint8_t* t, int k0) const {
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if constexpr (KC) {
+      const uint32_t bytes = k0 < o.K ? kNowhere - 1 : 0;
+      const rsrc_t r1 = make_rsrc(o.base + 2l * k0, bytes);
+      const rsrc_t r2 = PAIR ? make_rsrc(o.base2 + 2l * k0, bytes) : r1;
+      const bool tail = k0 + BK > o.K;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = wave * (64 * kPer) + 64 * i;
+        uint32_t v = vo[i];
+        if (tail) {
+          int row, piece;
+          source(at + (threadIdx.x & 63), &row, &piece);
+          v = k0 + 8 * piece < o.K ? v : kNowhere;
+        }
+        const bool second = PAIR && ((at / kPieces) & 32);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? r2 : r1, lds_opaque(t + 16 * at), 16, v, 0, 0, 0);
+      }
+    } else {
+      const int left = o.K - k0;                // rows of k
+      const rsrc_t r = make_rsrc(o.base + 2l * k0 * o.ld, left > 0 ? (uint32_t)((left < BK ? left - 1 : BK - 1) * o.ld * 2 + 2 * ((o.n + 7) & ~7)) : 0);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = wave * (64 * kPer) + 64 * i;
+        const uint32_t v = vo[i];
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_opaque(t + 16 * at), 16, v, 0, 0, 0);
+      }
+    }
+  }
+
+  // ---- any size: through registers
+  __device__ __forceinline__ void fetch(const Operand& o, int k0, u32x4_t (&v)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      int row, piece;
+      source((int)threadIdx.x + NT * i, &row, &piece);
+      const uint8_t* b = o.base;
+      if (PAIR && (row & 32)) b = o.base2;
+      const long m = matrix_row(row);
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(b) + (KC ? m * o.ld + k0 + 8 * piece : (long)(k0 + row) * o.ld + 8 * piece);
+      const int have = KC ? (m < o.n ? o.K - k0 - 8 * piece : 0) : (k0 + row < o.K ? o.n - 8 * piece : 0);
+      if (have >= 8) {
+        v[i] = *reinterpret_cast<const Piece16*>(p);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (j < have) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+        v[i] = (u32x4_t){w[0], w[1], w[2], w[3]};
+      }
+    }
+  }
+  __device__ __forceinline__ void put(uint8_t* t, const u32x4_t (&v)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<u32x4_t*>(t + 16 * ((int)threadIdx.x + NT * i)) = v[i];
+  }
+};
+
+// Block shape: WQ x WP waves of TQ x TP tiles of 32 x 32, k in steps of BK
+// through NS stages.  AL: rows are whole 16-byte pieces at 16-byte addresses.
+template <int TYPE_, bool QK_, bool PK_, int WQ_, int WP_, int TQ_, int TP_, int BK_, int NS_, bool PAIR_, bool AL_>
+struct Shape {
+  static constexpr int TYPE = TYPE_, WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, BK = BK_, NS = AL_ ? NS_ : 2;
+  static constexpr bool QK = QK_, PK = PK_, PAIR = PAIR_, AL = AL_;
+  static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
+  typedef Tile<QK, BQ, BK, NT, false> QT;
+  typedef Tile<PK, BP, BK, NT, PAIR> PT;
+  static constexpr int kStage = QT::kBytes + PT::kBytes;
+  static constexpr int kLds = NS * kStage;
+};
+
+// acc[q][p] += the product over k, in one segment or two of K each (of the
+// operands at base, then at next); live_q of the wave's TQ tiles of q count.
+template <class S, int SEGS>
+__device__ __forceinline__ void tile_product(Operand qo, Operand po, uint8_t* lds, int live_q,
+                                             f32x16_t (&acc)[S::TQ][S::TP]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wq = wave / S::WP, wp = wave % S::WP;
+  const int per = (qo.K + S::BK - 1) / S::BK, steps = SEGS * per;
+  const auto compute = [&](const uint8_t* st) {
+#pragma unroll
+    for (int kk = 0; kk < S::BK / 16; ++kk) {
+      s16x8_t p[S::TP];
+#pragma unroll
+      for (int t = 0; t < S::TP; ++t) p[t] = S::PT::frag(st + S::QT::kBytes, 32 * (wp * S::TP + t), kk, lane);
+#pragma unroll
+      for (int q = 0; q < S::TQ; ++q) {
+        if (q < live_q) {
+          const s16x8_t f = S::QT::frag(st, 32 * (wq * S::TQ + q), kk, lane);
+#pragma unroll
+          for (int t = 0; t < S::TP; ++t) acc[q][t] = mfma32<S::TYPE>(p[t], f, acc[q][t]);
+        }
+      }
+    }
+  };
+  typename S::QT qt;
+  typename S::PT pt;
+  if constexpr (S::AL) {
+    constexpr int kDma = S::QT::kPer + S::PT::kPer;
+    qt.plan(qo);
+    pt.plan(po);
+    const auto issue = [&](int s) {
+      if (SEGS == 2 && s == per) {
+        qo.base = qo.next;
+        po.base = po.next;
+      }
+      uint8_t* st = lds + (s % S::NS) * S::kStage;
+      const int k0 = s < steps ? (SEGS == 2 && s >= per ? s - per : s) * S::BK : qo.K;
+      qt.dma(qo, st, k0);
+      pt.dma(po, st + S::QT::kBytes, k0);
+    };
+#pragma unroll
+    for (int s = 0; s < S::NS - 1; ++s) issue(s);
+    for (int s = 0; s < steps; ++s) {
+      stage_wait<(S::NS - 2) * kDma>();
+      issue(s + S::NS - 1);
+      compute(lds + (s % S::NS) * S::kStage);
+    }
+    stage_wait<0>();
+  } else {
+    u32x4_t qv[S::QT::kPer], pv[S::PT::kPer];
+    const auto fetch = [&](int s) {
+      if (SEGS == 2 && s == per) {
+        qo.base = qo.next;
+        po.base = po.next;
+      }
+      const int k0 = (SEGS == 2 && s >= per ? s - per : s) * S::BK;
+      qt.fetch(qo, k0, qv);
+      pt.fetch(po, k0, pv);
+    };
+    const auto put = [&](int s) {
+      uint8_t* st = lds + (s & 1) * S::kStage;
+      qt.put(st, qv);
+      pt.put(st + S::QT::kBytes, pv);
+    };
+    if (steps > 0) {
+      fetch(0);
+      put(0);
+    }
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+      if (s + 1 < steps) fetch(s + 1);
+      compute(lds + (s & 1) * S::kStage);
+      if (s + 1 < steps) put(s + 1);
+      __syncthreads();
+    }
+  }
+}
+
+// 32 rows of q by 32 NP columns of p, one wave: from the sums' layout (lane:
+// row l % 32, columns 8 (i / 4) + 4 (l / 32) + i % 4 of each 32) through the
+// wave's own LDS to rows in memory, each rounded once to OUT.  out: (row 0,
+// column 0); rows and cols that exist; rows whole 16-byte pieces (AL) or not.
+template <int OUT, int NP, bool AL>
+__device__ __forceinline__ void store_rows(uint8_t* lds, const f32x16_t* v, void* out, long ld, int rows, int cols) {
+  typedef typename El<OUT>::raw raw;
+  constexpr int kN = El<OUT>::kN;               // elements of a piece
+  constexpr int kPitch = 32 * NP * (int)sizeof(raw) + 16;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int t = 0; t < NP; ++t)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      typedef raw raw4 __attribute__((ext_vector_type(4)));
+      raw4 e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = El<OUT>::down(v[t][4 * b + i]);
+      *reinterpret_cast<raw4*>(lds + (lane & 31) * kPitch + (32 * t + 8 * b + 4 * (lane >> 5)) * sizeof(raw)) = e;
+    }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  constexpr int kRow = 32 * NP / kN;            // pieces a row
+#pragma unroll
+  for (int j = 0; j < 32 * kRow / 64; ++j) {
+    const int at = 64 * j + lane, row = at / kRow, c = (at % kRow) * kN;
+    if (row < rows && c < cols) {
+      const uint8_t* from = lds + row * kPitch + c * sizeof(raw);
+      raw* to = reinterpret_cast<raw*>(out) + row * ld + c;
+      if (AL || c + kN <= cols) {
+        *reinterpret_cast<Piece16*>(to) = *reinterpret_cast<const u32x4_t*>(from);
+      } else {
+        for (int i = 0; c + i < cols; ++i) to[i] = reinterpret_cast<const raw*>(from)[i];
+      }
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Which (unit, tile) a block works on.  Workgroups go to the 8 XCDs in turn,
+// each with its own L2: an XCD takes whole groups of `group` neighbouring units
+// (chunks of rows, or tiles of q) with all their tiles of p, so that what the
+// tiles share is read into one L2 (by_unit); or, where units are few, a range
+// of the tiles of p for all units.
+struct Grid {
+  int by_unit, group;
+  int tiles;                    // of p
+  int per_xcd;                  // !by_unit: tiles of p of an XCD
+  int unit0, units;             // this launch's
+};
+__device__ __forceinline__ bool grid_place(const Grid& g, int* unit, int* tile) {
+  const int xcd = blockIdx.x & 7, at = (int)(blockIdx.x >> 3);
+  const int row = g.by_unit ? g.tiles : g.per_xcd;
+  const int band = at / (g.group * row), in = at - band * (g.group * row);
+  const int u = in % g.group, t = in / g.group;
+  const int v = g.by_unit ? (band * 8 + xcd) * g.group + u : band * g.group + u;
+  *unit = g.unit0 + v;
+  *tile = g.by_unit ? t : xcd * g.per_xcd + t;
+  return v < g.units && *tile < g.tiles;
+}
+constexpr long kMaxBlocks = 1l << 22;           // of a launch (its threads are counted in 32 bits)
+// launch(grid, blocks) for all units, in as few launches as that allows
+template <class F> int grid_launch(long units, long tiles, int group, F launch) {
+  Grid g{};
+  g.tiles = (int)tiles;
+  g.group = group;
+  g.per_xcd = (int)((tiles + 7) / 8);
+  const long row = 8l * g.per_xcd;              // blocks a unit, at most
+  const long per = kMaxBlocks / row / (8 * group) * (8 * group);
+  if (per < 1) return MOE_ERR_UNSUPPORTED;
+  for (long u = 0; u < units; u += per) {
+    g.unit0 = (int)u;
+    g.units = (int)(units - u < per ? units - u : per);
+    g.by_unit = g.units >= 16 * group;
+    const long bands = g.by_unit ? (g.units + 8 * group - 1) / (8 * group) : (g.units + group - 1) / group;
+    MOE_TRY(launch(g, (unsigned)(8 * bands * group * (g.by_unit ? tiles : g.per_xcd))));
+  }
+  return MOE_OK;
+}
+
+// ------------------------------------------------- rows of x by a matrix
+struct RowsArgs {
+  const uint8_t* q;             // rows [N][q_ld]
+  long q_ld;
+  const uint8_t *p, *p2;        // the experts' matrices; the second ones (PAIR, or the second segment of k)
+  uint64_t p_stride, p2_stride; // bytes from expert to expert
+  long p_ld;
+  int K, P;                     // k of a segment; columns of the output
+  const int32_t* offsets;       // [E + 1], or null: one matrix for all rows
+  int E;
+  long N;
+  int act;
+  void *out, *pre;              // [N][P]; or null, or [N][2 P]
+  Grid grid;
+};
+
+__device__ __forceinline__ float sigmoid_fast(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+constexpr float kGeluB = 1.5957691216057308f;   // 2 sqrt(2 / pi): gelu_tanh(g) = g sigmoid(kGeluB (g + 0.044715 g^3))
+__device__ __forceinline__ float act_value(int act, float g) {
+  if (act == MOE_ACT_SILU) return g * sigmoid_fast(g);
+  if (act == MOE_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  return g * sigmoid_fast(kGeluB * (g + 0.044715f * g * g * g));
+}
+// act(g) and its derivative
+__device__ __forceinline__ float act_slope(int act, float g, float* value) {
+  if (act == MOE_ACT_GELU) {
+    const float p = 0.5f * erfcf(g * -0.70710678118654752f);
+    *value = g * p;
+    return fmaf(g, 0.39894228040143268f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f), p);
+  }
+  const bool silu = act == MOE_ACT_SILU;
+  const float s = sigmoid_fast(silu ? g : kGeluB * (g + 0.044715f * g * g * g));
+  *value = g * s;
+  if (fabsf(g) > 1e4f) return s;                // s is 0 or 1 here, and g * g might overflow
+  return s * fmaf(g * (1.f - s), silu ? 1.f : kGeluB * fmaf(0.134145f * g, g, 1.f), 1.f);
+}
+
+// GATED: out = act(x p^T) (x p2^T), and both products before it to pre.
+template <class S, int SEGS, bool GATED, int OUT>
+__global__ __launch_bounds__(S::NT) void rows_kernel(RowsArgs a) {
+  extern __shared__ uint8_t tile_lds[];
+  static_assert(!GATED || (S::PAIR && S::TP % 2 == 0), "tiles of both matrices in a wave");
+  constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
+  int unit, tile;
+  if (!grid_place(a.grid, &unit, &tile)) return;
+  long start;
+  int n, e = 0;
+  if (a.offsets) {
+    const RowChunk c = find_chunk(a.offsets, nullptr, a.E, a.N, unit, S::BQ);
+    if (!c.any || c.n == 0) return;
+    start = c.start;
+    n = c.n;
+    e = c.slot;
+  } else {
+    start = (long)unit * S::BQ;
+    n = a.N - start < S::BQ ? (int)(a.N - start) : S::BQ;
+  }
+  constexpr int kCols = GATED ? S::BP / 2 : S::BP;
+  const int p0 = tile * kCols;
+  const int cols = a.P - p0 < kCols ? a.P - p0 : kCols;
+  Operand q{}, p{};
+  q.base = a.q + 2 * start * a.q_ld;
+  q.next = q.base + 2l * a.K;
+  q.ld = a.q_ld;
+  q.n = n;
+  q.K = p.K = a.K;
+  const uint64_t off = 2ull * (uint64_t)p0 * (S::PK ? a.p_ld : 1);
+  p.base = a.p + (uint64_t)e * a.p_stride + off;
+  p.base2 = p.next = a.p2 + (uint64_t)e * a.p2_stride + off;
+  p.ld = a.p_ld;
+  p.n = cols;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wq = wave / S::WP, wp = wave % S::WP;
+  const int left = n - 32 * wq * S::TQ;
+  const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
+  f32x16_t acc[S::TQ][S::TP] = {};
+  tile_product<S, SEGS>(q, p, tile_lds, live, acc);
+  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+#pragma unroll
+  for (int t = 0; t < S::TQ; ++t) {
+    if (t >= live) continue;
+    const long r0 = start + 32 * (wq * S::TQ + t);
+    const int rows = left - 32 * t < 32 ? left - 32 * t : 32;
+    if constexpr (GATED) {
+      constexpr int kH = S::TP / 2;
+      const int c0 = 32 * kH * wp, have = cols - c0;
+      f32x16_t h[kH], g[kH], u[kH];
+#pragma unroll
+      for (int j = 0; j < kH; ++j) {
+        g[j] = acc[t][2 * j];
+        u[j] = acc[t][2 * j + 1];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[j][i] = act_value(a.act, g[j][i]) * u[j][i];
+      }
+      store_rows<OUT, kH, S::AL>(mine, h, static_cast<uint8_t*>(a.out) + kSize * (r0 * a.P + p0 + c0), a.P, rows, have);
+      if (a.pre) {
+        uint8_t* to = static_cast<uint8_t*>(a.pre) + kSize * (2 * r0 * a.P + p0 + c0);
+        store_rows<OUT, kH, S::AL>(mine, g, to, 2l * a.P, rows, have);
+        store_rows<OUT, kH, S::AL>(mine, u, to + kSize * (long)a.P, 2l * a.P, rows, have);
+      }
+    } else {
+      const int c0 = 32 * S::TP * wp;
+      store_rows<OUT, S::TP, S::AL>(mine, acc[t], static_cast<uint8_t*>(a.out) + kSize * (r0 * a.P + p0 + c0), a.P, rows,
+                                    cols - c0);
+    }
+  }
+}
+
+// ------------------------------------------- gradients of the matrices
+struct MatsArgs {
+  const uint8_t *q, *p;         // [N][q_ld], [N][p_ld]
+  long q_ld, p_ld;
+  int Q, P;                     // the matrix: dW[Q][P] = sum over an expert's rows of q p
+  int q_tiles;                  // of a matrix
+  int mats;                     // 1, or 2: columns Q .. 2 Q - 1 of q give the second matrix
+  const int32_t* offsets;
+  int E;
+  long N;
+  void *out, *out2;
+  uint64_t out_stride, out2_stride;             // bytes from expert to expert
+  Grid grid;
+};
+template <class S, int OUT>
+__global__ __launch_bounds__(S::NT) void mats_kernel(MatsArgs a) {
+  extern __shared__ uint8_t tile_lds[];
+  constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
+  int unit, tile;
+  if (!grid_place(a.grid, &unit, &tile)) return;
+  const int per = a.mats * a.q_tiles, e = unit / per, qt = unit - e * per;
+  const int second = qt >= a.q_tiles ? 1 : 0;
+  long start = 0, end = a.N;
+  if (a.offsets) {
+    start = a.offsets[e];
+    end = a.offsets[e + 1];
+    start = start < 0 ? 0 : start;
+    end = end > a.N ? a.N : end;
+    if (end < start) start = end = 0;
+  }
+  const int q0 = (qt - second * a.q_tiles) * S::BQ, p0 = tile * S::BP;
+  Operand q{}, p{};
+  q.base = a.q + 2 * (start * a.q_ld + second * a.Q + q0);
+  q.ld = a.q_ld;
+  q.n = a.Q - q0 < S::BQ ? a.Q - q0 : S::BQ;
+  p.base = a.p + 2 * (start * a.p_ld + p0);
+  p.ld = a.p_ld;
+  p.n = a.P - p0 < S::BP ? a.P - p0 : S::BP;
+  q.K = p.K = (int)(end - start);
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wq = wave / S::WP, wp = wave % S::WP;
+  const int left = q.n - 32 * wq * S::TQ;
+  const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
+  f32x16_t acc[S::TQ][S::TP] = {};
+  tile_product<S, 1>(q, p, tile_lds, live, acc);
+  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+  uint8_t* out = second ? static_cast<uint8_t*>(a.out2) + (uint64_t)e * a.out2_stride
+                        : static_cast<uint8_t*>(a.out) + (uint64_t)e * a.out_stride;
+#pragma unroll
+  for (int t = 0; t < S::TQ; ++t) {
+    if (t >= live) continue;
+    const long r0 = q0 + 32 * (wq * S::TQ + t);
+    const int c0 = p0 + 32 * S::TP * wp;
+    store_rows<OUT, S::TP, S::AL>(mine, acc[t], out + kSize * (r0 * a.P + c0), a.P, left - 32 * t < 32 ? left - 32 * t : 32,
+                                  a.P - c0);
+  }
+}
+
+}  // namespace moe

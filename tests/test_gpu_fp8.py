@@ -1,0 +1,214 @@
+"""Quantisation to e4m3 and products of e4m3 codes on the GPU against fp64.
+
+Codes of 16-bit values are those of exact arithmetic, bit for bit: 448 v is
+exact and the quotient by the block's largest magnitude, rounded to fp32, is on
+the same side of every border between two codes as the exact one (borders have
+5 significant bits, so a quotient of an 11-bit by an 11-bit number that is not
+on one is 2^-16 of it away at least).  448 v of fp32 values is rounded as well:
+there a quotient within 2^-22 of a border may go to either side.  Scales are one fp32 division.
+
+Products, derived.  The matrix core adds the products of 8 consecutive inputs
+at once, each cut towards zero to whole multiples of 2^-13 of the largest's
+power of two (test_what_the_matrix_core_drops holds it to that): 7 of them lose
+less than 7 2^-13 m, m the largest |x w| of the 8.  Everything else is fp32,
+each addition off by at most s = 2^-23 of the partial sum: 16 groups of 8 a
+block, two scales multiplied, the scaled sum added to the running one, so
+    |y - y*| <= sum_b sx sw (7 2^-13 sum_8 m + (16 + B + 4) s sum |x| |w|) + u |y*|,
+B blocks, u the rounding of the output's type."""
+import numpy as np
+import pytest
+
+from oracle import products as oproducts
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+moe = pytest.importorskip("sparse_moe_decode_router_amd")
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+E4M3 = torch.float8_e4m3fn
+
+
+def _bytes(codes):
+    return codes.view(torch.uint8).cpu().numpy()
+
+
+def _values(rng, rows, n, t):
+    v = rng.standard_normal((rows, n)) * np.exp2(rng.integers(-9, 9, (rows, n)))
+    v[rng.random((rows, n)) < 0.05] = 0.0
+    return torch.from_numpy(v).to(t)
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("rows,n", [(1, 1), (1, 128), (3, 130), (5, 2048), (17, 1001), (40, 64), (128, 256), (129, 136),
+                                    (300, 100), (260, 513)])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize(t, rows, n, block_rows):
+    x = _values(np.random.default_rng([rows, n]), rows, n, t)
+    codes, scales = moe.moe_quantize_fp8(x.cuda(), block_rows)
+    want, s = oproducts.quantize_fp8(x.double().numpy(), block_rows)
+    assert np.array_equal(scales.cpu().numpy(), (s * 448).astype(np.float32) / np.float32(448))
+    got = _bytes(codes)
+    if t == F32:
+        up = lambda a, m, axis, k: np.take(np.repeat(a, k, axis), np.arange(m), axis)
+        q = np.abs(x.double().numpy()) / up(up(s, rows, 0, block_rows), n, 1, 128)
+        mid = (oproducts.E4M3[1:] + oproducts.E4M3[:-1]) / 2
+        near = (np.abs(q[..., None] / mid - 1) < 2.0 ** -22).any(-1)
+        assert near.mean() < 0.01
+        got, want = np.where(near, 0, got), np.where(near, 0, want)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+def test_quantize_ties_and_every_code(t):
+    """A block whose largest magnitude is 448 keeps every e4m3 number, and every
+    midpoint of two goes to the even one."""
+    mid = (oproducts.E4M3[1:] + oproducts.E4M3[:-1]) / 2
+    v = np.concatenate([oproducts.E4M3, mid, -oproducts.E4M3, -mid])
+    v = np.concatenate([v, np.zeros(-len(v) % 127)]).reshape(-1, 127)
+    x = torch.from_numpy(np.concatenate([np.full((len(v), 1), 448.0), v], 1)).to(t)
+    assert torch.equal(x.double(), torch.from_numpy(np.concatenate([np.full((len(v), 1), 448.0), v], 1)))
+    codes, scales = moe.moe_quantize_fp8(x.cuda())
+    assert (scales == 1).all() and np.array_equal(_bytes(codes), oproducts.e4m3_codes(x.double().numpy()))
+
+
+def test_quantize_extremes():
+    """Zeros, the smallest and the largest values; blocks that are not finite spoil themselves only."""
+    x = torch.zeros(8, 256)
+    x[1, :128] = torch.linspace(-1, 1, 128) * 3.3e38
+    x[2, :128] = 1e-38
+    x[3, :128] = 2.0 ** -96
+    x[4, 5] = float("inf")
+    x[5, 200] = float("nan")
+    x[6] = 2.0 ** 100
+    x[:, 255] += 1.0
+    for t in (F32, BF16):
+        xt = x.to(t)
+        codes, scales = (v.cpu() for v in moe.moe_quantize_fp8(xt.cuda()))
+        up = codes.double() * scales.double().repeat_interleave(128, 1)
+        ok = torch.ones(8, 256, dtype=torch.bool)
+        ok[4, :128], ok[5, 128:] = False, False
+        # half a step of a code, or of the smallest, 2^-9 scales (2^-96 / 448 at least)
+        tol = torch.maximum(xt.double().abs() * 2.0 ** -4 * 1.001, scales.double().repeat_interleave(128, 1) * 2.0 ** -10 * 1.001)
+        assert ((up - xt.double()).abs() <= tol)[ok].all()
+        assert (scales[3, 0] == 2.0 ** -96 / 448) and (codes[0, :128].float() == 0).all()
+        assert not torch.isfinite(up[4, 5]) and not torch.isfinite(up[5, 200])
+    w = torch.randn(33, 256).cuda()
+    wc, ws = moe.moe_quantize_fp8(w, 128)
+    y = moe.moe_linear_fp8(wc, ws, *moe.moe_quantize_fp8(x.cuda()))
+    assert not torch.isfinite(y[4]).any() and not torch.isfinite(y[5]).any()
+    # (row 1 holds 128 values of up to 3.3e38, whose products with w of order one pass fp32's largest, 3.4e38)
+    assert torch.isfinite(y[[0, 2, 3, 6, 7]]).all()
+
+
+def test_quantize_batches_and_views():
+    x = torch.randn(5, 200, 264, device="cuda").bfloat16()
+    c, s = moe.moe_quantize_fp8(x, 128)
+    assert c.shape == x.shape and s.shape == (5, 2, 3)
+    for i in range(5):
+        ci, si = moe.moe_quantize_fp8(x[i], 128)
+        assert torch.equal(ci.view(torch.uint8), c[i].view(torch.uint8)) and torch.equal(si, s[i])
+    flat = torch.zeros(200 * 264 + 3, dtype=BF16, device="cuda")
+    odd = flat[3:].view(200, 264)                                # no 16-byte address
+    odd.copy_(x[0])
+    for br in (1, 128):
+        for a, b in zip(moe.moe_quantize_fp8(odd, br), moe.moe_quantize_fp8(x[0], br)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def _case(N, n_in, n_out, E, behind, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rng = np.random.default_rng([N, n_in, n_out, E])
+    lead = (E,) if E else ()
+    w = (torch.randn(*lead, n_out, n_in, generator=g, device="cuda") *
+         torch.exp2(torch.randint(-3, 4, (*lead, n_out, 1), generator=g, device="cuda"))).bfloat16()
+    x = torch.randn(N, n_in, generator=g, device="cuda").bfloat16()
+    off = None
+    if E:
+        p = rng.permutation(1.0 / np.arange(1, E + 1) ** 1.2)
+        off = np.concatenate([[0], np.cumsum(rng.multinomial(N - behind, p / p.sum()))]).astype(np.int32)
+        x[int(off[-1]):] = float("nan")
+    return (*moe.moe_quantize_fp8(w, 128), *moe.moe_quantize_fp8(x), off)
+
+
+def _check(y, wc, ws, xc, xs, off, what=""):
+    n_out, n_in = wc.shape[-2:]
+    up = lambda s, n, axis: s.double().repeat_interleave(128, axis).narrow(axis, 0, n)
+    u = 2.0 ** -24 if y.dtype == F32 else torch.finfo(y.dtype).eps / 2
+    buckets = [(0, 0, y.shape[0])] if off is None else [(e, off[e], off[e + 1]) for e in range(len(off) - 1)]
+    end = y.shape[0]
+    for e, a, b in buckets:
+        we, se = (wc, ws) if off is None else (wc[e], ws[e])
+        W = we.double() * up(up(se, n_out, 0), n_in, 1)
+        X = xc[a:b].double() * up(xs[a:b], n_in, 1)
+        want = X @ W.t()
+        cut = torch.zeros_like(want)
+        if b > a:
+            for k in range(0, n_in, 8):
+                top = torch.zeros_like(want)
+                for j in range(k, k + 8):
+                    top = torch.maximum(top, X[:, j].abs().unsqueeze(1) * W[:, j].abs())
+                cut += 7 * 2.0 ** -13 * top
+        tol = cut + (16 + xs.shape[1] + 4) * 2.0 ** -23 * (X.abs() @ W.abs().t()) + u * want.abs() + (2.0 ** -25 if y.dtype == F16 else 0)
+        bad = ~((y[a:b].double() - want).abs() <= tol)
+        assert not bad.any(), (what, e, a, b, bad.nonzero()[0].tolist(), int(bad.sum()))
+        end = b
+    assert torch.isnan(y[end:]).all()
+
+
+DENSE = [(1, 16, 1), (1, 128, 128), (1, 2048, 512), (1, 2048, 5003), (2, 144, 33), (7, 4096, 130), (16, 256, 300),
+         (17, 400, 129), (31, 128, 64), (33, 512, 257), (64, 1024, 1000), (65, 272, 200), (128, 128, 128), (129, 2064, 131),
+         (300, 640, 520), (1000, 96, 77)]
+
+
+@pytest.mark.parametrize("N,n_in,n_out", DENSE)
+@pytest.mark.parametrize("t", [F32, BF16, F16])
+def test_linear_dense(N, n_in, n_out, t):
+    wc, ws, xc, xs, _ = _case(N, n_in, n_out, 0, 0)
+    y = moe.moe_linear_fp8(wc, ws, xc, xs, out=torch.full((N, n_out), float("nan"), dtype=t, device="cuda"))
+    _check(y, wc, ws, xc, xs, None)
+
+
+@pytest.mark.parametrize("N,n_in,n_out,E,behind", [
+    (1, 64, 64, 1, 0), (10, 512, 2048, 64, 0), (10, 2048, 512, 512, 1), (7, 32, 40, 3, 2), (40, 144, 65, 9, 3),
+    (96, 256, 136, 8, 11), (300, 80, 88, 5, 0), (700, 208, 264, 3, 77), (640, 48, 100, 64, 5), (1500, 64, 72, 1024, 100),
+    (2100, 144, 392, 12, 0), (129, 1008, 56, 2, 1)])
+def test_linear_experts(N, n_in, n_out, E, behind):
+    wc, ws, xc, xs, off = _case(N, n_in, n_out, E, behind)
+    o = torch.from_numpy(off).cuda()
+    t = [F32, BF16, F16][N % 3]
+    y = moe.moe_linear_fp8(wc, ws, xc, xs, o, out=torch.full((N, n_out), float("nan"), dtype=t, device="cuda"))
+    _check(y, wc, ws, xc, xs, off)
+    alloc = moe.moe_linear_fp8(wc, ws, xc, xs, o)
+    assert alloc.dtype == F32 and (alloc[int(off[-1]):] == 0).all()
+
+
+@pytest.mark.parametrize("small", [1.0, 1.5, 1.875])
+@pytest.mark.parametrize("m", range(8, 18))
+def test_what_the_matrix_core_drops(m, small):
+    """2^16 and seven products of +- small 2^(16 - m): whole multiples of 2^3 of
+    each are kept where they are added at once, everything where they are not."""
+    one = torch.ones(1, 1, device="cuda")
+    for sign in (1.0, -1.0):
+        for apart in (1, 8):
+            x, w = torch.zeros(1, 128), torch.zeros(1, 128)
+            x[0, 0] = w[0, 0] = 256.0
+            for i in range(1, 8):
+                x[0, i * apart], w[0, i * apart] = sign * small * 2.0 ** (8 - m // 2), 2.0 ** (8 - (m - m // 2))
+            y = moe.moe_linear_fp8(w.to(E4M3).cuda(), one, x.to(E4M3).cuda(), one).item()
+            p = small * 2.0 ** (16 - m)
+            exact, kept = 65536 + 7 * sign * p, 65536 + 7 * sign * (p // 8 * 8)
+            assert (y == exact) if apart == 8 else (abs(y - exact) <= abs(kept - exact)), (sign, apart, y, exact, kept)
+
+
+def test_matrices_apart():
+    """Experts' codes and scales as views into larger tensors."""
+    wc, ws, xc, xs, off = _case(60, 144, 200, 4, 0)
+    big = torch.zeros(4, 200 * 144 + 48, dtype=torch.uint8, device="cuda")
+    view = torch.as_strided(big.view(E4M3), (4, 200, 144), (big.stride(0), 144, 1), 16)
+    view.copy_(wc)
+    sbig = torch.full((4, ws[0].numel() + 5), float("nan"), device="cuda")
+    sview = torch.as_strided(sbig, ws.shape, (sbig.stride(0), ws.shape[2], 1), 3)
+    sview.copy_(ws)
+    o = torch.from_numpy(off).cuda()
+    assert torch.equal(moe.moe_linear_fp8(view, sview, xc, xs, o), moe.moe_linear_fp8(wc, ws, xc, xs, o))
