@@ -170,8 +170,10 @@ def _run_own(st):
         if not c["grad"]:
             return {"h": moe.moe_gated(st["w_gate"], st["w_up"], st["x"], st["offsets"], act=c["act"],
                                        out=st["h_out"])}
+        # what the gradients need, in fp32
+        pre = torch.empty(st["x"].shape[0], 2 * c["I"], device="cuda")
         h, pre = moe.moe_gated(st["w_gate"], st["w_up"], st["x"], st["offsets"], act=c["act"], save=True,
-                               out=(st["h_out"], st["pre_out"]))
+                               out=(st["h_out"], pre))
         dx, dwg, dwu = moe.moe_gated_backward(st["dh"], pre, st["w_gate"], st["w_up"], st["x"], st["offsets"],
                                               act=c["act"], workspace=st["ws"], out=st["grads"])
         return {"h": h, "dx": dx, "dw_gate": dwg, "dw_up": dwu}
