@@ -637,7 +637,7 @@ int moe_linear_backward(const void* dy_dev, const void* w_dev,
  * g and u in fp32 until h is rounded.  act: MOE_ACT_SILU g / (1 + e^-g),
  * MOE_ACT_GELU g (1 + erf(g / sqrt 2)) / 2, MOE_ACT_GELU_TANH
  * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.  pre_dev (or NULL): g | u
- * [N][2 I] in `type`, what the gradients need. */
+ * [N][2 I] in fp32, what the gradients need. */
 enum {
   MOE_ACT_SILU = 0,
   MOE_ACT_GELU = 1,
@@ -647,13 +647,13 @@ int moe_gated(const void* w_gate_dev, size_t gate_stride_bytes,
               const void* w_up_dev, size_t up_stride_bytes, int32_t E,
               const void* x_dev, int32_t type, int32_t N, int32_t d, int32_t I,
               const int32_t* offsets_dev, int32_t act, void* h_dev,
-              void* pre_dev, hipStream_t stream);
+              float* pre_dev, hipStream_t stream);
 /* From dh [N][I] and the saved pre: dg = dh u act'(g) and du = dh act(g)
  * (rounded to `type` in the workspace), dx = dg Wg + du Wu, dWg = dg^T x,
  * dWu = du^T x; dx, or both gradients of matrices, may be NULL.  The workspace
  * (16-byte aligned) needs no fill. */
 size_t moe_gated_backward_workspace_bytes(int32_t N, int32_t I);
-int moe_gated_backward(const void* dh_dev, const void* pre_dev,
+int moe_gated_backward(const void* dh_dev, const float* pre_dev,
                        const void* w_gate_dev, size_t gate_stride_bytes,
                        const void* w_up_dev, size_t up_stride_bytes, int32_t E,
                        const void* x_dev, int32_t type, int32_t N, int32_t d,

@@ -961,7 +961,7 @@ def moe_linear_backward(dy, w, x, offsets=None, out=None, stream=None):
 def moe_gated(w_gate, w_up, x, offsets=None, act: str = "silu", save: bool = False, out=None, stream=None):
     """h [N, I] = act(x Wg^T) * (x Wu^T): x [N, d], w_gate and w_up [I, d], or
     with offsets [E, I, d]; act "silu", "gelu" or "gelu_tanh".  With save
-    (h, pre): pre [N, 2 I] holds both products for moe_gated_backward.  out: h,
+    (h, pre): pre fp32 [N, 2 I] holds both products for moe_gated_backward.  out: h,
     or that pair.  Rows outside the buckets keep what they held, or are zeros in
     buffers allocated here."""
     if stream is not None:
@@ -972,7 +972,7 @@ def moe_gated(w_gate, w_up, x, offsets=None, act: str = "silu", save: bool = Fal
         I = _matrices(w_gate, "w_gate", offsets)[0]
         out = _rows_out(x, I, offsets)
         if save:
-            out = (out, _rows_out(x, 2 * I, offsets))
+            out = (out, _rows_out(x, 2 * I, offsets, torch.float32))
     h, pre = out if save else (out, None)
     if save and pre is None:
         raise ValueError("pre: a device tensor is wanted")

@@ -417,7 +417,7 @@ PyObject* py_gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const On on(dev);
     return g.gated(wg.p, wg.stride, wu.p, wu.stride, wg.E, need(x, "x", t, {N, wg.n_in}, dev), type_code(t), size32(N, "N"),
                    size32(wg.n_in, "d"), size32(I, "I"), borders(a[3], wg.E, dev), number32(a[4], "act"),
-                   need<void>(a[5], "h", t, {N, I}, dev), may<void>(a[6], "pre", t, {N, 2 * I}, dev), on.stream);
+                   need<void>(a[5], "h", t, {N, I}, dev), may<float>(a[6], "pre", kF32, {N, 2 * I}, dev), on.stream);
   });
 }
 
@@ -435,7 +435,7 @@ PyObject* py_gated_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     size_t nws;
     uint8_t* ws = workspace(a[10], dev, &nws);
     const On on(dev);
-    return g.gated_grad(need(dh, "dh", t, {N, I}, dev), need<void>(a[1], "pre", t, {N, 2 * I}, dev), wg.p, wg.stride, wu.p,
+    return g.gated_grad(need(dh, "dh", t, {N, I}, dev), need<float>(a[1], "pre", kF32, {N, 2 * I}, dev), wg.p, wg.stride, wu.p,
                         wu.stride, wg.E, need<void>(a[4], "x", t, {N, d}, dev), type_code(t), size32(N, "N"), size32(d, "d"),
                         size32(I, "I"), borders(a[5], wg.E, dev), number32(a[6], "act"),
                         may<void>(a[7], "dx", t, {N, d}, dev), dg.p, dg.stride, du.p, du.stride, type_code(td), ws, nws,

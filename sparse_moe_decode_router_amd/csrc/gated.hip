@@ -7,9 +7,9 @@
 // its relatives).  Both products and the activation are one kernel: a wave
 // holds the same 32 columns of g and of u in the same registers, so h is formed
 // on the fp32 sums and rounded once.  For the gradients g and u are saved in
-// the rows' type (a second rounding of them that moves dg and du by about as
-// much as their own rounding to matrix operands does; fp32 would double what
-// is kept of every row).
+// fp32: dg and du have to be rounded to the rows' type, as operands of the
+// matrix cores, which alone moves dx and dW by as much as their own rounding
+// does; g and u rounded as well moved them by 1.8 instead of 1.4 times that.
 #include "products.h"
 
 namespace moe {
@@ -24,10 +24,20 @@ template <int TYPE, bool AL> int backward_dx(RowsArgs& a, hipStream_t s) {
   return rows_grid<S, 2, false, TYPE>(a, s);
 }
 
+// VN consecutive fp32 values
+template <int VN> __device__ __forceinline__ void load_f32(const float* p, float (&v)[VN]) {
+  constexpr int kN = VN == 8 ? 4 : 1;
+#pragma unroll
+  for (int h = 0; h < VN / kN; ++h) {
+    const Vec<MOE_TYPE_F32, kN> e = vec_load<MOE_TYPE_F32, kN>(p + h * kN);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[h * kN + i] = e.e[i];
+  }
+}
 // dg | du [N][2 I] from dh [N][I] and pre = g | u [N][2 I], VN elements a
 // thread: bound by HBM.
 template <int TYPE, int VN>
-__global__ __launch_bounds__(256) void slope_kernel(const typename El<TYPE>::raw* dh, const typename El<TYPE>::raw* pre,
+__global__ __launch_bounds__(256) void slope_kernel(const typename El<TYPE>::raw* dh, const float* pre,
                                                     typename El<TYPE>::raw* out, int I, long pieces, int act) {
   const int row_pieces = I / VN;
   const long first = (long)blockIdx.x * 256;
@@ -37,28 +47,29 @@ __global__ __launch_bounds__(256) void slope_kernel(const typename El<TYPE>::raw
   const long row = row0 + in / (unsigned)row_pieces;
   const int c = (int)(in % (unsigned)row_pieces) * VN;
   const Vec<TYPE, VN> d = vec_load<TYPE, VN>(dh + row * I + c);
-  const Vec<TYPE, VN> g = vec_load<TYPE, VN>(pre + 2 * row * I + c);
-  const Vec<TYPE, VN> u = vec_load<TYPE, VN>(pre + (2 * row + 1) * I + c);
+  float g[VN], u[VN];
+  load_f32<VN>(pre + 2 * row * I + c, g);
+  load_f32<VN>(pre + (2 * row + 1) * I + c, u);
   Vec<TYPE, VN> dg, du;
 #pragma unroll
   for (int i = 0; i < VN; ++i) {
     float f;
-    const float df = act_slope(act, El<TYPE>::up(g.e[i]), &f), v = El<TYPE>::up(d.e[i]);
-    dg.e[i] = El<TYPE>::down(v * El<TYPE>::up(u.e[i]) * df);
+    const float df = act_slope(act, g[i], &f), v = El<TYPE>::up(d.e[i]);
+    dg.e[i] = El<TYPE>::down(v * u[i] * df);
     du.e[i] = El<TYPE>::down(v * f);
   }
   vec_store<TYPE, VN>(out + 2 * row * I + c, dg);
   vec_store<TYPE, VN>(out + (2 * row + 1) * I + c, du);
 }
 template <int TYPE>
-int slope(const void* dh, const void* pre, void* out, long N, int I, int act, hipStream_t s) {
+int slope(const void* dh, const float* pre, void* out, long N, int I, int act, hipStream_t s) {
   typedef typename El<TYPE>::raw raw;
   const int vn = I % 8 == 0 ? 8 : 1;
   const long per = (1l << 30) / (I / vn);       // rows a launch
   for (long r = 0; r < N; r += per) {
     const long rows = N - r < per ? N - r : per, pieces = rows * (I / vn);
     const raw* d = static_cast<const raw*>(dh) + r * I;
-    const raw* p = static_cast<const raw*>(pre) + 2 * r * I;
+    const float* p = pre + 2 * r * I;
     raw* o = static_cast<raw*>(out) + 2 * r * I;
     const unsigned blocks = (unsigned)((pieces + 255) / 256);
     if (vn == 8)
@@ -79,12 +90,12 @@ using namespace moe;
 
 extern "C" int moe_gated(const void* w_gate, size_t gate_stride, const void* w_up, size_t up_stride, int32_t E,
                          const void* x, int32_t type, int32_t N, int32_t d, int32_t I, const int32_t* offsets,
-                         int32_t act, void* h, void* pre, hipStream_t s) {
+                         int32_t act, void* h, float* pre, hipStream_t s) {
   MOE_TRY(product_check(E, type, N, d, I, offsets));
   MOE_CHECK(act_ok(act) && matrices_ok(w_gate, gate_stride, E, (long)d * I) &&
             matrices_ok(w_up, up_stride, E, (long)d * I));
   if (N == 0) return MOE_OK;
-  MOE_CHECK(w_gate && w_up && x && h && aligned(x, 2) && aligned(h, 2) && aligned(pre, 2));
+  MOE_CHECK(w_gate && w_up && x && h && aligned(x, 2) && aligned(h, 2) && aligned(pre, 4));
   RowsArgs a{};
   a.q = static_cast<const uint8_t*>(x);
   a.q_ld = a.p_ld = a.K = d;
@@ -108,7 +119,7 @@ extern "C" size_t moe_gated_backward_workspace_bytes(int32_t N, int32_t I) {
   return N < 0 || N > (1 << 30) || I < 1 || I > kMostSize ? 0 : (size_t)N * I * 4 + 256;
 }
 
-extern "C" int moe_gated_backward(const void* dh, const void* pre, const void* w_gate, size_t gate_stride,
+extern "C" int moe_gated_backward(const void* dh, const float* pre, const void* w_gate, size_t gate_stride,
                                   const void* w_up, size_t up_stride, int32_t E, const void* x, int32_t type,
                                   int32_t N, int32_t d, int32_t I, const int32_t* offsets, int32_t act, void* dx,
                                   void* dw_gate, size_t dw_gate_stride, void* dw_up, size_t dw_up_stride,
@@ -119,7 +130,7 @@ extern "C" int moe_gated_backward(const void* dh, const void* pre, const void* w
   MOE_CHECK(!dw_gate || ((dw_type == type || dw_type == MOE_TYPE_F32) &&
                          matrices_ok(dw_gate, dw_gate_stride, E, (long)d * I, type_size(dw_type)) &&
                          matrices_ok(dw_up, dw_up_stride, E, (long)d * I, type_size(dw_type))));
-  MOE_CHECK(N == 0 || (dh && pre && ws && aligned(dh, 2) && aligned(pre, 2) && aligned(ws, 16) &&
+  MOE_CHECK(N == 0 || (dh && pre && ws && aligned(dh, 2) && aligned(pre, 4) && aligned(ws, 16) &&
                        ws_bytes >= moe_gated_backward_workspace_bytes(N, I) &&
                        (!dx || (w_gate && w_up && aligned(dx, 2))) && (!dw_gate || (x && aligned(x, 2)))));
   if (N > 0) {

@@ -361,7 +361,8 @@ struct RowsArgs {
   int E;
   long N;
   int act;
-  void *out, *pre;              // [N][P]; or null, or [N][2 P]
+  void* out;                    // [N][P]
+  float* pre;                   // null, or [N][2 P]
   Grid grid;
 };
 
@@ -447,9 +448,9 @@ __global__ __launch_bounds__(S::NT) void rows_kernel(RowsArgs a) {
       }
       store_rows<OUT, kH, S::AL>(mine, h, static_cast<uint8_t*>(a.out) + kSize * (r0 * a.P + p0 + c0), a.P, rows, have);
       if (a.pre) {
-        uint8_t* to = static_cast<uint8_t*>(a.pre) + kSize * (2 * r0 * a.P + p0 + c0);
-        store_rows<OUT, kH, S::AL>(mine, g, to, 2l * a.P, rows, have);
-        store_rows<OUT, kH, S::AL>(mine, u, to + kSize * (long)a.P, 2l * a.P, rows, have);
+        float* to = a.pre + 2 * r0 * a.P + p0 + c0;
+        store_rows<MOE_TYPE_F32, kH, S::AL>(mine, g, to, 2l * a.P, rows, have);
+        store_rows<MOE_TYPE_F32, kH, S::AL>(mine, u, to + a.P, 2l * a.P, rows, have);
       }
     } else {
       const int c0 = 32 * S::TP * wp;

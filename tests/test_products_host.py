@@ -133,7 +133,7 @@ def test_gated_refusals():
                    dict(us=4094), dict(us=8193), dict(act=-1), dict(act=3)]:
             assert f(**kw) == BAD, (f, kw)
     assert fwd(N=0, g=None, u=None, x=None, h=None) == OK
-    for kw in [dict(h=None), dict(h=P + 1), dict(pre=P + 1)]:
+    for kw in [dict(h=None), dict(h=P + 1), dict(pre=P + 2)]:
         assert fwd(**kw) == BAD, kw
     for kw in [dict(dh=None), dict(pre=None), dict(ws=None), dict(ws=P + 8), dict(n=3 * 32 * 4), dict(dx=None, dg=None, du=None),
                dict(dg=None), dict(du=None), dict(dx=P + 1), dict(dg=P + 1), dict(dt=F16), dict(dt=F32, du=P + 2),
@@ -169,7 +169,7 @@ def test_host_tensors_and_wrong_arguments_are_refused():
     x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
     c, s = torch.zeros(2, 64, dtype=torch.float8_e4m3fn), torch.zeros(2, 1)
     dy = torch.zeros(2, 8, dtype=torch.bfloat16)
-    pre = torch.zeros(2, 16, dtype=torch.bfloat16)
+    pre = torch.zeros(2, 16)
     for call in [lambda: moe.moe_linear(w, x), lambda: moe.moe_linear_backward(dy, w, x), lambda: moe.moe_gated(w, w, x),
                  lambda: moe.moe_gated_backward(dy, pre, w, w, x), lambda: moe.moe_quantize_fp8(x),
                  lambda: moe.moe_linear_fp8(c, s[:1], c, s), lambda: moe.moe_linear(w, x[0]), lambda: moe.moe_linear(w[0], x),
