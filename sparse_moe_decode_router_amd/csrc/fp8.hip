@@ -13,6 +13,7 @@
 // about 1e-5 of a random product, the codes' own rounding is 2^-4); its sums of
 // these are fp32.  It has twice the rate of the 16-bit products.
 #include "products.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
@@ -201,8 +202,66 @@ template <class T> __device__ __forceinline__ i32x8_t fp8_frag(const uint8_t* t,
   return (i32x8_t){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// The K loop, for the first LIVE of the wave's tiles of x (a constant, as in
+// tiles.h).  A row tile's fragments are read while the products of the one
+// before run; each pair of products is folded into its sums meanwhile.
+template <class S, int LIVE>
+__device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uint8_t* lds, int blocks, const float* const* sx,
+                                         const float* const* sw, f32x16_t (&acc)[S::TQ][S::TP]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wq = wave / S::WP, wp = wave % S::WP;
+  typename S::QT qt;
+  typename S::PT pt;
+  qt.plan(q);
+  pt.plan(p);
+  constexpr int kDma = S::QT::kPer + S::PT::kPer;
+  const auto issue = [&](int s) {
+    uint8_t* st = lds + (s % S::NS) * S::kStage;
+    const int k0 = s < blocks ? s * 64 : q.K;
+    qt.dma(q, st, k0);
+    pt.dma(p, st + S::QT::kBytes, k0);
+  };
+#pragma unroll
+  for (int s = 0; s < S::NS - 1; ++s) issue(s);
+  for (int s = 0; s < blocks; ++s) {
+    float fx[LIVE + 1], fw[S::TP];
+#pragma unroll
+    for (int t = 0; t < LIVE; ++t) fx[t] = sx[t][s];
+#pragma unroll
+    for (int t = 0; t < S::TP; ++t) fw[t] = sw[t][s];
+    stage_wait<(S::NS - 2) * kDma>();
+    issue(s + S::NS - 1);
+    const uint8_t* st = lds + (s % S::NS) * S::kStage;
+    if constexpr (LIVE > 0) {
+      i32x8_t pf[S::TP][2], qf[2][2];
+      const auto read = [&](int u) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) qf[u & 1][h] = fp8_frag<typename S::QT>(st, 32 * (wq * S::TQ + u), h, lane);
+      };
+#pragma unroll
+      for (int t = 0; t < S::TP; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pf[t][h] = fp8_frag<typename S::PT>(st + S::QT::kBytes, 32 * (wp * S::TP + t), h, lane);
+      read(0);
+#pragma unroll
+      for (int u = 0; u < LIVE; ++u) {
+        if (u + 1 < LIVE) read(u + 1);
+#pragma unroll
+        for (int t = 0; t < S::TP; ++t) {
+          f32x16_t part{};
+          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][0], qf[u & 1][0], part, 0, 0, 0, 0, 0, 0);
+          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][1], qf[u & 1][1], part, 0, 0, 0, 0, 0, 0);
+          const float f = fx[u] * fw[t];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[u][t][i] = fmaf(f, part[i], acc[u][t][i]);
+        }
+      }
+    }
+  }
+}
+
 template <class S, int OUT>
-__global__ __launch_bounds__(S::NT) void linear_fp8_kernel(Fp8Args a) {
+__global__ __launch_bounds__(S::NT, 2) void linear_fp8_kernel(Fp8Args a) {
   extern __shared__ uint8_t tile_lds[];
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
   int unit, tile;
@@ -242,50 +301,17 @@ __global__ __launch_bounds__(S::NT) void linear_fp8_kernel(Fp8Args a) {
     const int o = p0 + 32 * (wp * S::TP + t);
     sw[t] = a.w_scales + (uint64_t)e * a.w_scales_stride + (uint64_t)((o < a.n_out ? o : a.n_out - 1) / kBlock) * a.blocks;
   }
-  typename S::QT qt;
-  typename S::PT pt;
-  qt.plan(q);
-  pt.plan(p);
-  constexpr int kDma = S::QT::kPer + S::PT::kPer;
-  const auto issue = [&](int s) {
-    uint8_t* st = tile_lds + (s % S::NS) * S::kStage;
-    const int k0 = s < a.blocks ? s * 64 : q.K;
-    qt.dma(q, st, k0);
-    pt.dma(p, st + S::QT::kBytes, k0);
-  };
   f32x16_t acc[S::TQ][S::TP] = {};
-#pragma unroll
-  for (int s = 0; s < S::NS - 1; ++s) issue(s);
-  for (int s = 0; s < a.blocks; ++s) {
-    float fx[S::TQ], fw[S::TP];
-#pragma unroll
-    for (int t = 0; t < S::TQ; ++t) fx[t] = sx[t][s];
-#pragma unroll
-    for (int t = 0; t < S::TP; ++t) fw[t] = sw[t][s];
-    stage_wait<(S::NS - 2) * kDma>();
-    issue(s + S::NS - 1);
-    const uint8_t* st = tile_lds + (s % S::NS) * S::kStage;
-    i32x8_t pf[S::TP][2];
-#pragma unroll
-    for (int t = 0; t < S::TP; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) pf[t][h] = fp8_frag<typename S::PT>(st + S::QT::kBytes, 32 * (wp * S::TP + t), h, lane);
-#pragma unroll
-    for (int u = 0; u < S::TQ; ++u) {
-      if (u < live) {
-        const i32x8_t f0 = fp8_frag<typename S::QT>(st, 32 * (wq * S::TQ + u), 0, lane);
-        const i32x8_t f1 = fp8_frag<typename S::QT>(st, 32 * (wq * S::TQ + u), 1, lane);
-#pragma unroll
-        for (int t = 0; t < S::TP; ++t) {
-          f32x16_t part{};
-          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][0], f0, part, 0, 0, 0, 0, 0, 0);
-          part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][1], f1, part, 0, 0, 0, 0, 0, 0);
-          const float f = fx[u] * fw[t];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[u][t][i] = fmaf(f, part[i], acc[u][t][i]);
-        }
-      }
-    }
+  if (live == S::TQ) {
+    fp8_loop<S, S::TQ>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (S::TQ > 3 && live == 3) {
+    fp8_loop<S, S::TQ < 3 ? S::TQ : 3>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (S::TQ > 2 && live == 2) {
+    fp8_loop<S, S::TQ < 2 ? S::TQ : 2>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (live == 1) {
+    fp8_loop<S, 1>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else {
+    fp8_loop<S, 0>(q, p, tile_lds, a.blocks, sx, sw, acc);
   }
   stage_wait<0>();
   uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
@@ -299,8 +325,117 @@ __global__ __launch_bounds__(S::NT) void linear_fp8_kernel(Fp8Args a) {
   }
 }
 
-template <int OUT> int product(Fp8Args& a, hipStream_t s) {
-  typedef Fp8Shape<2, 2, 2, 2, 2> S;
+// Few rows (stream.h): a block of 16 RT columns of W by 16 NT rows, its waves
+// take the blocks of 128 inputs in turn, U of them in flight.  Lane (m = lane &
+// 15, b = lane >> 4) holds inputs 32 b .. + 31 of column m and of row m.
+template <int RT, int NT, int NW, int U, int OUT>
+__global__ __launch_bounds__(64 * NW) void stream_fp8_kernel(Fp8Args a) {
+  constexpr int kTiles = RT * NT;
+  __shared__ float red[NW * kTiles * 256];
+  int unit, tile;
+  if (!grid_place(a.grid, &unit, &tile)) return;
+  const Rows rows = chunk_rows(a.offsets, a.E, a.N, unit, 16 * NT);
+  if (rows.n == 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int m = lane & 15, b = lane >> 4;
+  const int p0 = tile * 16 * RT;
+  const uint8_t* wp[RT];
+  const float* sw[RT];
+  const uint8_t* xp[NT];
+  const float* sx[NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int c = p0 + 16 * r + m < a.n_out ? p0 + 16 * r + m : a.n_out - 1;
+    const int o = p0 + 16 * r < a.n_out ? p0 + 16 * r : a.n_out - 1;          // 16 columns share their scales
+    wp[r] = a.w + (uint64_t)rows.e * a.w_stride + (uint64_t)c * a.n_in + 32 * b;
+    sw[r] = a.w_scales + (uint64_t)rows.e * a.w_scales_stride + (uint64_t)(o / kBlock) * a.blocks;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const long q = rows.start + (16 * t + m < rows.n ? 16 * t + m : rows.n - 1);
+    xp[t] = a.x + q * a.n_in + 32 * b;
+    sx[t] = a.x_scales + q * a.blocks;
+  }
+  f32x4_t acc[RT][NT] = {};
+  u32x4_t wv[U][RT][2], xv[U][NT][2];
+  float fw[U][RT], fx[U][NT];
+  // pieces past n_in: zeros (the first of the row is loaded instead)
+  const auto piece = [&](const uint8_t* p, int s, int h) {
+    const int k = kBlock * s + 16 * h;
+    const bool in = k + 32 * b < a.n_in;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(in ? p + k : p - 32 * b);
+    return in ? v : (u32x4_t){0, 0, 0, 0};
+  };
+  const auto load = [&](int u, int s) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      wv[u][r][0] = piece(wp[r], s, 0);
+      wv[u][r][1] = piece(wp[r], s, 1);
+      fw[u][r] = sw[r][s];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      xv[u][t][0] = piece(xp[t], s, 0);
+      xv[u][t][1] = piece(xp[t], s, 1);
+      fx[u][t] = sx[t][s];
+    }
+  };
+  const auto join = [](const u32x4_t (&v)[2]) {
+    return (i32x8_t){(int)v[0][0], (int)v[0][1], (int)v[0][2], (int)v[0][3], (int)v[1][0], (int)v[1][1], (int)v[1][2], (int)v[1][3]};
+  };
+  const auto compute = [&](int u) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const f32x4_t part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(wv[u][r]), join(xv[u][t]), (f32x4_t){}, 0, 0, 0, 0, 0, 0);
+        const float f = fw[u][r] * fx[u][t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(f, part[i], acc[r][t][i]);
+      }
+  };
+  const int count = wave < a.blocks ? (a.blocks - wave + NW - 1) / NW : 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < count) load(u, wave + u * NW);
+  int i = 0;
+  for (; i + U <= count; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+      compute(u);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + U + u < count) load(u, wave + (i + U + u) * NW);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (i + u < count) compute(u);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) share_put<kTiles>(red, wave, r * NT + t, acc[r][t]);
+  __syncthreads();
+  typedef typename El<OUT>::raw raw;
+  raw* out = static_cast<raw*>(a.y);
+  for (int v = threadIdx.x; v < 16 * RT * 16 * NT; v += 64 * NW) {
+    const int c = v % (16 * RT), q = v / (16 * RT), t = q / 16;
+    if (q < rows.n && p0 + c < a.n_out)
+      out[(rows.start + q) * a.n_out + p0 + c] = El<OUT>::down(share_sum<kTiles, NW>(red, (c / 16) * NT + t, q & 15, c & 15));
+  }
+}
+
+template <int RT, int NT, int NW, int U, int OUT> int stream(Fp8Args& a, hipStream_t s) {
+  const long units = a.offsets ? max_chunks(a.N, a.E, 16 * NT) : (a.N + 16 * NT - 1) / (16 * NT);
+  return grid_launch(units, (a.n_out + 16 * RT - 1) / (16 * RT), 1, [&](const Grid& g, unsigned blocks) {
+    a.grid = g;
+    stream_fp8_kernel<RT, NT, NW, U, OUT><<<blocks, 64 * NW, 0, s>>>(a);
+    MOE_HIP(hipGetLastError());
+    return (int)MOE_OK;
+  });
+}
+
+template <class S, int OUT> int tiled(Fp8Args& a, hipStream_t s) {
   const long units = a.offsets ? max_chunks(a.N, a.E, S::BQ) : (a.N + S::BQ - 1) / S::BQ;
   return grid_launch(units, (a.n_out + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
@@ -308,6 +443,15 @@ template <int OUT> int product(Fp8Args& a, hipStream_t s) {
     MOE_HIP(hipGetLastError());
     return (int)MOE_OK;
   });
+}
+
+template <int OUT> int product(Fp8Args& a, hipStream_t s) {
+  const int form = few_rows(a.offsets ? a.E : 0, a.N, a.n_out);
+  if (form == 1) return a.n_out >= 16384 ? stream<2, 1, 4, 4, OUT>(a, s) : stream<1, 1, 8, 4, OUT>(a, s);
+  if (form == 2) return stream<2, 2, 8, 2, OUT>(a, s);
+  if (form == 4) return stream<2, 4, 8, 2, OUT>(a, s);
+  if (wide_rows(a.offsets ? a.E : 0, a.N, a.n_out)) return tiled<Fp8Shape<2, 4, 4, 2, 2>, OUT>(a, s);
+  return tiled<Fp8Shape<2, 2, 2, 2, 2>, OUT>(a, s);
 }
 
 }  // namespace

@@ -11,17 +11,26 @@
 // matrix cores, which alone moves dx and dW by as much as their own rounding
 // does; g and u rounded as well moved them by 1.8 instead of 1.4 times that.
 #include "products.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
 
 template <int TYPE, bool AL> int forward(RowsArgs& a, hipStream_t s) {
-  typedef Shape<TYPE, true, true, 2, 2, 2, 2, 64, 2, true, AL> S;
-  return rows_grid<S, 1, true, TYPE>(a, s);
+  const int form = few_rows(a.offsets ? a.E : 0, a.N, 2l * a.P);
+  if (form == 1) return stream_launch<TYPE, true, 2, 1, 8, 4, TYPE, AL>(a, s);
+  if (form == 2) return stream_launch<TYPE, true, 2, 2, 8, 2, TYPE, AL>(a, s);
+  if (form == 4) return stream_launch<TYPE, true, 2, 4, 8, 1, TYPE, AL>(a, s);
+  if (few_tiles(a.offsets ? a.E : 0, a.N, 2l * a.P)) return rows_grid<Small<TYPE, true, true, true, AL>, 1, true, TYPE>(a, s);
+  if constexpr (AL)
+    if (wide_rows(a.offsets ? a.E : 0, a.N, 2l * a.P)) return rows_grid<Wide<TYPE, true, true, true>, 1, true, TYPE>(a, s);
+  return rows_grid<Large<TYPE, true, true, true, AL>, 1, true, TYPE>(a, s);
 }
 template <int TYPE, bool AL> int backward_dx(RowsArgs& a, hipStream_t s) {
-  typedef Shape<TYPE, true, false, 2, 2, 2, 2, 64, 2, false, AL> S;
-  return rows_grid<S, 2, false, TYPE>(a, s);
+  if (few_tiles(a.offsets ? a.E : 0, a.N, a.P)) return rows_grid<Small<TYPE, true, false, false, AL>, 2, false, TYPE>(a, s);
+  if constexpr (AL)
+    if (wide_rows(a.offsets ? a.E : 0, a.N, a.P)) return rows_grid<Wide<TYPE, true, false, false>, 2, false, TYPE>(a, s);
+  return rows_grid<Large<TYPE, true, false, false, AL>, 2, false, TYPE>(a, s);
 }
 
 // VN consecutive fp32 values

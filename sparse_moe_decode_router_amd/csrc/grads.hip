@@ -6,8 +6,7 @@
 namespace moe {
 namespace {
 
-template <int TYPE, int OUT, bool AL> int launch(MatsArgs& a, hipStream_t s) {
-  typedef Shape<TYPE, false, false, 2, 2, 2, 2, 64, 2, false, AL> S;
+template <class S, int OUT> int launch(MatsArgs& a, hipStream_t s) {
   a.q_tiles = (a.Q + S::BQ - 1) / S::BQ;
   return grid_launch((long)a.E * a.mats * a.q_tiles, (a.P + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
@@ -16,9 +15,16 @@ template <int TYPE, int OUT, bool AL> int launch(MatsArgs& a, hipStream_t s) {
     return (int)MOE_OK;
   });
 }
+template <int TYPE, int OUT, bool AL> int sized(MatsArgs& a, hipStream_t s) {
+  const long tiles = (long)a.E * a.mats * ((a.Q + 127) / 128) * ((a.P + 127) / 128);
+  if (tiles <= 256) return launch<Small<TYPE, false, false, false, AL>, OUT>(a, s);
+  if constexpr (AL)
+    if (wide_better((long)a.E * a.mats, a.Q, a.P, 3)) return launch<Wide<TYPE, false, false, false>, OUT>(a, s);
+  return launch<Mats<TYPE, AL>, OUT>(a, s);
+}
 template <int TYPE> int typed(MatsArgs& a, int out_type, bool al, hipStream_t s) {
-  if (out_type == MOE_TYPE_F32) return al ? launch<TYPE, MOE_TYPE_F32, true>(a, s) : launch<TYPE, MOE_TYPE_F32, false>(a, s);
-  return al ? launch<TYPE, TYPE, true>(a, s) : launch<TYPE, TYPE, false>(a, s);
+  if (out_type == MOE_TYPE_F32) return al ? sized<TYPE, MOE_TYPE_F32, true>(a, s) : sized<TYPE, MOE_TYPE_F32, false>(a, s);
+  return al ? sized<TYPE, TYPE, true>(a, s) : sized<TYPE, TYPE, false>(a, s);
 }
 
 }  // namespace

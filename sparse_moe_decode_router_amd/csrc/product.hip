@@ -5,16 +5,26 @@
 // pages applies k of E experts to each token).  Sums in fp32 on the matrix
 // cores; tiles.h has the tiles.
 #include "products.h"
+#include "stream.h"
 
 namespace moe {
 namespace {
 
 // y = x W^T: k and k; dx = dy W: k and p
 template <int TYPE, bool PK, int OUT, bool AL> int rows_launch(RowsArgs& a, hipStream_t s) {
-  typedef Shape<TYPE, true, PK, 2, 2, 2, 2, 64, 2, false, AL> S;
-  return rows_grid<S, 1, false, OUT>(a, s);
+  if (few_tiles(a.offsets ? a.E : 0, a.N, a.P)) return rows_grid<Small<TYPE, true, PK, false, AL>, 1, false, OUT>(a, s);
+  if constexpr (AL)
+    if (wide_rows(a.offsets ? a.E : 0, a.N, a.P)) return rows_grid<Wide<TYPE, true, PK, false>, 1, false, OUT>(a, s);
+  return rows_grid<Large<TYPE, true, PK, false, AL>, 1, false, OUT>(a, s);
+}
+template <int TYPE, int OUT, bool AL> int forward_few(RowsArgs& a, int form, hipStream_t s) {
+  if (form == 1) return stream_launch<TYPE, false, 1, 1, 8, 4, OUT, AL>(a, s);
+  if (form == 2) return stream_launch<TYPE, false, 2, 2, 8, 2, OUT, AL>(a, s);
+  return stream_launch<TYPE, false, 2, 4, 8, 1, OUT, AL>(a, s);
 }
 template <int TYPE, int OUT> int forward_typed(RowsArgs& a, bool al, hipStream_t s) {
+  if (const int form = few_rows(a.offsets ? a.E : 0, a.N, a.P))
+    return al ? forward_few<TYPE, OUT, true>(a, form, s) : forward_few<TYPE, OUT, false>(a, form, s);
   return al ? rows_launch<TYPE, true, OUT, true>(a, s) : rows_launch<TYPE, true, OUT, false>(a, s);
 }
 template <int TYPE> int dx_typed(RowsArgs& a, bool al, hipStream_t s) {

@@ -39,6 +39,35 @@ template <class S, int SEGS, bool GATED, int OUT> int rows_grid(RowsArgs& a, hip
   });
 }
 
+// The form of a product of N rows, in E buckets or (E 0) of one matrix, with P
+// columns: 0 tiles of 128 x 128, or 16 NT rows a block of stream.h (NT 1, 2, 4).
+inline int few_rows(int E, long N, long P) {
+  const long rows = E ? (N + E - 1) / E : N;                    // of a bucket
+  const long chunks = E ? (N < E ? N : E * ((rows + 127) / 128)) : (N + 127) / 128;
+  if (rows > 64 || chunks * ((P + 127) / 128) > 1024) return 0;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+
+// Whether tiles of 128 x 128 would be few for the 256 CUs.
+inline bool few_tiles(int E, long N, long P) {
+  const long chunks = E ? (N < E ? N : E * ((N / E + 127) / 128)) : (N + 127) / 128;
+  return chunks * ((P + 127) / 128) <= 256;
+}
+// Whether tiles of 256 x 256 (one a CU, 1.12 times the rate) take less than
+// those of 128 x 128 (`slots` a CU) for `units` matrices of q x p, in whole rounds of the 256 CUs.
+// Measured (16-bit, wide against large): 4096 x 4096 -> 4096 115 and 127 us, 4160
+// x 4160 -> 4160 194 and 172, 4096 x 8192 -> 2048 564 and 382.
+inline bool wide_better(long units, long q, long p, int slots) {
+  const long wide = units * ((q + 255) / 256) * ((p + 255) / 256);
+  const long large = units * ((q + 127) / 128) * ((p + 127) / 128);
+  return (wide + 255) / 256 * 4 < 1.12 * ((large + 256 * slots - 1) / (256 * slots) * slots);
+}
+// The same for rows: buckets of 512 rows and more, which fill the taller tile.
+inline bool wide_rows(int E, long N, long P) {
+  const long rows = E ? N / E : N;
+  return rows >= 512 && wide_better(E ? E : 1, rows, P, 2);
+}
+
 // Gradients of the matrices (grads.hip).
 int mats_launch(MatsArgs& a, int type, int out_type, bool al, hipStream_t s);
 

@@ -35,6 +35,28 @@ __device__ __forceinline__ f32x16_t mfma32(s16x8_t a, s16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
 }
 
+// Elements k .. k + 7 of a row of K, zeros past its end.  A piece over the end
+// is the row's last 8 elements, shifted: loading it element by element means as
+// many dependent waits (rows of 1001: 35 us for what takes 9).  Rows shorter
+// than that have no other way.
+__device__ __forceinline__ u32x4_t load_piece(const uint16_t* row, int k, int K) {
+  if (K < 8) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (k + j < K) w[j / 2] |= (uint32_t)row[k + j] << (16 * (j & 1));
+    return (u32x4_t){w[0], w[1], w[2], w[3]};
+  }
+  const int from = k < K - 8 ? k : K - 8;
+  const u32x4_t v = *reinterpret_cast<const Piece16*>(row + from);
+  const int past = 16 * (k - from);             // bits
+  if (past == 0) return v;
+  const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+  const uint64_t a = past < 64 ? lo >> past | hi << (64 - past) : past < 128 ? hi >> (past - 64) : 0;
+  const uint64_t b = past < 64 ? hi >> past : 0;
+  return (u32x4_t){(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+}
+
 // s_waitcnt vmcnt <= N, lgkmcnt == 0, then s_barrier, and no memory access
 // moved across it by the compiler.
 template <int N> __device__ __forceinline__ void stage_wait() {
@@ -51,6 +73,7 @@ struct Operand {
   const uint8_t* base2;         // PAIR: the second matrix's
   const uint8_t* next;          // base in the second segment of k
   long ld;                      // elements from row to row (KC), from k to k (else)
+  long col;                     // else: columns of the matrix before the first one
   int n;                        // rows (KC) or columns (else) that exist, of R
   int K;
 };
@@ -149,27 +172,52 @@ struct Tile {
     }
   }
 
-  // ---- any size: through registers
-  __device__ __forceinline__ void fetch(const Operand& o, int k0, u32x4_t (&v)[kPer]) const {
+  // ---- any size: through registers, vo as below.  Rows that do not exist are
+  // the last one's, never stored; k past K are zeros.
+  __device__ __forceinline__ void plan_any(const Operand& o) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       int row, piece;
       source((int)threadIdx.x + NT * i, &row, &piece);
-      const uint8_t* b = o.base;
-      if (PAIR && (row & 32)) b = o.base2;
-      const long m = matrix_row(row);
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(b) + (KC ? m * o.ld + k0 + 8 * piece : (long)(k0 + row) * o.ld + 8 * piece);
-      const int have = KC ? (m < o.n ? o.K - k0 - 8 * piece : 0) : (k0 + row < o.K ? o.n - 8 * piece : 0);
-      if (have >= 8) {
-        v[i] = *reinterpret_cast<const Piece16*>(p);
+      if constexpr (KC) {
+        const int r = matrix_row(row) < o.n ? matrix_row(row) : o.n - 1;
+        vo[i] = (uint32_t)(r * o.ld * 2 + piece * 16);
       } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (j < have) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-        v[i] = (u32x4_t){w[0], w[1], w[2], w[3]};
+        vo[i] = (uint32_t)(row * o.ld * 2 + piece * 16);
       }
     }
+  }
+  __device__ __forceinline__ void fetch(const Operand& o, int k0, u32x4_t (&v)[kPer]) const {
+    // whole pieces: one scalar base, one offset a piece
+    const bool whole = k0 + BK <= o.K && (KC || o.n == R);
+    const uint8_t* b1 = o.base + (KC ? 2l * k0 : 2l * k0 * o.ld);
+    const uint8_t* b2 = PAIR ? o.base2 + 2l * k0 : b1;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>((second(i) ? b2 : b1) + vo[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      int row, piece;
+      source((int)threadIdx.x + NT * i, &row, &piece);
+      const uint8_t* p = (second(i) ? b2 : b1) + (vo[i] - 16 * piece);
+      if constexpr (KC) {
+        v[i] = load_piece(reinterpret_cast<const uint16_t*>(p) - k0, k0 + 8 * piece, o.K);
+      } else {
+        const bool in = k0 + row < o.K;
+        const long back = in ? 0 : (long)(k0 + row - (o.K - 1)) * o.ld * 2;
+        const u32x4_t w = load_piece(reinterpret_cast<const uint16_t*>(p - back) - o.col, (int)o.col + 8 * piece,
+                                     (int)o.col + o.n);
+        v[i] = in ? w : (u32x4_t){0, 0, 0, 0};
+      }
+    }
+  }
+  // PAIR: whether a thread's piece i is of the second matrix (the same for its wave)
+  static __device__ __forceinline__ bool second(int i) {
+    if constexpr (!PAIR) return false;
+    if constexpr (NT / kPieces == 32) return i & 1;             // 32 rows a turn of the block
+    return __builtin_amdgcn_readfirstlane(((int)threadIdx.x + NT * i) / kPieces) & 32;
   }
   __device__ __forceinline__ void put(uint8_t* t, const u32x4_t (&v)[kPer]) const {
 #pragma unroll
@@ -179,11 +227,13 @@ struct Tile {
 
 // Block shape: WQ x WP waves of TQ x TP tiles of 32 x 32, k in steps of BK
 // through NS stages.  AL: rows are whole 16-byte pieces at 16-byte addresses.
-template <int TYPE_, bool QK_, bool PK_, int WQ_, int WP_, int TQ_, int TP_, int BK_, int NS_, bool PAIR_, bool AL_>
+template <int TYPE_, bool QK_, bool PK_, int WQ_, int WP_, int TQ_, int TP_, int BK_, int NS_, bool PAIR_, bool AL_, int WAVES_ = 1>
 struct Shape {
   static constexpr int TYPE = TYPE_, WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, BK = BK_, NS = AL_ ? NS_ : 2;
+  static constexpr int WAVES = WAVES_;           // a SIMD at least
   static constexpr bool QK = QK_, PK = PK_, PAIR = PAIR_, AL = AL_;
   static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
+  static constexpr int AHEAD = TQ * TP >= 4 ? 2 : 3;            // !AL: steps in registers
   typedef Tile<QK, BQ, BK, NT, false> QT;
   typedef Tile<PK, BP, BK, NT, PAIR> PT;
   static constexpr int kStage = QT::kBytes + PT::kBytes;
@@ -191,27 +241,48 @@ struct Shape {
 };
 
 // acc[q][p] += the product over k, in one segment or two of K each (of the
-// operands at base, then at next); live_q of the wave's TQ tiles of q count.
-template <class S, int SEGS>
-__device__ __forceinline__ void tile_product(Operand qo, Operand po, uint8_t* lds, int live_q,
-                                             f32x16_t (&acc)[S::TQ][S::TP]) {
+// operands at base, then at next), for the first LIVE of the wave's tiles of q.
+// LIVE is a constant of the loop: with a branch around each tile every
+// fragment's read is waited for before its products.
+template <class S, int SEGS, int LIVE>
+__device__ __forceinline__ void tile_loop(Operand qo, Operand po, uint8_t* lds, f32x16_t (&acc)[S::TQ][S::TP]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
   const int per = (qo.K + S::BK - 1) / S::BK, steps = SEGS * per;
   const auto compute = [&](const uint8_t* st) {
+    if constexpr (LIVE > 0) {
+      // a step's fragments are read while the products of the one before run
+      s16x8_t p[2][S::TP], q[2][LIVE];
+      const auto read = [&](int kk) {
 #pragma unroll
-    for (int kk = 0; kk < S::BK / 16; ++kk) {
-      s16x8_t p[S::TP];
+        for (int t = 0; t < S::TP; ++t) p[kk & 1][t] = S::PT::frag(st + S::QT::kBytes, 32 * (wp * S::TP + t), kk, lane);
 #pragma unroll
-      for (int t = 0; t < S::TP; ++t) p[t] = S::PT::frag(st + S::QT::kBytes, 32 * (wp * S::TP + t), kk, lane);
+        for (int t = 0; t < LIVE; ++t) q[kk & 1][t] = S::QT::frag(st, 32 * (wq * S::TQ + t), kk, lane);
+      };
+      read(0);
 #pragma unroll
-      for (int q = 0; q < S::TQ; ++q) {
-        if (q < live_q) {
-          const s16x8_t f = S::QT::frag(st, 32 * (wq * S::TQ + q), kk, lane);
+      for (int kk = 0; kk < S::BK / 16; ++kk) {
+        if (kk + 1 < S::BK / 16) read(kk + 1);
 #pragma unroll
-          for (int t = 0; t < S::TP; ++t) acc[q][t] = mfma32<S::TYPE>(p[t], f, acc[q][t]);
-        }
+        for (int u = 0; u < LIVE; ++u)
+#pragma unroll
+          for (int t = 0; t < S::TP; ++t) acc[u][t] = mfma32<S::TYPE>(p[kk & 1][t], q[kk & 1][u], acc[u][t]);
       }
+      constexpr int kFirst = (S::PK ? 1 : 2) * S::TP + (S::QK ? 1 : 2) * LIVE;  // LDS reads of a kk
+      __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+#pragma unroll
+      for (int kk = 0; kk < S::BK / 16; ++kk)
+#pragma unroll
+        for (int m = 0; m < LIVE * S::TP; ++m) {
+          if (kk + 1 < S::BK / 16) {            // reads spread over the products
+            constexpr int kEach = kFirst / (LIVE * S::TP), kMore = kFirst % (LIVE * S::TP);
+            if (m < kMore)
+              __builtin_amdgcn_sched_group_barrier(0x100, kEach + 1, 0);
+            else if (kEach > 0)
+              __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
     }
   };
   typename S::QT qt;
@@ -239,33 +310,54 @@ __device__ __forceinline__ void tile_product(Operand qo, Operand po, uint8_t* ld
     }
     stage_wait<0>();
   } else {
-    u32x4_t qv[S::QT::kPer], pv[S::PT::kPer];
-    const auto fetch = [&](int s) {
-      if (SEGS == 2 && s == per) {
-        qo.base = qo.next;
-        po.base = po.next;
+    // AHEAD steps in registers, then LDS
+    constexpr int D = S::AHEAD;
+    u32x4_t qv[D][S::QT::kPer], pv[D][S::PT::kPer];
+    qt.plan_any(qo);
+    pt.plan_any(po);
+    const auto fetch = [&](int s, int d) {
+      const bool second = SEGS == 2 && s >= per;
+      Operand q = qo, p = po;
+      if (second) {
+        q.base = qo.next;
+        p.base = po.next;
       }
-      const int k0 = (SEGS == 2 && s >= per ? s - per : s) * S::BK;
-      qt.fetch(qo, k0, qv);
-      pt.fetch(po, k0, pv);
+      const int k0 = (second ? s - per : s) * S::BK;
+      qt.fetch(q, k0, qv[d]);
+      pt.fetch(p, k0, pv[d]);
     };
-    const auto put = [&](int s) {
-      uint8_t* st = lds + (s & 1) * S::kStage;
-      qt.put(st, qv);
-      pt.put(st + S::QT::kBytes, pv);
-    };
-    if (steps > 0) {
-      fetch(0);
-      put(0);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < steps) fetch(d, d);
+    for (int s = 0; s < steps; s += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (s + d >= steps) break;
+        // the other buffer is read in the step before: one barrier a step
+        uint8_t* st = lds + ((s + d) & 1) * S::kStage;
+        qt.put(st, qv[d]);
+        pt.put(st + S::QT::kBytes, pv[d]);
+        if (s + d + D < steps) fetch(s + d + D, d);
+        stage_wait<63>();
+        compute(st);
+      }
     }
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-      if (s + 1 < steps) fetch(s + 1);
-      compute(lds + (s & 1) * S::kStage);
-      if (s + 1 < steps) put(s + 1);
-      __syncthreads();
-    }
+    stage_wait<63>();
   }
+}
+
+template <class S, int SEGS>
+__device__ __forceinline__ void tile_product(const Operand& q, const Operand& p, uint8_t* lds, int live,
+                                             f32x16_t (&acc)[S::TQ][S::TP]) {
+  // every wave meets the same barriers, whichever loop it is in
+  if (live == S::TQ) return tile_loop<S, SEGS, S::TQ>(q, p, lds, acc);
+  if constexpr (S::TQ > 3)
+    if (live == 3) return tile_loop<S, SEGS, 3>(q, p, lds, acc);
+  if constexpr (S::TQ > 2)
+    if (live == 2) return tile_loop<S, SEGS, 2>(q, p, lds, acc);
+  if constexpr (S::TQ > 1)
+    if (live == 1) return tile_loop<S, SEGS, 1>(q, p, lds, acc);
+  tile_loop<S, SEGS, 0>(q, p, lds, acc);
 }
 
 // 32 rows of q by 32 NP columns of p, one wave: from the sums' layout (lane:
@@ -349,6 +441,21 @@ template <class F> int grid_launch(long units, long tiles, int group, F launch) 
   return MOE_OK;
 }
 
+// Block shapes.  Large: 128 x 128, two blocks a CU, so that one's products fill
+// the other's waits.  Wide: 256 x 256 by 8 waves of 128 x 64, which read a third
+// less from LDS for a product and leave one block a CU.  Small: 64 x 64 (PAIR 64
+// x 128) with more steps in flight, where larger ones would leave CUs idle.
+// Mats (gradients of matrices, few steps of k a tile): 128 x 128 in half steps,
+// three blocks a CU (32768 tiles of 2 steps: 400 us, 470 as Large).
+template <int TYPE, bool QK, bool PK, bool PAIR, bool AL>
+using Large = Shape<TYPE, QK, PK, 2, 2, 2, 2, 64, 2, PAIR, AL, 2>;
+template <int TYPE, bool QK, bool PK, bool PAIR>
+using Wide = Shape<TYPE, QK, PK, 2, 4, 4, 2, 64, 2, PAIR, true, 2>;
+template <int TYPE, bool QK, bool PK, bool PAIR, bool AL>
+using Small = Shape<TYPE, QK, PK, 2, 2, 1, PAIR ? 2 : 1, 64, PAIR ? 4 : 5, PAIR, AL, 2>;
+template <int TYPE, bool AL>
+using Mats = Shape<TYPE, false, false, 2, 2, 2, 2, 32, 2, false, AL, AL ? 3 : 2>;
+
 // ------------------------------------------------- rows of x by a matrix
 struct RowsArgs {
   const uint8_t* q;             // rows [N][q_ld]
@@ -370,17 +477,35 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
 constexpr float kGeluB = 1.5957691216057308f;   // 2 sqrt(2 / pi): gelu_tanh(g) = g sigmoid(kGeluB (g + 0.044715 g^3))
+// Phi(g), the normal distribution, and e = exp(-g^2 / 2).  With z = |g| / sqrt 2
+// and t = 1 / (1 + 0.45 z), erfc(z) exp(z^2) / (2 t) is smooth on 0 < t <= 1: a
+// polynomial of degree 9 fitted to it (least largest relative error, 3.2e-8).
+// The tail keeps its relative precision, which 1 + erf would lose (and the
+// library's erfc took 10 us of 59 for 4200 rows of 1001 x 2 x 347).
+__device__ __forceinline__ float normal(float g, float* e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.45f * 0.70710678118654752f, fabsf(g), 1.f));
+  constexpr float c[10] = {1.269426604e-01f, 1.269415815e-01f, 1.141358193e-01f, 8.762608203e-02f, 5.997511320e-02f,
+                           -1.117864780e-02f, 7.119989770e-02f, -1.502906264e-01f, 9.534360267e-02f, -2.069547559e-02f};
+  float q = c[9];
+#pragma unroll
+  for (int i = 8; i >= 0; --i) q = fmaf(q, t, c[i]);
+  *e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+  const float tail = q * t * *e;
+  return g < 0.f ? tail : 1.f - tail;
+}
 __device__ __forceinline__ float act_value(int act, float g) {
+  float e;
   if (act == MOE_ACT_SILU) return g * sigmoid_fast(g);
-  if (act == MOE_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  if (act == MOE_ACT_GELU) return g * normal(g, &e);
   return g * sigmoid_fast(kGeluB * (g + 0.044715f * g * g * g));
 }
 // act(g) and its derivative
 __device__ __forceinline__ float act_slope(int act, float g, float* value) {
   if (act == MOE_ACT_GELU) {
-    const float p = 0.5f * erfcf(g * -0.70710678118654752f);
+    float e;
+    const float p = normal(g, &e);
     *value = g * p;
-    return fmaf(g, 0.39894228040143268f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f), p);
+    return fmaf(g, 0.39894228040143268f * e, p);
   }
   const bool silu = act == MOE_ACT_SILU;
   const float s = sigmoid_fast(silu ? g : kGeluB * (g + 0.044715f * g * g * g));
@@ -391,7 +516,7 @@ __device__ __forceinline__ float act_slope(int act, float g, float* value) {
 
 // GATED: out = act(x p^T) (x p2^T), and both products before it to pre.
 template <class S, int SEGS, bool GATED, int OUT>
-__global__ __launch_bounds__(S::NT) void rows_kernel(RowsArgs a) {
+__global__ __launch_bounds__(S::NT, S::WAVES) void rows_kernel(RowsArgs a) {
   extern __shared__ uint8_t tile_lds[];
   static_assert(!GATED || (S::PAIR && S::TP % 2 == 0), "tiles of both matrices in a wave");
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
@@ -422,6 +547,7 @@ __global__ __launch_bounds__(S::NT) void rows_kernel(RowsArgs a) {
   p.base = a.p + (uint64_t)e * a.p_stride + off;
   p.base2 = p.next = a.p2 + (uint64_t)e * a.p2_stride + off;
   p.ld = a.p_ld;
+  p.col = p0;
   p.n = cols;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
@@ -475,7 +601,7 @@ struct MatsArgs {
   Grid grid;
 };
 template <class S, int OUT>
-__global__ __launch_bounds__(S::NT) void mats_kernel(MatsArgs a) {
+__global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
   extern __shared__ uint8_t tile_lds[];
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
   int unit, tile;
@@ -494,9 +620,11 @@ __global__ __launch_bounds__(S::NT) void mats_kernel(MatsArgs a) {
   Operand q{}, p{};
   q.base = a.q + 2 * (start * a.q_ld + second * a.Q + q0);
   q.ld = a.q_ld;
+  q.col = second * a.Q + q0;
   q.n = a.Q - q0 < S::BQ ? a.Q - q0 : S::BQ;
   p.base = a.p + 2 * (start * a.p_ld + p0);
   p.ld = a.p_ld;
+  p.col = p0;
   p.n = a.P - p0 < S::BP ? a.P - p0 : S::BP;
   q.K = p.K = (int)(end - start);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));

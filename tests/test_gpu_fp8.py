@@ -158,7 +158,7 @@ def _check(y, wc, ws, xc, xs, off, what=""):
 
 DENSE = [(1, 16, 1), (1, 128, 128), (1, 2048, 512), (1, 2048, 5003), (2, 144, 33), (7, 4096, 130), (16, 256, 300),
          (17, 400, 129), (31, 128, 64), (33, 512, 257), (64, 1024, 1000), (65, 272, 200), (128, 128, 128), (129, 2064, 131),
-         (300, 640, 520), (1000, 96, 77)]
+         (300, 640, 520), (1000, 96, 77), (600, 144, 13210), (777, 272, 13330)]     # the last two: tiles of 256 x 256
 
 
 @pytest.mark.parametrize("N,n_in,n_out", DENSE)
@@ -172,7 +172,7 @@ def test_linear_dense(N, n_in, n_out, t):
 @pytest.mark.parametrize("N,n_in,n_out,E,behind", [
     (1, 64, 64, 1, 0), (10, 512, 2048, 64, 0), (10, 2048, 512, 512, 1), (7, 32, 40, 3, 2), (40, 144, 65, 9, 3),
     (96, 256, 136, 8, 11), (300, 80, 88, 5, 0), (700, 208, 264, 3, 77), (640, 48, 100, 64, 5), (1500, 64, 72, 1024, 100),
-    (2100, 144, 392, 12, 0), (129, 1008, 56, 2, 1)])
+    (2100, 144, 392, 12, 0), (129, 1008, 56, 2, 1), (2600, 48, 8200, 4, 9), (900, 528, 300, 300, 4)])
 def test_linear_experts(N, n_in, n_out, E, behind):
     wc, ws, xc, xs, off = _case(N, n_in, n_out, E, behind)
     o = torch.from_numpy(off).cuda()

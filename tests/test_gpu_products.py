@@ -128,6 +128,24 @@ def test_linear_experts(t, N, n_in, n_out, E, behind):
     _run_linear(c, n_in, n_out)
 
 
+# Sizes by the form that they take: tiles of 256 x 256 (long buckets and more
+# than two rounds of smaller ones), of 128 x 128 past 256 of them, with rows that
+# end in every tile of a wave, whole pieces or not.
+@pytest.mark.parametrize("N,n_in,n_out,E", [
+    (600, 72, 13208, 0), (520, 13208, 72, 0), (770, 136, 13320, 0), (70, 13208, 1000, 0),      # 256 x 256: y, dx, y, dw
+    (3000, 40, 8200, 4), (2700, 8200, 40, 4), (90, 2056, 1032, 12),                          # and for experts
+    (1100, 1000, 4104, 0), (1000, 201, 4103, 0), (5000, 264, 520, 40), (5000, 265, 521, 40), (300, 521, 263, 100),
+    (700, 2048, 512, 512), (700, 331, 515, 512)])
+def test_linear_forms(N, n_in, n_out, E):
+    _run_linear(Case(BF16 if N % 3 else F16, N, n_in, n_out, E, N // 50 if E else 0), n_in, n_out)
+
+
+@pytest.mark.parametrize("N,d,I,E", [(600, 72, 6608, 0), (530, 6608, 264, 0), (2600, 72, 4104, 4), (1030, 520, 2056, 0),
+                                     (1000, 201, 2055, 0), (5000, 136, 264, 40), (5000, 137, 263, 40), (600, 1024, 136, 300)])
+def test_gated_forms(N, d, I, E):
+    _run_gated(Case(BF16 if N % 3 else F16, N, d, I, E, N // 50 if E else 0, mats=2), d, I, oproducts.ACTS[d % 3])
+
+
 @pytest.mark.parametrize("N,n_in,n_out,E", [(70, 136, 200, 0), (70, 35, 201, 0), (90, 72, 264, 4), (3, 512, 65, 2)])
 def test_linear_fp32_outputs(N, n_in, n_out, E):
     _run_linear(Case(BF16, N, n_in, n_out, E), n_in, n_out, F32)
