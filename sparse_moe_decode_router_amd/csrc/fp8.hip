@@ -23,20 +23,29 @@ constexpr float kMax = 448.f, kSmallest = 0x1p-96f, kLarge = 0x1p64f;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // ------------------------------------------------------------ quantisation
-// What values of a block with the largest magnitude `top` are divided by: codes
-// are e4m3(448 (v m) / a).  m (a power of two) keeps 448 v below infinity.
+// A block with the largest magnitude `top`: codes are e4m3((v m) / a), m 448 or
+// (so that 448 v stays finite) 448 2^-32 with a smaller by as much.
 struct Block {
-  float a, m, scale;
+  float a, inv, m, scale;
 };
 __device__ __forceinline__ Block block_of(float top) {
   Block b;
   top = top < kSmallest ? kSmallest : top;
   b.scale = top / kMax;
-  b.m = top > kLarge ? 0x1p-32f : 1.f;
-  b.a = top * b.m;
+  const float down = top > kLarge ? 0x1p-32f : 1.f;
+  b.m = kMax * down;
+  b.a = top * down;
+  b.inv = __builtin_amdgcn_rcpf(b.a);
   return b;
 }
-__device__ __forceinline__ float quotient(const Block& b, float v) { return kMax * (v * b.m) / b.a; }
+// The quotient, rounded once: an estimate and its exact remainder (a quotient
+// that is a code or a border between two comes out as it is).  The division
+// itself, with its care for extremes that cannot occur, made the kernel bound
+// by its instructions (32768 x 2048: 58 us).
+__device__ __forceinline__ float quotient(const Block& b, float v) {
+  const float t = v * b.m, q = t * b.inv;
+  return __builtin_copysignf(fmaf(fmaf(-q, b.a, t), b.inv, q), v);
+}
 
 // A thread's 8 elements of a row: consecutive ones (VN 8), or every `step`th;
 // zeros past `have`.
@@ -206,8 +215,8 @@ template <class T> __device__ __forceinline__ i32x8_t fp8_frag(const uint8_t* t,
 // tiles.h).  A row tile's fragments are read while the products of the one
 // before run; each pair of products is folded into its sums meanwhile.
 template <class S, int LIVE>
-__device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uint8_t* lds, int blocks, const float* const* sx,
-                                         const float* const* sw, f32x16_t (&acc)[S::TQ][S::TP]) {
+__device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uint8_t* lds, int blocks, const float* const (&sx)[S::TQ],
+                                         const float* const (&sw)[S::TP], f32x16_t (&acc)[S::TQ][S::TP]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
   typename S::QT qt;
@@ -215,14 +224,16 @@ __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uin
   qt.plan(q);
   pt.plan(p);
   constexpr int kDma = S::QT::kPer + S::PT::kPer;
-  const auto issue = [&](int s) {
-    uint8_t* st = lds + (s % S::NS) * S::kStage;
+  const uint32_t base = lds_address(lds);
+  const auto issue = [&](int s, uint32_t st) {
     const int k0 = s < blocks ? s * 64 : q.K;
-    qt.dma(q, st, k0);
-    pt.dma(p, st + S::QT::kBytes, k0);
+    qt.dma(q, base + st, k0);
+    pt.dma(p, base + st + S::QT::kBytes, k0);
   };
 #pragma unroll
-  for (int s = 0; s < S::NS - 1; ++s) issue(s);
+  for (int s = 0; s < S::NS - 1; ++s) issue(s, s * S::kStage);
+  uint32_t now = 0, fill = (S::NS - 1) * S::kStage;             // stages, as bytes
+  const auto after = [](uint32_t st) { return st == (S::NS - 1) * S::kStage ? 0 : st + S::kStage; };
   for (int s = 0; s < blocks; ++s) {
     float fx[LIVE + 1], fw[S::TP];
 #pragma unroll
@@ -230,8 +241,10 @@ __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uin
 #pragma unroll
     for (int t = 0; t < S::TP; ++t) fw[t] = sw[t][s];
     stage_wait<(S::NS - 2) * kDma>();
-    issue(s + S::NS - 1);
-    const uint8_t* st = lds + (s % S::NS) * S::kStage;
+    issue(s + S::NS - 1, fill);
+    const uint8_t* st = lds + now;
+    now = after(now);
+    fill = after(fill);
     if constexpr (LIVE > 0) {
       i32x8_t pf[S::TP][2], qf[2][2];
       const auto read = [&](int u) {
@@ -304,12 +317,12 @@ __global__ __launch_bounds__(S::NT, 2) void linear_fp8_kernel(Fp8Args a) {
   f32x16_t acc[S::TQ][S::TP] = {};
   if (live == S::TQ) {
     fp8_loop<S, S::TQ>(q, p, tile_lds, a.blocks, sx, sw, acc);
-  } else if (S::TQ > 3 && live == 3) {
-    fp8_loop<S, S::TQ < 3 ? S::TQ : 3>(q, p, tile_lds, a.blocks, sx, sw, acc);
-  } else if (S::TQ > 2 && live == 2) {
-    fp8_loop<S, S::TQ < 2 ? S::TQ : 2>(q, p, tile_lds, a.blocks, sx, sw, acc);
-  } else if (live == 1) {
-    fp8_loop<S, 1>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (S::TQ == 4 && live == 3) {
+    fp8_loop<S, (S::TQ == 4 ? 3 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (S::TQ == 4 && live == 2) {
+    fp8_loop<S, (S::TQ == 4 ? 2 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
+  } else if (S::TQ > 1 && live == 1) {
+    fp8_loop<S, (S::TQ > 1 ? 1 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
   } else {
     fp8_loop<S, 0>(q, p, tile_lds, a.blocks, sx, sw, acc);
   }
@@ -446,10 +459,18 @@ template <class S, int OUT> int tiled(Fp8Args& a, hipStream_t s) {
 }
 
 template <int OUT> int product(Fp8Args& a, hipStream_t s) {
-  const int form = few_rows(a.offsets ? a.E : 0, a.N, a.n_out);
-  if (form == 1) return a.n_out >= 16384 ? stream<2, 1, 4, 4, OUT>(a, s) : stream<1, 1, 8, 4, OUT>(a, s);
-  if (form == 2) return stream<2, 2, 8, 2, OUT>(a, s);
-  if (form == 4) return stream<2, 4, 8, 2, OUT>(a, s);
+  // experts: tiles sooner than in 16 bits (us, streamed and in tiles, 2048 -> 512:
+  // 160 rows of 512 experts 42 and 46, 320 79 and 75, 640 109 and 78)
+  const int form = a.offsets && (a.N < a.E ? a.N : a.E) * ((a.n_out + 127) / 128) > 1024 ? 0 : few_rows(a.offsets ? a.E : 0, a.N);
+  // waves that share the inputs (us: 2048 x 512, 10 rows of 512 experts: 8 waves
+  // 6.0, 4 6.1, 2 6.8; 512 x 2048: 7.9, 7.1, 5.6; 1 row of 2048 x 100003 37.9,
+  // 36.5, 39.5; of 4096 x 4096 6.4, 6.8, 9.3)
+  if (form == 1 && a.blocks < 8) return stream<2, 1, 2, 4, OUT>(a, s);
+  if (form == 1) return a.n_out >= 16384 ? stream<1, 1, 4, 4, OUT>(a, s) : stream<1, 1, 8, 2, OUT>(a, s);
+  // more columns a block where there are many, as in product.hip
+  if (form == 2) return a.n_out <= 8192 ? stream<1, 2, 8, 4, OUT>(a, s) : stream<2, 2, 4, 4, OUT>(a, s);
+  if (form == 4) return a.n_out <= 8192 ? stream<1, 4, 8, 1, OUT>(a, s) : stream<2, 4, 4, 2, OUT>(a, s);
+  if (few_tiles(a.offsets ? a.E : 0, a.N, a.n_out)) return tiled<Fp8Shape<2, 2, 1, 1, 5>, OUT>(a, s);
   if (wide_rows(a.offsets ? a.E : 0, a.N, a.n_out)) return tiled<Fp8Shape<2, 4, 4, 2, 2>, OUT>(a, s);
   return tiled<Fp8Shape<2, 2, 2, 2, 2>, OUT>(a, s);
 }

@@ -17,10 +17,11 @@ namespace moe {
 namespace {
 
 template <int TYPE, bool AL> int forward(RowsArgs& a, hipStream_t s) {
-  const int form = few_rows(a.offsets ? a.E : 0, a.N, 2l * a.P);
-  if (form == 1) return stream_launch<TYPE, true, 2, 1, 8, 4, TYPE, AL>(a, s);
-  if (form == 2) return stream_launch<TYPE, true, 2, 2, 8, 2, TYPE, AL>(a, s);
-  if (form == 4) return stream_launch<TYPE, true, 2, 4, 8, 1, TYPE, AL>(a, s);
+  const int form = few_rows(a.offsets ? a.E : 0, a.N);
+  if (form == 1)                                // as product.hip
+    return a.K >= 1024 ? stream_launch<TYPE, true, 2, 1, 8, 4, TYPE, AL>(a, s) : stream_launch<TYPE, true, 2, 1, 4, 4, TYPE, AL>(a, s);
+  if (form == 2) return stream_launch<TYPE, true, 2, 2, 4, 2, TYPE, AL>(a, s);
+  if (form == 4) return stream_launch<TYPE, true, 2, 4, 4, 1, TYPE, AL>(a, s);
   if (few_tiles(a.offsets ? a.E : 0, a.N, 2l * a.P)) return rows_grid<Small<TYPE, true, true, true, AL>, 1, true, TYPE>(a, s);
   if constexpr (AL)
     if (wide_rows(a.offsets ? a.E : 0, a.N, 2l * a.P)) return rows_grid<Wide<TYPE, true, true, true>, 1, true, TYPE>(a, s);

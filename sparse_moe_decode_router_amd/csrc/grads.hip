@@ -17,7 +17,7 @@ template <class S, int OUT> int launch(MatsArgs& a, hipStream_t s) {
 }
 template <int TYPE, int OUT, bool AL> int sized(MatsArgs& a, hipStream_t s) {
   const long tiles = (long)a.E * a.mats * ((a.Q + 127) / 128) * ((a.P + 127) / 128);
-  if (tiles <= 256) return launch<Small<TYPE, false, false, false, AL>, OUT>(a, s);
+  if (tiles <= 128) return launch<Small<TYPE, false, false, false, AL>, OUT>(a, s);
   if constexpr (AL)
     if (wide_better((long)a.E * a.mats, a.Q, a.P, 3)) return launch<Wide<TYPE, false, false, false>, OUT>(a, s);
   return launch<Mats<TYPE, AL>, OUT>(a, s);

@@ -18,12 +18,22 @@ template <int TYPE, bool PK, int OUT, bool AL> int rows_launch(RowsArgs& a, hipS
   return rows_grid<Large<TYPE, true, PK, false, AL>, 1, false, OUT>(a, s);
 }
 template <int TYPE, int OUT, bool AL> int forward_few(RowsArgs& a, int form, hipStream_t s) {
-  if (form == 1) return stream_launch<TYPE, false, 1, 1, 8, 4, OUT, AL>(a, s);
-  if (form == 2) return stream_launch<TYPE, false, 2, 2, 8, 2, OUT, AL>(a, s);
-  return stream_launch<TYPE, false, 2, 4, 8, 1, OUT, AL>(a, s);
+  // rows of 1024 and more: 8 waves share k.  Shorter ones have not the steps
+  // for that: 4 waves, or where blocks are many 2 with 4 tiles each (us, 512 x
+  // 2048: 10 rows of 512 experts 9.2, 6.9 and 8.4, 40 rows of 256 26, 23 and 17;
+  // 2048 x 512: 10 rows of 512 8.4, 8.5 and 13)
+  if (form == 1 && a.K >= 1024) return stream_launch<TYPE, false, 1, 1, 8, 2, OUT, AL>(a, s);
+  if (form == 1 && (a.offsets ? max_chunks(a.N, a.E, 16) : 1) * ((a.P + 15) / 16) <= 2048)
+    return stream_launch<TYPE, false, 1, 1, 4, 4, OUT, AL>(a, s);
+  if (form == 1) return stream_launch<TYPE, false, 4, 1, 2, 2, OUT, AL>(a, s);
+  // more columns a block where there are many (32 rows: 4096 -> 4096 14.4 us with
+  // 16 columns, 18.9 with 32; 2048 -> 16384 25.6 and 21.4)
+  if (a.P <= 8192)
+    return form == 2 ? stream_launch<TYPE, false, 1, 2, 4, 4, OUT, AL>(a, s) : stream_launch<TYPE, false, 1, 4, 4, 2, OUT, AL>(a, s);
+  return form == 2 ? stream_launch<TYPE, false, 2, 2, 4, 4, OUT, AL>(a, s) : stream_launch<TYPE, false, 2, 4, 4, 2, OUT, AL>(a, s);
 }
 template <int TYPE, int OUT> int forward_typed(RowsArgs& a, bool al, hipStream_t s) {
-  if (const int form = few_rows(a.offsets ? a.E : 0, a.N, a.P))
+  if (const int form = few_rows(a.offsets ? a.E : 0, a.N))
     return al ? forward_few<TYPE, OUT, true>(a, form, s) : forward_few<TYPE, OUT, false>(a, form, s);
   return al ? rows_launch<TYPE, true, OUT, true>(a, s) : rows_launch<TYPE, true, OUT, false>(a, s);
 }

@@ -39,19 +39,22 @@ template <class S, int SEGS, bool GATED, int OUT> int rows_grid(RowsArgs& a, hip
   });
 }
 
-// The form of a product of N rows, in E buckets or (E 0) of one matrix, with P
-// columns: 0 tiles of 128 x 128, or 16 NT rows a block of stream.h (NT 1, 2, 4).
-inline int few_rows(int E, long N, long P) {
-  const long rows = E ? (N + E - 1) / E : N;                    // of a bucket
-  const long chunks = E ? (N < E ? N : E * ((rows + 127) / 128)) : (N + 127) / 128;
-  if (rows > 64 || chunks * ((P + 127) / 128) > 1024) return 0;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+// The form of a product of N rows, in E buckets or (E 0) of one matrix: 0 tiles
+// through LDS, or NT (1, 2, 4): 16 NT rows a block of stream.h.
+// One matrix: up to 64 rows (us, streamed and in tiles: 16 x 4096 -> 4096 11 and
+// 21, 64 21.4 and 22.2, 64 x 2048 -> 16384 28 and 42).  Experts: up to 8 rows a
+// bucket; more of them fill a second chunk, for which W is read again (2048 ->
+// 2 x 512 of 512, 5 rows 407 and 454, 10 rows 467 and 459; 2048 -> 2048 of 64, 8
+// rows 115 and 135, 16 rows 172 and 135).
+inline int few_rows(int E, long N) {
+  if (E) return N <= 8l * E ? 1 : 0;
+  return N > 64 ? 0 : N > 32 ? 4 : N > 16 ? 2 : 1;
 }
 
 // Whether tiles of 128 x 128 would be few for the 256 CUs.
 inline bool few_tiles(int E, long N, long P) {
   const long chunks = E ? (N < E ? N : E * ((N / E + 127) / 128)) : (N + 127) / 128;
-  return chunks * ((P + 127) / 128) <= 256;
+  return chunks * ((P + 127) / 128) <= 128;
 }
 // Whether tiles of 256 x 256 (one a CU, 1.12 times the rate) take less than
 // those of 128 x 128 (`slots` a CU) for `units` matrices of q x p, in whole rounds of the 256 CUs.

@@ -67,6 +67,12 @@ template <int N> __device__ __forceinline__ void stage_wait() {
   asm volatile("" ::: "memory");
 }
 
+// LDS address of block-uniform p, hidden from the compiler: its alias tracking
+// would wait for every DMA in flight before a read of LDS.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const lds_void*)p);
+}
+
 // An operand of one block: R rows of q (or p), k in [0, K).
 struct Operand {
   const uint8_t* base;          // KC: element (row 0, k 0); else (k 0, column 0)
@@ -94,9 +100,10 @@ struct Tile {
   // swizzle of a row's pieces
   static __device__ __forceinline__ int swz(int row) {
     if constexpr (KC)
-      return BK == 64 ? (row & 7) ^ ((row >> 3) & 1) : (row >> 2) & 3;
+      return BK == 128 ? row & 15 : BK == 64 ? (row & 7) ^ ((row >> 3) & 1) : (row >> 2) & 3;
     else
-      return 4 * (row & 3 & (R / 32 - 1));
+      // four rows' 64 bytes on four quarters of the 256 bytes of a pass
+      return R == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3);
   }
   static __device__ __forceinline__ int pos(int row, int piece) {
     return row * (16 * kPieces) + 16 * (piece ^ swz(row));
@@ -140,36 +147,40 @@ struct Tile {
         vo[i] = 8 * piece < o.n ? (uint32_t)(row * o.ld * 2 + piece * 16) : kNowhere;
     }
   }
-  // k0 .. k0 + BK of the operand (all zeros where k0 >= K)
-  __device__ __forceinline__ void dma(const Operand& o, uint8_t* t, int k0) const {
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  // k0 .. k0 + BK of the operand (all zeros where k0 >= K) to LDS address t.
+  // A wave's turns are 1 KB apart; it starts at kWave bytes of the tile.
+  static constexpr int kWave = 1024 * kPer;
+  __device__ __forceinline__ void dma(const Operand& o, uint32_t t, int k0) const {
+    const int left = o.K - k0;
+    const uint32_t to = t + wave_uniform() * kWave;
     if constexpr (KC) {
-      const uint32_t bytes = k0 < o.K ? kNowhere - 1 : 0;
-      const rsrc_t r1 = make_rsrc(o.base + 2l * k0, bytes);
-      const rsrc_t r2 = PAIR ? make_rsrc(o.base2 + 2l * k0, bytes) : r1;
-      const bool tail = k0 + BK > o.K;
+      // PAIR: a wave's 32 rows are of one matrix
+      static_assert(!PAIR || (kPieces == 8 && kPer == 4), "32 rows a wave");
+      // (as arithmetic: of a choice of pointers the compiler makes a load from scratch memory)
+      const uint8_t* b = o.base + (PAIR ? (o.base2 - o.base) & -(long)(wave_uniform() & 1) : 0);
+      const rsrc_t r = make_rsrc(b + 2l * k0, left > 0 ? kNowhere - 1 : 0);
+      if (left >= BK) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int at = wave * (64 * kPer) + 64 * i;
-        uint32_t v = vo[i];
-        if (tail) {
+        for (int i = 0; i < kPer; ++i) dma16(r, to + 1024 * i, vo[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
           int row, piece;
-          source(at + (threadIdx.x & 63), &row, &piece);
-          v = k0 + 8 * piece < o.K ? v : kNowhere;
+          source((int)(threadIdx.x >> 6) * (64 * kPer) + 64 * i + (threadIdx.x & 63), &row, &piece);
+          dma16(r, to + 1024 * i, 8 * piece < left ? vo[i] : kNowhere);
         }
-        const bool second = PAIR && ((at / kPieces) & 32);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(second ? r2 : r1, lds_opaque(t + 16 * at), 16, v, 0, 0, 0);
       }
     } else {
-      const int left = o.K - k0;                // rows of k
-      const rsrc_t r = make_rsrc(o.base + 2l * k0 * o.ld, left > 0 ? (uint32_t)((left < BK ? left - 1 : BK - 1) * o.ld * 2 + 2 * ((o.n + 7) & ~7)) : 0);
+      const int rows = left < BK ? left : BK;   // of k
+      const long bytes = 2 * ((rows - 1) * o.ld + ((o.n + 7) & ~7));
+      const rsrc_t r = make_rsrc(o.base + 2l * k0 * o.ld, rows > 0 ? (uint32_t)bytes : 0);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int at = wave * (64 * kPer) + 64 * i;
-        const uint32_t v = vo[i];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds_opaque(t + 16 * at), 16, v, 0, 0, 0);
-      }
+      for (int i = 0; i < kPer; ++i) dma16(r, to + 1024 * i, vo[i]);
     }
+  }
+  static __device__ __forceinline__ int wave_uniform() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+  static __device__ __forceinline__ void dma16(rsrc_t r, uint32_t to, uint32_t from) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(uintptr_t)to, 16, from, 0, 0, 0);
   }
 
   // ---- any size: through registers, vo as below.  Rows that do not exist are
@@ -194,14 +205,14 @@ struct Tile {
     const uint8_t* b2 = PAIR ? o.base2 + 2l * k0 : b1;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>((second(i) ? b2 : b1) + vo[i]);
+      for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>(b1 + (second(i) ? b2 - b1 : 0) + vo[i]);
       return;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       int row, piece;
       source((int)threadIdx.x + NT * i, &row, &piece);
-      const uint8_t* p = (second(i) ? b2 : b1) + (vo[i] - 16 * piece);
+      const uint8_t* p = b1 + (second(i) ? b2 - b1 : 0) + (vo[i] - 16 * piece);
       if constexpr (KC) {
         v[i] = load_piece(reinterpret_cast<const uint16_t*>(p) - k0, k0 + 8 * piece, o.K);
       } else {
@@ -233,7 +244,7 @@ struct Shape {
   static constexpr int WAVES = WAVES_;           // a SIMD at least
   static constexpr bool QK = QK_, PK = PK_, PAIR = PAIR_, AL = AL_;
   static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
-  static constexpr int AHEAD = TQ * TP >= 4 ? 2 : 3;            // !AL: steps in registers
+  static constexpr int AHEAD = TQ * TP >= 4 ? 1 : PAIR ? 4 : 6;            // !AL: steps in registers
   typedef Tile<QK, BQ, BK, NT, false> QT;
   typedef Tile<PK, BP, BK, NT, PAIR> PT;
   static constexpr int kStage = QT::kBytes + PT::kBytes;
@@ -291,22 +302,26 @@ __device__ __forceinline__ void tile_loop(Operand qo, Operand po, uint8_t* lds, 
     constexpr int kDma = S::QT::kPer + S::PT::kPer;
     qt.plan(qo);
     pt.plan(po);
-    const auto issue = [&](int s) {
+    const uint32_t base = lds_address(lds);
+    const auto issue = [&](int s, uint32_t st) {
       if (SEGS == 2 && s == per) {
         qo.base = qo.next;
         po.base = po.next;
       }
-      uint8_t* st = lds + (s % S::NS) * S::kStage;
       const int k0 = s < steps ? (SEGS == 2 && s >= per ? s - per : s) * S::BK : qo.K;
-      qt.dma(qo, st, k0);
-      pt.dma(po, st + S::QT::kBytes, k0);
+      qt.dma(qo, base + st, k0);
+      pt.dma(po, base + st + S::QT::kBytes, k0);
     };
 #pragma unroll
-    for (int s = 0; s < S::NS - 1; ++s) issue(s);
+    for (int s = 0; s < S::NS - 1; ++s) issue(s, s * S::kStage);
+    uint32_t now = 0, fill = (S::NS - 1) * S::kStage;           // stages, as bytes
+    const auto after = [](uint32_t st) { return st == (S::NS - 1) * S::kStage ? 0 : st + S::kStage; };
     for (int s = 0; s < steps; ++s) {
       stage_wait<(S::NS - 2) * kDma>();
-      issue(s + S::NS - 1);
-      compute(lds + (s % S::NS) * S::kStage);
+      issue(s + S::NS - 1, fill);
+      compute(lds + now);
+      now = after(now);
+      fill = after(fill);
     }
     stage_wait<0>();
   } else {
@@ -444,7 +459,10 @@ template <class F> int grid_launch(long units, long tiles, int group, F launch) 
 // Block shapes.  Large: 128 x 128, two blocks a CU, so that one's products fill
 // the other's waits.  Wide: 256 x 256 by 8 waves of 128 x 64, which read a third
 // less from LDS for a product and leave one block a CU.  Small: 64 x 64 (PAIR 64
-// x 128) with more steps in flight, where larger ones would leave CUs idle.
+// x 128), where larger ones would leave CUs idle; there a step's fixed cost
+// counts (barrier, loads issued, first fragments: about 0.35 us against 0.06 of
+// products), so steps are twice as long where the columns of P are turned (256 x
+// 4096 dx 51 -> 35 us; forward 22 -> 28, which keeps five stages).
 // Mats (gradients of matrices, few steps of k a tile): 128 x 128 in half steps,
 // three blocks a CU (32768 tiles of 2 steps: 400 us, 470 as Large).
 template <int TYPE, bool QK, bool PK, bool PAIR, bool AL>
@@ -452,7 +470,7 @@ using Large = Shape<TYPE, QK, PK, 2, 2, 2, 2, 64, 2, PAIR, AL, 2>;
 template <int TYPE, bool QK, bool PK, bool PAIR>
 using Wide = Shape<TYPE, QK, PK, 2, 4, 4, 2, 64, 2, PAIR, true, 2>;
 template <int TYPE, bool QK, bool PK, bool PAIR, bool AL>
-using Small = Shape<TYPE, QK, PK, 2, 2, 1, PAIR ? 2 : 1, 64, PAIR ? 4 : 5, PAIR, AL, 2>;
+using Small = Shape<TYPE, QK, PK, 2, 2, 1, PAIR ? 2 : 1, PK || !AL ? 64 : 128, PAIR ? 4 : PK ? 5 : 2, PAIR, AL, 2>;
 template <int TYPE, bool AL>
 using Mats = Shape<TYPE, false, false, 2, 2, 2, 2, 32, 2, false, AL, AL ? 3 : 2>;
 
