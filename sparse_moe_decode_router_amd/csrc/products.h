@@ -31,7 +31,7 @@ inline bool whole_pieces(std::initializer_list<int> sizes, std::initializer_list
 template <class S, int SEGS, bool GATED, int OUT> int rows_grid(RowsArgs& a, hipStream_t s) {
   const long units = a.offsets ? max_chunks(a.N, a.E, S::BQ) : (a.N + S::BQ - 1) / S::BQ;
   const int cols = GATED ? S::BP / 2 : S::BP;
-  return grid_launch(units, (a.P + cols - 1) / cols, 4, [&](const Grid& g, unsigned blocks) {
+  return grid_launch(units, (a.P + cols - 1) / cols, a.offsets ? 2 : 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
     rows_kernel<S, SEGS, GATED, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
     MOE_HIP(hipGetLastError());

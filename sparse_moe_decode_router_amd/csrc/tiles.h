@@ -35,6 +35,13 @@ __device__ __forceinline__ f32x16_t mfma32(s16x8_t a, s16x8_t b, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
 }
 
+// v without its lowest `past` bits (a multiple of 16), zeros above.
+__device__ __forceinline__ u32x4_t shift_down(u32x4_t v, int past) {
+  const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+  const uint64_t a = past == 0 ? lo : past < 64 ? lo >> past | hi << (64 - past) : past < 128 ? hi >> (past - 64) : 0;
+  const uint64_t b = past < 64 ? hi >> past : 0;
+  return (u32x4_t){(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+}
 // Elements k .. k + 7 of a row of K, zeros past its end.  A piece over the end
 // is the row's last 8 elements, shifted: loading it element by element means as
 // many dependent waits (rows of 1001: 35 us for what takes 9).  Rows shorter
@@ -49,12 +56,7 @@ __device__ __forceinline__ u32x4_t load_piece(const uint16_t* row, int k, int K)
   }
   const int from = k < K - 8 ? k : K - 8;
   const u32x4_t v = *reinterpret_cast<const Piece16*>(row + from);
-  const int past = 16 * (k - from);             // bits
-  if (past == 0) return v;
-  const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
-  const uint64_t a = past < 64 ? lo >> past | hi << (64 - past) : past < 128 ? hi >> (past - 64) : 0;
-  const uint64_t b = past < 64 ? hi >> past : 0;
-  return (u32x4_t){(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  return k == from ? v : shift_down(v, 16 * (k - from));
 }
 
 // s_waitcnt vmcnt <= N, lgkmcnt == 0, then s_barrier, and no memory access
@@ -184,7 +186,9 @@ struct Tile {
   }
 
   // ---- any size: through registers, vo as below.  Rows that do not exist are
-  // the last one's, never stored; k past K are zeros.
+  // the last one's, never stored; k past K are zeros.  Columns (not KC): a piece
+  // over the last one is the matrix's last 8 columns, shifted by `past`.
+  int past[KC ? 1 : kPer];
   __device__ __forceinline__ void plan_any(const Operand& o) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -194,33 +198,50 @@ struct Tile {
         const int r = matrix_row(row) < o.n ? matrix_row(row) : o.n - 1;
         vo[i] = (uint32_t)(r * o.ld * 2 + piece * 16);
       } else {
-        vo[i] = (uint32_t)(row * o.ld * 2 + piece * 16);
+        // (columns from the matrix's first one: o.base is o.col before that)
+        const int c = (int)o.col + 8 * piece, last = (int)o.col + o.n - 8, from = c < last || last < 0 ? c : last;
+        vo[i] = (uint32_t)(row * o.ld * 2 + from * 2);
+        past[i] = 16 * (c - from);
       }
     }
   }
   __device__ __forceinline__ void fetch(const Operand& o, int k0, u32x4_t (&v)[kPer]) const {
-    // whole pieces: one scalar base, one offset a piece
-    const bool whole = k0 + BK <= o.K && (KC || o.n == R);
-    const uint8_t* b1 = o.base + (KC ? 2l * k0 : 2l * k0 * o.ld);
-    const uint8_t* b2 = PAIR ? o.base2 + 2l * k0 : b1;
-    if (whole) {
+    if constexpr (KC) {
+      const uint8_t* b1 = o.base + 2l * k0;
+      const uint8_t* b2 = PAIR ? o.base2 + 2l * k0 : b1;
+      if (k0 + BK <= o.K) {                     // whole pieces: one scalar base, one offset a piece
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>(b1 + (second(i) ? b2 - b1 : 0) + vo[i]);
-      return;
-    }
+        for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>(b1 + (second(i) ? b2 - b1 : 0) + vo[i]);
+        return;
+      }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      int row, piece;
-      source((int)threadIdx.x + NT * i, &row, &piece);
-      const uint8_t* p = b1 + (second(i) ? b2 - b1 : 0) + (vo[i] - 16 * piece);
-      if constexpr (KC) {
+      for (int i = 0; i < kPer; ++i) {
+        int row, piece;
+        source((int)threadIdx.x + NT * i, &row, &piece);
+        const uint8_t* p = b1 + (second(i) ? b2 - b1 : 0) + (vo[i] - 16 * piece);
         v[i] = load_piece(reinterpret_cast<const uint16_t*>(p) - k0, k0 + 8 * piece, o.K);
+      }
+    } else {
+      const uint8_t* b = o.base - 2 * o.col + 2l * k0 * o.ld;
+      const bool wide = o.col + o.n >= 8;       // a matrix with 8 columns
+      if (wide && k0 + BK <= o.K) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = *reinterpret_cast<const Piece16*>(b + vo[i]);
       } else {
-        const bool in = k0 + row < o.K;
-        const long back = in ? 0 : (long)(k0 + row - (o.K - 1)) * o.ld * 2;
-        const u32x4_t w = load_piece(reinterpret_cast<const uint16_t*>(p - back) - o.col, (int)o.col + 8 * piece,
-                                     (int)o.col + o.n);
-        v[i] = in ? w : (u32x4_t){0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          int row, piece;
+          source((int)threadIdx.x + NT * i, &row, &piece);
+          const bool in = k0 + row < o.K;
+          const uint8_t* p = b + (in ? (long)vo[i] : (long)vo[i] - (long)(k0 + row - (o.K - 1)) * o.ld * 2);
+          const u32x4_t w = wide ? (u32x4_t)*reinterpret_cast<const Piece16*>(p)
+                                 : load_piece(reinterpret_cast<const uint16_t*>(p) - 8 * piece, 8 * piece, o.n);
+          v[i] = in ? w : (u32x4_t){0, 0, 0, 0};
+        }
+      }
+      if (wide && o.n < R) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = shift_down(v[i], past[i]);
       }
     }
   }
@@ -251,51 +272,54 @@ struct Shape {
   static constexpr int kLds = NS * kStage;
 };
 
+// acc[q][p] += the products of one step of k, for the first LIVE of the wave's
+// tiles of q (LIVE is a constant: with a branch around each tile every
+// fragment's read is waited for before its products).  Fragments are read while
+// the products of the 16 k before run.
+template <class S, int LIVE>
+__device__ __forceinline__ void tile_step(const uint8_t* st, int lane, int wq, int wp, f32x16_t (&acc)[S::TQ][S::TP]) {
+  if constexpr (LIVE > 0) {
+    s16x8_t p[2][S::TP], q[2][LIVE];
+    const auto read = [&](int kk) {
+#pragma unroll
+      for (int t = 0; t < S::TP; ++t) p[kk & 1][t] = S::PT::frag(st + S::QT::kBytes, 32 * (wp * S::TP + t), kk, lane);
+#pragma unroll
+      for (int t = 0; t < LIVE; ++t) q[kk & 1][t] = S::QT::frag(st, 32 * (wq * S::TQ + t), kk, lane);
+    };
+    read(0);
+#pragma unroll
+    for (int kk = 0; kk < S::BK / 16; ++kk) {
+      if (kk + 1 < S::BK / 16) read(kk + 1);
+#pragma unroll
+      for (int u = 0; u < LIVE; ++u)
+#pragma unroll
+        for (int t = 0; t < S::TP; ++t) acc[u][t] = mfma32<S::TYPE>(p[kk & 1][t], q[kk & 1][u], acc[u][t]);
+    }
+    constexpr int kFirst = (S::PK ? 1 : 2) * S::TP + (S::QK ? 1 : 2) * LIVE;    // LDS reads of a kk
+    __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
+#pragma unroll
+    for (int kk = 0; kk < S::BK / 16; ++kk)
+#pragma unroll
+      for (int m = 0; m < LIVE * S::TP; ++m) {
+        if (kk + 1 < S::BK / 16) {              // reads spread over the products
+          constexpr int kEach = kFirst / (LIVE * S::TP), kMore = kFirst % (LIVE * S::TP);
+          if (m < kMore)
+            __builtin_amdgcn_sched_group_barrier(0x100, kEach + 1, 0);
+          else if (kEach > 0)
+            __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+  }
+}
+
 // acc[q][p] += the product over k, in one segment or two of K each (of the
-// operands at base, then at next), for the first LIVE of the wave's tiles of q.
-// LIVE is a constant of the loop: with a branch around each tile every
-// fragment's read is waited for before its products.
+// operands at base, then at next).
 template <class S, int SEGS, int LIVE>
 __device__ __forceinline__ void tile_loop(Operand qo, Operand po, uint8_t* lds, f32x16_t (&acc)[S::TQ][S::TP]) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
   const int per = (qo.K + S::BK - 1) / S::BK, steps = SEGS * per;
-  const auto compute = [&](const uint8_t* st) {
-    if constexpr (LIVE > 0) {
-      // a step's fragments are read while the products of the one before run
-      s16x8_t p[2][S::TP], q[2][LIVE];
-      const auto read = [&](int kk) {
-#pragma unroll
-        for (int t = 0; t < S::TP; ++t) p[kk & 1][t] = S::PT::frag(st + S::QT::kBytes, 32 * (wp * S::TP + t), kk, lane);
-#pragma unroll
-        for (int t = 0; t < LIVE; ++t) q[kk & 1][t] = S::QT::frag(st, 32 * (wq * S::TQ + t), kk, lane);
-      };
-      read(0);
-#pragma unroll
-      for (int kk = 0; kk < S::BK / 16; ++kk) {
-        if (kk + 1 < S::BK / 16) read(kk + 1);
-#pragma unroll
-        for (int u = 0; u < LIVE; ++u)
-#pragma unroll
-          for (int t = 0; t < S::TP; ++t) acc[u][t] = mfma32<S::TYPE>(p[kk & 1][t], q[kk & 1][u], acc[u][t]);
-      }
-      constexpr int kFirst = (S::PK ? 1 : 2) * S::TP + (S::QK ? 1 : 2) * LIVE;  // LDS reads of a kk
-      __builtin_amdgcn_sched_group_barrier(0x100, kFirst, 0);
-#pragma unroll
-      for (int kk = 0; kk < S::BK / 16; ++kk)
-#pragma unroll
-        for (int m = 0; m < LIVE * S::TP; ++m) {
-          if (kk + 1 < S::BK / 16) {            // reads spread over the products
-            constexpr int kEach = kFirst / (LIVE * S::TP), kMore = kFirst % (LIVE * S::TP);
-            if (m < kMore)
-              __builtin_amdgcn_sched_group_barrier(0x100, kEach + 1, 0);
-            else if (kEach > 0)
-              __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-          }
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-    }
-  };
   typename S::QT qt;
   typename S::PT pt;
   if constexpr (S::AL) {
@@ -319,7 +343,7 @@ __device__ __forceinline__ void tile_loop(Operand qo, Operand po, uint8_t* lds, 
     for (int s = 0; s < steps; ++s) {
       stage_wait<(S::NS - 2) * kDma>();
       issue(s + S::NS - 1, fill);
-      compute(lds + now);
+      tile_step<S, LIVE>(lds + now, lane, wq, wp, acc);
       now = after(now);
       fill = after(fill);
     }
@@ -354,7 +378,7 @@ __device__ __forceinline__ void tile_loop(Operand qo, Operand po, uint8_t* lds, 
         pt.put(st + S::QT::kBytes, pv[d]);
         if (s + d + D < steps) fetch(s + d + D, d);
         stage_wait<63>();
-        compute(st);
+        tile_step<S, LIVE>(st, lane, wq, wp, acc);
       }
     }
     stage_wait<63>();
@@ -379,6 +403,8 @@ __device__ __forceinline__ void tile_product(const Operand& q, const Operand& p,
 // row l % 32, columns 8 (i / 4) + 4 (l / 32) + i % 4 of each 32) through the
 // wave's own LDS to rows in memory, each rounded once to OUT.  out: (row 0,
 // column 0); rows and cols that exist; rows whole 16-byte pieces (AL) or not.
+// Stores past the caches, which keep what the other blocks read (a training
+// step's calls on 4096 x 8 rows of 256 experts 1840 -> 1779 us in all).
 template <int OUT, int NP, bool AL>
 __device__ __forceinline__ void store_rows(uint8_t* lds, const f32x16_t* v, void* out, long ld, int rows, int cols) {
   typedef typename El<OUT>::raw raw;
@@ -405,7 +431,7 @@ __device__ __forceinline__ void store_rows(uint8_t* lds, const f32x16_t* v, void
       const uint8_t* from = lds + row * kPitch + c * sizeof(raw);
       raw* to = reinterpret_cast<raw*>(out) + row * ld + c;
       if (AL || c + kN <= cols) {
-        *reinterpret_cast<Piece16*>(to) = *reinterpret_cast<const u32x4_t*>(from);
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4_t*>(from), reinterpret_cast<Piece16*>(to));
       } else {
         for (int i = 0; c + i < cols; ++i) to[i] = reinterpret_cast<const raw*>(from)[i];
       }
@@ -618,12 +644,13 @@ struct MatsArgs {
   uint64_t out_stride, out2_stride;             // bytes from expert to expert
   Grid grid;
 };
-template <class S, int OUT>
-__global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
-  extern __shared__ uint8_t tile_lds[];
-  constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
-  int unit, tile;
-  if (!grid_place(a.grid, &unit, &tile)) return;
+// A block's expert and tile of q, with its columns of p from p0.
+struct MatsTile {
+  Operand q, p;
+  int q0;
+  uint8_t* out;                 // the matrix
+};
+template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs& a, int unit, int p0) {
   const int per = a.mats * a.q_tiles, e = unit / per, qt = unit - e * per;
   const int second = qt >= a.q_tiles ? 1 : 0;
   long start = 0, end = a.N;
@@ -634,33 +661,43 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
     end = end > a.N ? a.N : end;
     if (end < start) start = end = 0;
   }
-  const int q0 = (qt - second * a.q_tiles) * S::BQ, p0 = tile * S::BP;
-  Operand q{}, p{};
-  q.base = a.q + 2 * (start * a.q_ld + second * a.Q + q0);
-  q.ld = a.q_ld;
-  q.col = second * a.Q + q0;
-  q.n = a.Q - q0 < S::BQ ? a.Q - q0 : S::BQ;
-  p.base = a.p + 2 * (start * a.p_ld + p0);
-  p.ld = a.p_ld;
-  p.col = p0;
-  p.n = a.P - p0 < S::BP ? a.P - p0 : S::BP;
-  q.K = p.K = (int)(end - start);
+  MatsTile m{};
+  m.q0 = (qt - second * a.q_tiles) * S::BQ;
+  m.q.base = a.q + 2 * (start * a.q_ld + second * a.Q + m.q0);
+  m.q.ld = a.q_ld;
+  m.q.col = second * a.Q + m.q0;
+  m.q.n = a.Q - m.q0 < S::BQ ? a.Q - m.q0 : S::BQ;
+  m.p.base = a.p + 2 * (start * a.p_ld + p0);
+  m.p.ld = a.p_ld;
+  m.p.col = p0;
+  m.p.n = a.P - p0 < S::BP ? a.P - p0 : S::BP;
+  m.q.K = m.p.K = (int)(end - start);
+  m.out = second ? static_cast<uint8_t*>(a.out2) + (uint64_t)e * a.out2_stride
+                 : static_cast<uint8_t*>(a.out) + (uint64_t)e * a.out_stride;
+  return m;
+}
+template <class S, int OUT>
+__global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
+  extern __shared__ uint8_t tile_lds[];
+  constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
+  int unit, tile;
+  if (!grid_place(a.grid, &unit, &tile)) return;
+  const int p0 = tile * S::BP;
+  const MatsTile m = mats_tile<S>(a, unit, p0);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
-  const int left = q.n - 32 * wq * S::TQ;
+  const int left = m.q.n - 32 * wq * S::TQ;
   const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
   f32x16_t acc[S::TQ][S::TP] = {};
-  tile_product<S, 1>(q, p, tile_lds, live, acc);
+  tile_product<S, 1>(m.q, m.p, tile_lds, live, acc);
   uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
-  uint8_t* out = second ? static_cast<uint8_t*>(a.out2) + (uint64_t)e * a.out2_stride
-                        : static_cast<uint8_t*>(a.out) + (uint64_t)e * a.out_stride;
 #pragma unroll
   for (int t = 0; t < S::TQ; ++t) {
     if (t >= live) continue;
-    const long r0 = q0 + 32 * (wq * S::TQ + t);
+    const long r0 = m.q0 + 32 * (wq * S::TQ + t);
     const int c0 = p0 + 32 * S::TP * wp;
-    store_rows<OUT, S::TP, S::AL>(mine, acc[t], out + kSize * (r0 * a.P + c0), a.P, left - 32 * t < 32 ? left - 32 * t : 32,
-                                  a.P - c0);
+    store_rows<OUT, S::TP, S::AL>(mine, acc[t], m.out + kSize * (r0 * a.P + c0), a.P,
+                                  left - 32 * t < 32 ? left - 32 * t : 32, a.P - c0);
   }
 }
 
