@@ -196,6 +196,10 @@ struct Fp8Args {
 
 // WQ x WP waves of TQ x TP tiles of 32 x 32, 128 inputs a step: a row's 128
 // bytes lie in LDS as 64 elements of 16 bits do in tiles.h.
+// Measured: 4096 rows, 4096 -> 16384 310 us (1770 TFLOP/s) with 256 x 256 a
+// block: by the sums' 16 scaled additions a tile and step beside the products,
+// and each step's barrier; 32768 rows of 256 experts, 2048 -> 512 99 us with 128 x
+// 128: by HBM (370 MB) and half-filled chunks.
 template <int WQ_, int WP_, int TQ_, int TP_, int NS_> struct Fp8Shape {
   static constexpr int WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, NS = NS_;
   static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;

@@ -97,7 +97,6 @@ struct Tile {
   static constexpr int kPieces = KC ? BK / 8 : R / 8;           // of a row
   static constexpr int kPer = kBytes / 16 / NT;                 // pieces a thread
   static_assert(kPer * NT * 16 == kBytes, "whole pieces a thread");
-  static constexpr int kRowsDma = 64 / kPieces > 0 ? 64 / kPieces : 1;
 
   // swizzle of a row's pieces
   static __device__ __forceinline__ int swz(int row) {
@@ -558,7 +557,15 @@ __device__ __forceinline__ float act_slope(int act, float g, float* value) {
   return s * fmaf(g * (1.f - s), silu ? 1.f : kGeluB * fmaf(0.134145f * g, g, 1.f), 1.f);
 }
 
-// GATED: out = act(x p^T) (x p2^T), and both products before it to pre.
+// A block: a chunk of rows by a tile of columns.  GATED: out = act(x p^T)
+// (x p2^T), and both products before it to pre.
+// Measured: 4096 rows, 2048 -> 2 x 8192 with pre 293 us (940 TFLOP/s, a library
+// product of 8192 reaches 1455), its dx 383 (717: 512 tiles of 128 x 128 in one
+// round, 128 of 256 x 256 would fill half the CUs); 8192 x 8192 -> 8192 888 us
+// (1239).  Bound by the matrix cores waiting for each step's barrier and first
+// fragments.  32768 rows of 256 experts, 2048 -> 2 x 512 with pre 296 us, dx 316
+// (4.7 and 4.0 TB/s of what they have to move): by HBM, and by buckets that fill
+// three quarters of their chunks.
 template <class S, int SEGS, bool GATED, int OUT>
 __global__ __launch_bounds__(S::NT, S::WAVES) void rows_kernel(RowsArgs a) {
   extern __shared__ uint8_t tile_lds[];
@@ -676,6 +683,12 @@ template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs&
                  : static_cast<uint8_t*>(a.out) + (uint64_t)e * a.out_stride;
   return m;
 }
+// A block: a tile of one expert's matrix, k over the expert's rows.
+// Measured: 32768 rows of 256 experts, 2 x 512 x 2048 405 us.  Writing the 1.07
+// GB alone takes 172 (no rows), the products of 128 rows alone about 130 at the
+// dense rate (4096 rows, 2 x 8192 x 2048: 279 us, 990 TFLOP/s); the two overlap
+// little, since a tile's loads, few steps and stores follow one another, at four
+// blocks a CU as at one.
 template <class S, int OUT>
 __global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
   extern __shared__ uint8_t tile_lds[];
