@@ -146,6 +146,19 @@ def test_gated_forms(N, d, I, E):
     _run_gated(Case(BF16 if N % 3 else F16, N, d, I, E, N // 50 if E else 0, mats=2), d, I, oproducts.ACTS[d % 3])
 
 
+@pytest.mark.parametrize("E,first,N", [(64, 63, 500), (64, 0, 500), (300, 150, 2000), (4, 2, 700)])
+@pytest.mark.parametrize("i,o", [(136, 200), (131, 203)])
+def test_all_rows_of_one_expert(E, first, N, i, o):
+    """Few rows a bucket on average, all of them in one."""
+    c = Case(BF16, N, i, o, E, 0, mats=2)
+    c.off = np.where(np.arange(E + 1) > first, N, 0).astype(np.int32)
+    c.offsets = torch.from_numpy(c.off).cuda()
+    c.x, c.dy = (torch.randn(N, w, device="cuda").to(BF16) for w in (i, o))
+    _run_gated(c, i, o, "silu")
+    c.w = c.w[:1]
+    _run_linear(c, i, o)
+
+
 @pytest.mark.parametrize("N,n_in,n_out,E", [(70, 136, 200, 0), (70, 35, 201, 0), (90, 72, 264, 4), (3, 512, 65, 2)])
 def test_linear_fp32_outputs(N, n_in, n_out, E):
     _run_linear(Case(BF16, N, n_in, n_out, E), n_in, n_out, F32)
