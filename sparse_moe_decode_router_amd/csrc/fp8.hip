@@ -205,7 +205,7 @@ template <int WQ_, int WP_, int TQ_, int TP_, int NS_> struct Fp8Shape {
   static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
   typedef Tile<true, BQ, 64, NT, false> QT;
   typedef Tile<true, BP, 64, NT, false> PT;
-  static constexpr int kStage = QT::kBytes + PT::kBytes, kLds = NS * kStage;
+  static constexpr int kStage = QT::kBytes + PT::kBytes, kStages = NS * kStage;
 };
 
 template <class T> __device__ __forceinline__ i32x8_t fp8_frag(const uint8_t* t, int r0, int half, int lane) {
@@ -280,6 +280,7 @@ __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uin
 template <class S, int OUT>
 __global__ __launch_bounds__(S::NT, 2) void linear_fp8_kernel(Fp8Args a) {
   extern __shared__ uint8_t tile_lds[];
+  static_assert(S::NT / 64 * kTurn<OUT, S::TP> <= kBlockLds<S, OUT> && kBlockLds<S, OUT> <= kMaxLds, "turns in LDS");
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
   int unit, tile;
   if (!grid_place(a.grid, &unit, &tile)) return;
@@ -331,7 +332,7 @@ __global__ __launch_bounds__(S::NT, 2) void linear_fp8_kernel(Fp8Args a) {
     fp8_loop<S, 0>(q, p, tile_lds, a.blocks, sx, sw, acc);
   }
   stage_wait<0>();
-  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+  uint8_t* mine = tile_lds + wave * kTurn<OUT, S::TP>;
 #pragma unroll
   for (int t = 0; t < S::TQ; ++t) {
     if (t >= live) continue;
@@ -456,7 +457,7 @@ template <class S, int OUT> int tiled(Fp8Args& a, hipStream_t s) {
   const long units = a.offsets ? max_chunks(a.N, a.E, S::BQ) : (a.N + S::BQ - 1) / S::BQ;
   return grid_launch(units, (a.n_out + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
-    linear_fp8_kernel<S, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
+    linear_fp8_kernel<S, OUT><<<blocks, S::NT, kBlockLds<S, OUT>, s>>>(a);
     MOE_HIP(hipGetLastError());
     return (int)MOE_OK;
   });

@@ -10,7 +10,7 @@ template <class S, int OUT> int launch(MatsArgs& a, hipStream_t s) {
   a.q_tiles = (a.Q + S::BQ - 1) / S::BQ;
   return grid_launch((long)a.E * a.mats * a.q_tiles, (a.P + S::BP - 1) / S::BP, 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
-    mats_kernel<S, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
+    mats_kernel<S, OUT><<<blocks, S::NT, kBlockLds<S, OUT>, s>>>(a);
     MOE_HIP(hipGetLastError());
     return (int)MOE_OK;
   });

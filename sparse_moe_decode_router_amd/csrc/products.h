@@ -34,7 +34,7 @@ template <class S, int SEGS, bool GATED, int OUT> int rows_grid(RowsArgs& a, hip
   // (experts: 2 chunks a group, 1 to 3 % better than 4)
   return grid_launch(units, (a.P + cols - 1) / cols, a.offsets ? 2 : 4, [&](const Grid& g, unsigned blocks) {
     a.grid = g;
-    rows_kernel<S, SEGS, GATED, OUT><<<blocks, S::NT, S::kLds, s>>>(a);
+    rows_kernel<S, SEGS, GATED, OUT><<<blocks, S::NT, kBlockLds<S, OUT>, s>>>(a);
     MOE_HIP(hipGetLastError());
     return (int)MOE_OK;
   });

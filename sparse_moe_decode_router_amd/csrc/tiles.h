@@ -87,6 +87,7 @@ struct Operand {
 };
 
 constexpr uint32_t kNowhere = 0x80000000u;      // past the end of any buffer here
+constexpr int kMaxLds = 160 << 10;              // of a block
 
 // R rows of q by BK k of 16 bits: 2 R BK bytes, KC: [R][BK], else [BK][R].
 // PAIR (KC): rows come from two matrices in turns of 32 (32 of the first, the
@@ -268,7 +269,7 @@ struct Shape {
   typedef Tile<QK, BQ, BK, NT, false> QT;
   typedef Tile<PK, BP, BK, NT, PAIR> PT;
   static constexpr int kStage = QT::kBytes + PT::kBytes;
-  static constexpr int kLds = NS * kStage;
+  static constexpr int kStages = NS * kStage;
 };
 
 // acc[q][p] += the products of one step of k, for the first LIVE of the wave's
@@ -398,6 +399,15 @@ __device__ __forceinline__ void tile_product(const Operand& q, const Operand& p,
   tile_loop<S, SEGS, 0>(q, p, lds, acc);
 }
 
+// LDS of a wave that turns 32 rows of 32 NP columns (store_rows), each padded by
+// a piece.
+template <int OUT, int NP> constexpr int kTurn = 32 * (32 * NP * (int)sizeof(typename El<OUT>::raw) + 16);
+// LDS of a block: its stages, then in their place the turns of its waves, which
+// may need more (fp32 in tiles of 128 x 128 in half steps: 34 KB, stages 32; three
+// blocks a CU all the same).
+template <class S, int OUT>
+constexpr int kBlockLds = S::kStages > S::NT / 64 * kTurn<OUT, S::TP> ? S::kStages : S::NT / 64 * kTurn<OUT, S::TP>;
+
 // 32 rows of q by 32 NP columns of p, one wave: from the sums' layout (lane:
 // row l % 32, columns 8 (i / 4) + 4 (l / 32) + i % 4 of each 32) through the
 // wave's own LDS to rows in memory, each rounded once to OUT.  out: (row 0,
@@ -408,7 +418,7 @@ template <int OUT, int NP, bool AL>
 __device__ __forceinline__ void store_rows(uint8_t* lds, const f32x16_t* v, void* out, long ld, int rows, int cols) {
   typedef typename El<OUT>::raw raw;
   constexpr int kN = El<OUT>::kN;               // elements of a piece
-  constexpr int kPitch = 32 * NP * (int)sizeof(raw) + 16;
+  constexpr int kPitch = kTurn<OUT, NP> / 32;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int t = 0; t < NP; ++t)
@@ -570,6 +580,8 @@ template <class S, int SEGS, bool GATED, int OUT>
 __global__ __launch_bounds__(S::NT, S::WAVES) void rows_kernel(RowsArgs a) {
   extern __shared__ uint8_t tile_lds[];
   static_assert(!GATED || (S::PAIR && S::TP % 2 == 0), "tiles of both matrices in a wave");
+  static_assert(S::NT / 64 * kTurn<OUT, S::TP> <= kBlockLds<S, OUT> && kBlockLds<S, OUT> <= kMaxLds, "turns in LDS");
+  static_assert(!GATED || kTurn<MOE_TYPE_F32, S::TP / 2> <= kTurn<OUT, S::TP>, "saved products turned in the same place");
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
   int unit, tile;
   if (!grid_place(a.grid, &unit, &tile)) return;
@@ -606,7 +618,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void rows_kernel(RowsArgs a) {
   const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
   f32x16_t acc[S::TQ][S::TP] = {};
   tile_product<S, SEGS>(q, p, tile_lds, live, acc);
-  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+  uint8_t* mine = tile_lds + wave * kTurn<OUT, S::TP>;
 #pragma unroll
   for (int t = 0; t < S::TQ; ++t) {
     if (t >= live) continue;
@@ -692,6 +704,7 @@ template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs&
 template <class S, int OUT>
 __global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
   extern __shared__ uint8_t tile_lds[];
+  static_assert(S::NT / 64 * kTurn<OUT, S::TP> <= kBlockLds<S, OUT> && kBlockLds<S, OUT> <= kMaxLds, "turns in LDS");
   constexpr int kSize = El<OUT>::kN == 4 ? 4 : 2;
   int unit, tile;
   if (!grid_place(a.grid, &unit, &tile)) return;
@@ -703,7 +716,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void mats_kernel(MatsArgs a) {
   const int live = left <= 0 ? 0 : left >= 32 * S::TQ ? S::TQ : (left + 31) / 32;
   f32x16_t acc[S::TQ][S::TP] = {};
   tile_product<S, 1>(m.q, m.p, tile_lds, live, acc);
-  uint8_t* mine = tile_lds + wave * (32 * (32 * S::TP * kSize + 16));
+  uint8_t* mine = tile_lds + wave * kTurn<OUT, S::TP>;
 #pragma unroll
   for (int t = 0; t < S::TQ; ++t) {
     if (t >= live) continue;
