@@ -611,9 +611,12 @@ int moe_router_topk_backward(const uint16_t* x_dev, int32_t T, int32_t d,
  * all N rows.  Otherwise rows in expert order (moe_sort_tokens): expert e's
  * matrix, at w_dev + e * w_stride_bytes, for rows offsets[e] .. offsets[e+1]-1;
  * rows outside the buckets keep what the output held, and what the inputs hold
- * there is not used.  E <= 1024.  Sizes from 1 to 2^20, N up to 2^30
- * (MOE_ERR_UNSUPPORTED beyond), any alignment of the element; rows of whole 16-byte pieces at 16-byte addresses (sizes that are
- * multiples of 8) are faster.  Products exact, sums in fp32 in an order that
+ * there is not used.  A border below 0 or past N is taken as 0 or N, in every
+ * output alike; borders have to ascend (rows of two buckets, and those behind a
+ * border that falls, are not defined; no row outside the N is touched).
+ * E <= 1024.  Sizes from 1 to 2^20, N up to 2^30 (MOE_ERR_UNSUPPORTED beyond),
+ * any alignment of the element; rows of whole 16-byte pieces at 16-byte
+ * addresses (sizes that are multiples of 8) are faster.  Products exact, sums in fp32 in an order that
  * depends on the sizes alone, each output rounded once: y and dx to `type` or
  * (y) to fp32, gradients of matrices to dw_type, `type` or MOE_TYPE_F32.  A row
  * that is not finite touches no row of another, and only its own expert's

@@ -14,10 +14,14 @@ struct RowChunk {
   int n;        // rows (0..size)
 };
 
+// A border outside 0 .. N is taken as the nearer of the two, wherever borders
+// are read.
+__device__ __forceinline__ int row_border(int at, long N) { return at < 0 ? 0 : at > N ? (int)N : at; }
+
 // Chunk j.  Every wave finds its own: borders and slots of all experts in
 // coalesced loads, all in flight at once (lane l holds experts l, l + 64, ..),
-// chunks counted by wave scans of 64 experts.  Offsets that do not describe N
-// rows give no row outside them.
+// chunks counted by wave scans of 64 experts.  Where borders fall, the chunk's
+// rows are some within N.
 __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offsets,
                                                const int32_t* __restrict__ slot_table, int E, long N, long j,
                                                int size) {
@@ -30,7 +34,7 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
     if (u < kU) slots[u] = 64 * u + lane;
     if (64 * u <= E) {
       const int e = 64 * u + lane;
-      off[u] = offsets[e < E ? e : E];
+      off[u] = row_border(offsets[e < E ? e : E], N);
       if (u < kU && slot_table) slots[u] = slot_table[e < E ? e : E - 1];
     }
   }

@@ -674,11 +674,9 @@ template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs&
   const int second = qt >= a.q_tiles ? 1 : 0;
   long start = 0, end = a.N;
   if (a.offsets) {
-    start = a.offsets[e];
-    end = a.offsets[e + 1];
-    start = start < 0 ? 0 : start;
-    end = end > a.N ? a.N : end;
-    if (end < start) start = end = 0;
+    start = row_border(a.offsets[e], a.N);
+    end = row_border(a.offsets[e + 1], a.N);
+    if (end < start) end = start;
   }
   MatsTile m{};
   m.q0 = (qt - second * a.q_tiles) * S::BQ;
