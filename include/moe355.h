@@ -686,7 +686,8 @@ int moe_quantize_fp8(const void* x_dev, int32_t type, int32_t count,
  * ceil(n_out / 128) * ceil(n_in / 128) apart or w_scales_stride (in floats).
  * A block's products are summed before they are scaled: 8 consecutive ones at
  * once by the matrix core, which drops of each what is below 2^-13 of the
- * largest's power of two, then in fp32.  y_type any. */
+ * largest's power of two, then in fp32; by the one scale and then by the other,
+ * whose product may leave fp32's range.  y_type any. */
 int moe_linear_fp8(const void* w_dev, size_t w_stride_bytes,
                    const float* w_scales_dev, size_t w_scales_stride,
                    int32_t E, const void* x_dev, const float* x_scales_dev,

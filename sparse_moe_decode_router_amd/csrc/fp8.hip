@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kBlock = 128;
 constexpr float kMax = 448.f, kSmallest = 0x1p-96f, kLarge = 0x1p64f;
+constexpr int kNormal = 0x108;                  // v_cmp_class: normal numbers of either sign
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // ------------------------------------------------------------ quantisation
@@ -202,6 +203,16 @@ struct Fp8Args {
 // 128: by HBM (370 MB) and half-filled chunks.
 template <int WQ_, int WP_, int TQ_, int TP_, int NS_> struct Fp8Shape {
   static constexpr int WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, NS = NS_;
+  // Scales are 2^-105 and larger, so that the product of two may leave fp32's range
+  // while y does not (x and W of 2^-70), whereas a step's sum times one scale stays
+  // above 2^-123 (nonzero products of codes are 2^-18 and larger).  With one tile a
+  // wave each sum is scaled by the one and then by the other; with more, where 16
+  // products a tile count, the scales are multiplied first and steps whose product
+  // is no normal number come after the loop (us, one after the other and this: 300
+  // x 4096 -> 4096, 64 x 64, 21.1 and 23.4; 500 x 4096 -> 16384, 128 x 128, 46.5 and
+  // 43.0; 4096 x 4096 -> 16384, 256 x 256, 373 and 353, with the range left open 347;
+  // where every step is such a one 2570, where sizes are filled up with zeros 360).
+  static constexpr bool TWICE = TQ_ * TP_ == 1;
   static constexpr int NT = 64 * WQ * WP, BQ = 32 * WQ * TQ, BP = 32 * WP * TP;
   typedef Tile<true, BQ, 64, NT, false> QT;
   typedef Tile<true, BP, 64, NT, false> PT;
@@ -218,9 +229,10 @@ template <class T> __device__ __forceinline__ i32x8_t fp8_frag(const uint8_t* t,
 // The K loop, for the first LIVE of the wave's tiles of x (a constant, as in
 // tiles.h).  A row tile's fragments are read while the products of the one
 // before run; each pair of products is folded into its sums meanwhile.
+// Steps that are left out (S::TWICE) lie from `first` to `last`.
 template <class S, int LIVE>
 __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uint8_t* lds, int blocks, const float* const (&sx)[S::TQ],
-                                         const float* const (&sw)[S::TP], f32x16_t (&acc)[S::TQ][S::TP]) {
+                                         const float* const (&sw)[S::TP], f32x16_t (&acc)[S::TQ][S::TP], int& first, int& last) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wq = wave / S::WP, wp = wave % S::WP;
   typename S::QT qt;
@@ -239,6 +251,7 @@ __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uin
   uint32_t now = 0, fill = (S::NS - 1) * S::kStage;             // stages, as bytes
   const auto after = [](uint32_t st) { return st == (S::NS - 1) * S::kStage ? 0 : st + S::kStage; };
   for (int s = 0; s < blocks; ++s) {
+    bool all = true;
     float fx[LIVE + 1], fw[S::TP];
 #pragma unroll
     for (int t = 0; t < LIVE; ++t) fx[t] = sx[t][s];
@@ -268,12 +281,59 @@ __device__ __forceinline__ void fp8_loop(const Operand& q, const Operand& p, uin
           f32x16_t part{};
           part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][0], qf[u & 1][0], part, 0, 0, 0, 0, 0, 0);
           part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pf[t][1], qf[u & 1][1], part, 0, 0, 0, 0, 0, 0);
-          const float f = fx[u] * fw[t];
+          if constexpr (S::TWICE) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[u][t][i] = fmaf(fx[u] * part[i], fw[t], acc[u][t][i]);
+            continue;
+          }
+          const float both = fx[u] * fw[t];
+          const bool normal = __builtin_amdgcn_classf(both, kNormal);
+          const float f = normal ? both : 0.f;
+          all &= normal;
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[u][t][i] = fmaf(f, part[i], acc[u][t][i]);
         }
       }
     }
+    if (!S::TWICE && __ballot(!all) != 0) {
+      first = s < first ? s : first;
+      last = s;
+    }
+  }
+}
+
+// Inputs k .. k + 31 of a row of n in memory, zeros past its end.
+__device__ __forceinline__ i32x8_t fp8_inputs(const uint8_t* row, int k, int n) {
+  i32x8_t v{};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (k + 16 * h < n) {
+      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(row + k + 16 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * h + i] = (int)q[i];
+    }
+  return v;
+}
+// The steps that fp8_loop left out of 32 rows by 32 columns, from first to last:
+// each sum is scaled by one scale and then by the other.  x, w: the lane's rows of
+// the operands.  Straight from memory, and past steps where W is zeros: what is left
+// out is mostly sizes filled up with zeros, whose scales are the smallest.
+__device__ __forceinline__ void fp8_left_out(const uint8_t* x, const uint8_t* w, int n, int first, int last, const float* sx,
+                                             const float* sw, f32x16_t& acc) {
+  for (int s = first; s <= last; ++s) {
+    const float fx = sx[s], fw = sw[s];
+    const bool far = !__builtin_amdgcn_classf(fx * fw, kNormal);
+    const int k = kBlock * s + 32 * ((threadIdx.x & 63) >> 5);
+    const i32x8_t p0 = fp8_inputs(w, k, n), p1 = fp8_inputs(w, k + 64, n);
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= p0[i] | p1[i];
+    if (__ballot(far) == 0 || __ballot((any & 0x7F7F7F7F) != 0 || !__builtin_isfinite(fw)) == 0) continue;
+    f32x16_t part{};
+    part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p0, fp8_inputs(x, k, n), part, 0, 0, 0, 0, 0, 0);
+    part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p1, fp8_inputs(x, k + 64, n), part, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = far ? fmaf(fx * part[i], fw, acc[i]) : acc[i];
   }
 }
 
@@ -320,18 +380,30 @@ __global__ __launch_bounds__(S::NT, 2) void linear_fp8_kernel(Fp8Args a) {
     sw[t] = a.w_scales + (uint64_t)e * a.w_scales_stride + (uint64_t)((o < a.n_out ? o : a.n_out - 1) / kBlock) * a.blocks;
   }
   f32x16_t acc[S::TQ][S::TP] = {};
+  int first = a.blocks, last = -1;
   if (live == S::TQ) {
-    fp8_loop<S, S::TQ>(q, p, tile_lds, a.blocks, sx, sw, acc);
+    fp8_loop<S, S::TQ>(q, p, tile_lds, a.blocks, sx, sw, acc, first, last);
   } else if (S::TQ == 4 && live == 3) {
-    fp8_loop<S, (S::TQ == 4 ? 3 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
+    fp8_loop<S, (S::TQ == 4 ? 3 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc, first, last);
   } else if (S::TQ == 4 && live == 2) {
-    fp8_loop<S, (S::TQ == 4 ? 2 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
+    fp8_loop<S, (S::TQ == 4 ? 2 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc, first, last);
   } else if (S::TQ > 1 && live == 1) {
-    fp8_loop<S, (S::TQ > 1 ? 1 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc);
+    fp8_loop<S, (S::TQ > 1 ? 1 : 0)>(q, p, tile_lds, a.blocks, sx, sw, acc, first, last);
   } else {
-    fp8_loop<S, 0>(q, p, tile_lds, a.blocks, sx, sw, acc);
+    fp8_loop<S, 0>(q, p, tile_lds, a.blocks, sx, sw, acc, first, last);
   }
   stage_wait<0>();
+  if (!S::TWICE && first <= last) {
+#pragma unroll
+    for (int t = 0; t < S::TQ; ++t)
+#pragma unroll
+      for (int u = 0; u < S::TP; ++u) {
+        const int r = 32 * (wq * S::TQ + t) + (lane & 31), o = p0 + 32 * (wp * S::TP + u) + (lane & 31);
+        fp8_left_out(a.x + (start + (r < n ? r : n - 1)) * a.n_in,
+                     a.w + (uint64_t)e * a.w_stride + (uint64_t)(o < a.n_out ? o : a.n_out - 1) * a.n_in, a.n_in, first, last,
+                     sx[t], sw[u], acc[t][u]);
+      }
+  }
   uint8_t* mine = tile_lds + wave * kTurn<OUT, S::TP>;
 #pragma unroll
   for (int t = 0; t < S::TQ; ++t) {
@@ -407,9 +479,9 @@ __global__ __launch_bounds__(64 * NW) void stream_fp8_kernel(Fp8Args a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const f32x4_t part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(wv[u][r]), join(xv[u][t]), (f32x4_t){}, 0, 0, 0, 0, 0, 0);
-        const float f = fw[u][r] * fx[u][t];
+        // (one scale after the other, as Fp8Shape says; here memory bounds)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(f, part[i], acc[r][t][i]);
+        for (int i = 0; i < 4; ++i) acc[r][t][i] = fmaf(fx[u][t] * part[i], fw[u][r], acc[r][t][i]);
       }
   };
   const int count = wave < a.blocks ? (a.blocks - wave + NW - 1) / NW : 0;
