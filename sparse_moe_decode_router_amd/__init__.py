@@ -944,7 +944,8 @@ def moe_linear(w, x, offsets=None, out=None, stream=None):
 def moe_linear_backward(dy, w, x, offsets=None, out=None, stream=None):
     """Gradients of moe_linear from dy [N, n_out]: (dx [N, n_in], dw like w).
     out: that pair to write into, None for one not wanted; dw of x's type or
-    float32, written whole (zeros for an expert without rows)."""
+    float32, written whole (zeros for an expert without rows).  Without dx w may
+    be None, without dw x."""
     if stream is not None:
         with _stream_of(dy, stream):
             return moe_linear_backward(dy, w, x, offsets, out)
@@ -990,7 +991,8 @@ def moe_gated_backward(dh, pre, w_gate, w_up, x, offsets=None, act: str = "silu"
     """Gradients of moe_gated from dh [N, I] and what it saved: (dx [N, d],
     dw_gate, dw_up like the matrices).  out: that triple to write into, None for
     dx, or for both gradients of matrices, where not wanted; those of x's type
-    or float32, written whole."""
+    or float32, written whole.  Without dx w_gate and w_up may be None, without
+    the gradients of matrices x."""
     if stream is not None:
         with _stream_of(dh, stream):
             return moe_gated_backward(dh, pre, w_gate, w_up, x, offsets, act, workspace, out)

@@ -356,16 +356,25 @@ Matrices matrices(PyObject* o, const char* name, at::ScalarType type, bool exper
   }
   return m;
 }
-// The same for an output or a second input of w's sizes; None passes as null.
+// m has the sizes of w.
+void same(const Matrices& m, const char* name, const Matrices& w) {
+  if (m.E == w.E && m.n_out == w.n_out && m.n_in == w.n_in) return;
+  PyErr_Format(PyExc_ValueError, "%s: %d matrices of %lld x %lld wanted, got %d of %lld x %lld", name, w.E, (long long)w.n_out,
+               (long long)w.n_in, m.E, (long long)m.n_out, (long long)m.n_in);
+  throw PyError{};
+}
+// Matrices of those sizes: an output or a second input; None passes as null.
 Matrices like(PyObject* o, const char* name, at::ScalarType type, bool experts, int dev, int E, int64_t n_out, int64_t n_in) {
   if (o == Py_None) return Matrices{nullptr, E, n_out, n_in, 0};
   const Matrices m = matrices(o, name, type, experts, dev);
-  if (m.E != E || m.n_out != n_out || m.n_in != n_in) {
-    PyErr_Format(PyExc_ValueError, "%s: %d matrices of %lld x %lld wanted, got %d of %lld x %lld", name, E, (long long)n_out,
-                 (long long)n_in, m.E, (long long)m.n_out, (long long)m.n_in);
-    throw PyError{};
-  }
+  same(m, name, Matrices{nullptr, E, n_out, n_in, 0});
   return m;
+}
+// Matrices that a call uses for an output alone that it does not write (no `use`):
+// may be None, with the sizes of the output that it does.
+Matrices unless_unused(PyObject* o, const char* name, bool use, const Matrices& sizes, at::ScalarType type, bool experts, int dev) {
+  if (o == Py_None && !use) return Matrices{nullptr, sizes.E, sizes.n_out, sizes.n_in, 0};
+  return matrices(o, name, type, experts, dev);
 }
 at::ScalarType type_of(PyObject* o, const char* name) { return tensor(o, name).scalar_type(); }
 int32_t* borders(PyObject* o, int E, int dev) { return may<int32_t>(o, "offsets", kI32, {E + 1}, dev); }
@@ -386,18 +395,21 @@ PyObject* py_product(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// dy, w, x, offsets, dx, dw
+// dy, w, x, offsets, dx, dw (w None without dx, x None without dw)
 PyObject* py_product_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return entry<6>(args, n, [](PyObject* const* a) {
     int dev;
     const at::Tensor& dy = matrix(a[0], "dy", &dev, true);
-    const at::ScalarType t = dy.scalar_type(), td = a[5] != Py_None && type_of(a[5], "dw") == kF32 ? kF32 : t;
-    const bool experts = a[3] != Py_None;
-    const Matrices w = matrices(a[1], "w", t, experts, dev);
+    const bool for_x = a[4] != Py_None, for_w = a[5] != Py_None, experts = a[3] != Py_None;
+    const at::ScalarType t = dy.scalar_type(), td = for_w && type_of(a[5], "dw") == kF32 ? kF32 : t;
+    Matrices dw{};
+    if (for_w) dw = matrices(a[5], "dw", td, experts, dev);
+    const Matrices w = unless_unused(a[1], "w", for_x || !for_w, dw, t, experts, dev);
+    if (for_w) same(dw, "dw", w);
     const int64_t N = dy.size(0);
-    const Matrices dw = like(a[5], "dw", td, experts, dev, w.E, w.n_out, w.n_in);
     const On on(dev);
-    return g.product_grad(need(dy, "dy", t, {N, w.n_out}, dev), w.p, w.stride, w.E, need<void>(a[2], "x", t, {N, w.n_in}, dev),
+    return g.product_grad(need(dy, "dy", t, {N, w.n_out}, dev), w.p, w.stride, w.E,
+                          for_w ? need<void>(a[2], "x", t, {N, w.n_in}, dev) : may<void>(a[2], "x", t, {N, w.n_in}, dev),
                           type_code(t), size32(N, "N"), size32(w.n_in, "n_in"), size32(w.n_out, "n_out"),
                           borders(a[3], w.E, dev), may<void>(a[4], "dx", t, {N, w.n_in}, dev), dw.p, dw.stride,
                           type_code(td), on.stream);
@@ -421,25 +433,30 @@ PyObject* py_gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-// dh, pre, w_gate, w_up, x, offsets, act, dx, dw_gate, dw_up, workspace
+// dh, pre, w_gate, w_up, x, offsets, act, dx, dw_gate, dw_up, workspace (both w
+// None without dx, x None without the gradients of matrices)
 PyObject* py_gated_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return entry<11>(args, n, [](PyObject* const* a) {
     int dev;
     const at::Tensor& dh = matrix(a[0], "dh", &dev, true);
-    const at::ScalarType t = dh.scalar_type(), td = a[8] != Py_None && type_of(a[8], "dw_gate") == kF32 ? kF32 : t;
-    const bool experts = a[5] != Py_None;
-    const Matrices wg = matrices(a[2], "w_gate", t, experts, dev);
-    const Matrices wu = like(a[3], "w_up", t, experts, dev, wg.E, wg.n_out, wg.n_in);
+    const bool for_x = a[7] != Py_None, for_w = a[8] != Py_None, experts = a[5] != Py_None;
+    const at::ScalarType t = dh.scalar_type(), td = for_w && type_of(a[8], "dw_gate") == kF32 ? kF32 : t;
+    Matrices dg{};
+    if (for_w) dg = matrices(a[8], "dw_gate", td, experts, dev);
+    const Matrices wg = unless_unused(a[2], "w_gate", for_x || !for_w, dg, t, experts, dev);
+    if (for_w) same(dg, "dw_gate", wg);
+    const Matrices wu = unless_unused(a[3], "w_up", for_x || !for_w, dg, t, experts, dev);
+    same(wu, "w_up", wg);
     const int64_t N = dh.size(0), I = wg.n_out, d = wg.n_in;
-    const Matrices dg = like(a[8], "dw_gate", td, experts, dev, wg.E, I, d), du = like(a[9], "dw_up", td, experts, dev, wg.E, I, d);
+    const Matrices du = like(a[9], "dw_up", td, experts, dev, wg.E, I, d);
     size_t nws;
     uint8_t* ws = workspace(a[10], dev, &nws);
     const On on(dev);
     return g.gated_grad(need(dh, "dh", t, {N, I}, dev), need<float>(a[1], "pre", kF32, {N, 2 * I}, dev), wg.p, wg.stride, wu.p,
-                        wu.stride, wg.E, need<void>(a[4], "x", t, {N, d}, dev), type_code(t), size32(N, "N"), size32(d, "d"),
-                        size32(I, "I"), borders(a[5], wg.E, dev), number32(a[6], "act"),
-                        may<void>(a[7], "dx", t, {N, d}, dev), dg.p, dg.stride, du.p, du.stride, type_code(td), ws, nws,
-                        on.stream);
+                        wu.stride, wg.E, for_w ? need<void>(a[4], "x", t, {N, d}, dev) : may<void>(a[4], "x", t, {N, d}, dev),
+                        type_code(t), size32(N, "N"), size32(d, "d"), size32(I, "I"), borders(a[5], wg.E, dev),
+                        number32(a[6], "act"), may<void>(a[7], "dx", t, {N, d}, dev), dg.p, dg.stride, du.p, du.stride,
+                        type_code(td), ws, nws, on.stream);
   });
 }
 
