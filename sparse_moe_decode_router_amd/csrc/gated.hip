@@ -10,6 +10,9 @@
 // fp32: dg and du have to be rounded to the rows' type, as operands of the
 // matrix cores, which alone moves dx and dW by as much as their own rounding
 // does; g and u rounded as well moved them by 1.8 instead of 1.4 times that.
+// In fp16 it also has fp16's range (the header says what becomes of dg and du
+// outside it): a scale would have to be one a row for dx and one a column of an
+// expert for dW, from a pass over dh and pre of its own.
 #include "products.h"
 #include "stream.h"
 
