@@ -676,6 +676,8 @@ int moe_gated_backward(const void* dh_dev, const float* pre_dev,
  * fp32 scale for a block of them: 128 inputs of a row of x, 128 x 128 of W.
  * Quantisation: with a the largest |v| of the block (2^-96 where it is smaller),
  *   scale = a / 448,   code = e4m3(448 v / a)   (nearest, ties to even).
+ * 16-bit values: exactly so.  fp32 values, whose 448 v is rounded: a quotient within
+ * 2^-22 (relative) of the middle of two codes may get either.
  * x [count][rows][n] of `type` (fp32, bf16, fp16), codes the same shape,
  * scales [count][ceil(rows / block_rows)][ceil(n / 128)]; block_rows 1 or 128.
  * fp32 values up to 2^100.  A block with a value that is not finite gets codes
