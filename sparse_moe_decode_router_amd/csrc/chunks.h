@@ -16,7 +16,7 @@ struct RowChunk {
 
 // A border outside 0 .. N is taken as the nearer of the two, wherever borders
 // are read.
-__device__ __forceinline__ int row_border(int at, long N) { return at < 0 ? 0 : at > N ? (int)N : at; }
+__device__ __forceinline__ int row_border(int at, int N) { return min(max(at, 0), N); }
 
 // Chunk j.  Every wave finds its own: borders and slots of all experts in
 // coalesced loads, all in flight at once (lane l holds experts l, l + 64, ..),
@@ -34,7 +34,7 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
     if (u < kU) slots[u] = 64 * u + lane;
     if (64 * u <= E) {
       const int e = 64 * u + lane;
-      off[u] = row_border(offsets[e < E ? e : E], N);
+      off[u] = offsets[e < E ? e : E];
       if (u < kU && slot_table) slots[u] = slot_table[e < E ? e : E - 1];
     }
   }
@@ -45,7 +45,9 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
     if (64 * u < E && !r.any) {
       // the next lane's border (lane 63: the first of the next 64)
       const int next = __builtin_amdgcn_update_dpp(__builtin_amdgcn_readlane(off[u + 1], 0), off[u], 0x130, 0xF, 0xF, false);
-      const int rows = 64 * u + 63 < E || lane < E - 64 * u ? next - off[u] : 0;
+      // (not where they are loaded: each load would be waited for before the next, 2.4 us of 7)
+      const int first = row_border(off[u], (int)N), end = row_border(next, (int)N);
+      const int rows = 64 * u + 63 < E || lane < E - 64 * u ? end - first : 0;
       const int c = rows > 0 ? (int)((unsigned)(rows + size - 1) / (unsigned)size) : 0;
       const int incl = wave_scan(c) + before;
       const uint64_t past = __ballot((long)incl > j);
@@ -53,7 +55,7 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
         const int owner = __ffsll((unsigned long long)past) - 1;
         const int skip = ((int)j - __builtin_amdgcn_readlane(incl - c, owner)) * size;
         const int left = __builtin_amdgcn_readlane(rows, owner) - skip;
-        r = RowChunk{true, __builtin_amdgcn_readlane(slots[u], owner), __builtin_amdgcn_readlane(off[u], owner) + skip,
+        r = RowChunk{true, __builtin_amdgcn_readlane(slots[u], owner), __builtin_amdgcn_readlane(first, owner) + skip,
                      left < size ? left : size};
       }
       before = __builtin_amdgcn_readlane(incl, 63);

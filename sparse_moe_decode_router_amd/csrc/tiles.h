@@ -674,8 +674,8 @@ template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs&
   const int second = qt >= a.q_tiles ? 1 : 0;
   long start = 0, end = a.N;
   if (a.offsets) {
-    start = row_border(a.offsets[e], a.N);
-    end = row_border(a.offsets[e + 1], a.N);
+    start = row_border(a.offsets[e], (int)a.N);
+    end = row_border(a.offsets[e + 1], (int)a.N);
     if (end < start) end = start;
   }
   MatsTile m{};
