@@ -45,7 +45,8 @@ __device__ __forceinline__ RowChunk find_chunk(const int32_t* __restrict__ offse
     if (64 * u < E && !r.any) {
       // the next lane's border (lane 63: the first of the next 64)
       const int next = __builtin_amdgcn_update_dpp(__builtin_amdgcn_readlane(off[u + 1], 0), off[u], 0x130, 0xF, 0xF, false);
-      // (not where they are loaded: each load would be waited for before the next, 2.4 us of 7)
+      // (not where they are loaded: each load would be waited for before the next, 9.2 us
+      // in place of 6.8 for ten rows of 512 experts, 512 -> 2048)
       const int first = row_border(off[u], (int)N), end = row_border(next, (int)N);
       const int rows = 64 * u + 63 < E || lane < E - 64 * u ? end - first : 0;
       const int c = rows > 0 ? (int)((unsigned)(rows + size - 1) / (unsigned)size) : 0;

@@ -197,10 +197,11 @@ struct Fp8Args {
 
 // WQ x WP waves of TQ x TP tiles of 32 x 32, 128 inputs a step: a row's 128
 // bytes lie in LDS as 64 elements of 16 bits do in tiles.h.
-// Measured: 4096 rows, 4096 -> 16384 310 us (1770 TFLOP/s) with 256 x 256 a
-// block: by the sums' 16 scaled additions a tile and step beside the products,
-// and each step's barrier; 32768 rows of 256 experts, 2048 -> 512 99 us with 128 x
-// 128: by HBM (370 MB) and half-filled chunks.
+// Measured: 4096 rows, 4096 -> 16384 316 us (1740 TFLOP/s; 374 in the first
+// launches on an idle card) with 256 x 256 a block: by the sums' 16 scaled
+// additions a tile and step beside the products, and each step's barrier; 32768
+// rows of 256 experts, 2048 -> 512 96 us with 128 x 128: by HBM (370 MB) and
+// half-filled chunks.
 template <int WQ_, int WP_, int TQ_, int TP_, int NS_> struct Fp8Shape {
   static constexpr int WQ = WQ_, WP = WP_, TQ = TQ_, TP = TP_, NS = NS_;
   // Scales are 2^-105 and larger, so that the product of two may leave fp32's range
@@ -328,7 +329,8 @@ __device__ __forceinline__ void fp8_left_out(const uint8_t* x, const uint8_t* w,
     int any = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) any |= p0[i] | p1[i];
-    if (__ballot(far) == 0 || __ballot((any & 0x7F7F7F7F) != 0 || !__builtin_isfinite(fw)) == 0) continue;
+    if (__ballot(far) == 0 || __ballot((any & 0x7F7F7F7F) != 0 || !__builtin_isfinite(fw) || !__builtin_isfinite(fx)) == 0)
+      continue;
     f32x16_t part{};
     part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p0, fp8_inputs(x, k, n), part, 0, 0, 0, 0, 0, 0);
     part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(p1, fp8_inputs(x, k + 64, n), part, 0, 0, 0, 0, 0, 0);

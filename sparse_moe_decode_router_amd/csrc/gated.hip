@@ -48,7 +48,7 @@ template <int VN> __device__ __forceinline__ void load_f32(const float* p, float
   }
 }
 // dg | du [N][2 I] from dh [N][I] and pre = g | u [N][2 I], VN elements a
-// thread: bound by HBM (4096 x 8192: 74 us, 6.4 TB/s).
+// thread: bound by HBM (4096 x 8192: 73 us, 6.4 TB/s).
 template <int TYPE, int VN>
 __global__ __launch_bounds__(256) void slope_kernel(const typename El<TYPE>::raw* dh, const float* pre,
                                                     typename El<TYPE>::raw* out, int I, long pieces, int act) {

@@ -17,7 +17,9 @@ template <class S, int OUT> int launch(MatsArgs& a, hipStream_t s) {
 }
 template <int TYPE, int OUT, bool AL> int sized(MatsArgs& a, hipStream_t s) {
   // (us, small and larger tiles: 1024 x 1024 of 1024 rows 10.4 and 17, 2048 x 2048
-  // of 256 rows, 256 tiles, 11.1 and 7.8)
+  // of 256 rows, 256 tiles, 11.1 and 7.8; 128 x 128 and 256 x 256: 256 experts of
+  // 128 rows, 2 x 512 x 2048 388 and 374, 512 x 2048 184 and 175, 4096 rows, 2 x 8192
+  // x 2048 284 and 262, 16 experts of 1024 rows, 1024 x 1024 40 and 37)
   const long tiles = (long)a.E * a.mats * ((a.Q + 127) / 128) * ((a.P + 127) / 128);
   if (tiles <= 128) return launch<Small<TYPE, false, false, false, AL>, OUT>(a, s);
   if constexpr (AL)

@@ -46,7 +46,10 @@ template <class S, int SEGS, bool GATED, int OUT> int rows_grid(RowsArgs& a, hip
 // 21, 64 21.4 and 22.2, 64 x 2048 -> 16384 28 and 42).  Experts: up to 8 rows a
 // bucket; more of them fill a second chunk, for which W is read again (2048 ->
 // 2 x 512 of 512, 5 rows 407 and 454, 10 rows 467 and 459; 2048 -> 2048 of 64, 8
-// rows 115 and 135, 16 rows 172 and 135).
+// rows 115 and 135, 16 rows 172 and 135).  The borders are on the device, so this
+// goes by the average bucket: rows that are all one expert's are streamed too, and
+// its matrix read for each 16 of them (4096 rows of 512 experts, 2048 -> 512: 264 us
+// evenly, 182 in one bucket, 17 as one matrix's).
 inline int few_rows(int E, long N) {
   if (E) return N <= 8l * E ? 1 : 0;
   return N > 64 ? 0 : N > 32 ? 4 : N > 16 ? 2 : 1;

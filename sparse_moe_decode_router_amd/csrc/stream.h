@@ -3,12 +3,12 @@
 // once by the one block that owns it, K shared by the waves of the block so
 // that all of a block's loads are in flight together.  (rows_kernel's tiles
 // would leave most CUs idle: 10 rows of 10 experts, 2048 -> 2 x 512, are 80
-// tiles, 22.7 us; here 320 blocks, 12.6.)
+// tiles, 22.7 us; here 320 blocks, 12.1.)
 //
 // Bound by HBM where the matrices are many or large (64 tokens of 8 of 256
 // experts, 2048 -> 2 x 512: 162 us, 5.8 TB/s; in e4m3 1 row, 2048 -> 100003:
-// 35.7 us, 5.7 TB/s), by the launch and two dependent loads (borders, then rows
-// and matrices) where they are few (10 rows of 10 experts, 512 -> 2048: 6.8 us
+// 34.3 us, 6.0 TB/s), by the launch and two dependent loads (borders, then rows
+// and matrices) where they are few (10 rows of 10 experts, 512 -> 2048: 6.9 us
 // for 21 MB).
 #pragma once
 

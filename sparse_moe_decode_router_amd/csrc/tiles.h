@@ -499,7 +499,8 @@ template <class F> int grid_launch(long units, long tiles, int group, F launch) 
 // products), so steps are twice as long where the columns of P are turned (256 x
 // 4096 dx 51 -> 35 us; forward 22 -> 28, which keeps five stages).
 // Mats (gradients of matrices, few steps of k a tile): 128 x 128 in half steps,
-// three blocks a CU (32768 tiles of 2 steps: 400 us, 470 as Large).
+// three blocks a CU (dW of 32768 rows of 256 experts, 2 x 512 x 2048: 388 us, 424
+// as Large; 512 x 2048 184 and 213).
 template <int TYPE, bool QK, bool PK, bool PAIR, bool AL>
 using Large = Shape<TYPE, QK, PK, 2, 2, 2, 2, 64, 2, PAIR, AL, 2>;
 template <int TYPE, bool QK, bool PK, bool PAIR>
@@ -569,12 +570,12 @@ __device__ __forceinline__ float act_slope(int act, float g, float* value) {
 
 // A block: a chunk of rows by a tile of columns.  GATED: out = act(x p^T)
 // (x p2^T), and both products before it to pre.
-// Measured: 4096 rows, 2048 -> 2 x 8192 with pre 293 us (940 TFLOP/s, a library
-// product of 8192 reaches 1455), its dx 383 (717: 512 tiles of 128 x 128 in one
-// round, 128 of 256 x 256 would fill half the CUs); 8192 x 8192 -> 8192 888 us
-// (1239).  Bound by the matrix cores waiting for each step's barrier and first
-// fragments.  32768 rows of 256 experts, 2048 -> 2 x 512 with pre 296 us, dx 316
-// (4.7 and 4.0 TB/s of what they have to move): by HBM, and by buckets that fill
+// Measured: 4096 rows, 2048 -> 2 x 8192 with pre 287 us (960 TFLOP/s, a library
+// product of 8192 reaches 1455), its dx 363 (757: 512 tiles of 128 x 128 in one
+// round, 128 of 256 x 256 would fill half the CUs); 8192 x 8192 -> 8192 886 us
+// (1240), with fp32 y 902.  Bound by the matrix cores waiting for each step's barrier and first
+// fragments.  32768 rows of 256 experts, 2048 -> 2 x 512 with pre 281 us, dx 298
+// (4.9 and 4.3 TB/s of what they have to move): by HBM, and by buckets that fill
 // three quarters of their chunks.
 template <class S, int SEGS, bool GATED, int OUT>
 __global__ __launch_bounds__(S::NT, S::WAVES) void rows_kernel(RowsArgs a) {
@@ -694,9 +695,9 @@ template <class S> __device__ __forceinline__ MatsTile mats_tile(const MatsArgs&
   return m;
 }
 // A block: a tile of one expert's matrix, k over the expert's rows.
-// Measured: 32768 rows of 256 experts, 2 x 512 x 2048 405 us.  Writing the 1.07
-// GB alone takes 172 (no rows), the products of 128 rows alone about 130 at the
-// dense rate (4096 rows, 2 x 8192 x 2048: 279 us, 990 TFLOP/s); the two overlap
+// Measured: 32768 rows of 256 experts, 2 x 512 x 2048 379 us (in fp32 500).
+// Writing the 1.07 GB alone takes 172 (no rows), the products of 128 rows alone
+// about 130 at the dense rate (4096 rows, 2 x 8192 x 2048: 257 us, 1070 TFLOP/s); the two overlap
 // little, since a tile's loads, few steps and stores follow one another, at four
 // blocks a CU as at one.
 template <class S, int OUT>

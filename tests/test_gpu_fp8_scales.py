@@ -96,3 +96,21 @@ def test_a_scale_of_zero_and_one_that_is_not_finite():
         y = moe.moe_linear_fp8(wc, ws, xc, xs)
         first = (n_out - 1) // 128 * 128
         assert not torch.isfinite(y[:, first:]).any() and torch.equal(y[:, :first], base[:, :first])
+
+
+@pytest.mark.parametrize("v", [float("inf"), float("nan")])
+def test_a_scale_that_is_not_finite_beside_zeros(v):
+    """A scale of x that is not finite where W is zeros, and the other way round: inf times 0 is no number."""
+    for N, n_in, n_out in DENSE:
+        x, w, _ = _inputs(N, n_in, n_out, 0)
+        w[:, :128] = 0
+        (wc, ws), (xc, xs) = moe.moe_quantize_fp8(w, 128), moe.moe_quantize_fp8(x)
+        base = moe.moe_linear_fp8(wc, ws, xc, xs)
+        xs[0, 0] = v
+        y = moe.moe_linear_fp8(wc, ws, xc, xs)
+        assert torch.isnan(y[0]).all() and torch.equal(y[1:], base[1:]), (N, n_in, n_out)
+        x[:, :128], w[:, :128] = 0, 1
+        (wc, ws), (xc, xs) = moe.moe_quantize_fp8(w, 128), moe.moe_quantize_fp8(x)
+        ws[0, 0] = v
+        y = moe.moe_linear_fp8(wc, ws, xc, xs)
+        assert torch.isnan(y[:, :128]).all() and torch.isfinite(y[:, 128:]).all(), (N, n_in, n_out)
