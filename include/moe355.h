@@ -654,7 +654,8 @@ int moe_gated(const void* w_gate_dev, size_t gate_stride_bytes,
 /* From dh [N][I] and the saved pre: dg = dh u act'(g) and du = dh act(g)
  * (rounded to `type` in the workspace), dx = dg Wg + du Wu, dWg = dg^T x,
  * dWu = du^T x; dx, or both gradients of matrices, may be NULL.  The rounding is
- * that of operands of the matrix cores; in fp16 it has their range too: a dg or
+ * that of operands of the matrix cores, and moves dx and dW about as much as their
+ * own rounding to `type` does; in fp16 it has their range too: a dg or
  * du of 65520 and more becomes infinite, and with it its row of dx and its row of
  * its expert's dWg or dWu, one of 2^-25 and less becomes zero, whether or not the
  * sums would fit (training in fp16 scales the loss, and so dh).  bf16 has the
